@@ -32,7 +32,8 @@ EXPORTED = ("csa_compress", "hca_compress", "csa_quantize_kv", "csa_quantize_fp4
             "csa_window_append", "csa_compress_append", "csa_topk_merge", "indexer_topk_paged", "hybrid_attn_decode_paged",
             "indexer_topk_workspace_size", "indexer_topk", "hybrid_attn_prefill",
             "hybrid_attn_decode_workspace_size", "hybrid_attn_decode", "csa_device_error",
-            "csa_status_string", "csa_abi_version", "csa_last_path", "csa_set_wait_limit_ns")
+            "latent_append", "latent_gather", "latent_attn_decode_workspace_size", "latent_attn_decode",
+            "latent_attn_prefill", "csa_status_string", "csa_abi_version", "csa_last_path", "csa_set_wait_limit_ns")
 
 
 class CsaError(RuntimeError):
@@ -85,6 +86,12 @@ def _load():
         "indexer_topk_static": ([vp, vp, vp, i32, vp, vp, i64, i64, i32, i32, i32, i32, i64, vp, vp, vp],
                                 ctypes.c_int),
         "csa_decode_glue": ([vp, vp, vp, i64, i32, i32, vp, P_f4, vp], ctypes.c_int),
+        "latent_append": ([vp, i32, i64, vp, f32, ctypes.c_double, vp, vp, i64, vp, i32, i32, vp, P_kv, vp], ctypes.c_int),
+        "latent_gather": ([P_kv, vp, vp, i64, vp, i32, i32, vp, i64, vp, vp, i32, vp], ctypes.c_int),
+        "latent_attn_decode_workspace_size": ([i64, i32, i32, i32, i64], sz),
+        "latent_attn_decode": ([vp, P_kv, vp, vp, i32, i32, vp, f32, i64, i32, i32, i64, vp, vp, vp, sz, vp], ctypes.c_int),
+        "latent_attn_prefill": ([vp, vp, vp, vp, vp, i64, i64, i64, i32, i32, i32, i32, i64, f32, i32, i32, vp, vp, vp],
+                                ctypes.c_int),
         "csa_device_error": ([vp, ctypes.POINTER(i32)], ctypes.c_int),
         "csa_status_string": ([i32], ctypes.c_char_p),
         "csa_abi_version": ([], i32),
@@ -435,6 +442,170 @@ def csa_decode_glue(o, P, Rm=None, q_next=None, qI: Fp4Rows | None = None, strea
     return q_next, qI
 
 
+# ----------------------------------------------------------------------------------------
+# latent attention (one latent row per token; see include/csa.h for the formulas and limits)
+# ----------------------------------------------------------------------------------------
+
+def _operand(name: str, t, dtypes, shape, device=None, optional: bool = False):
+    """Refuse an operand that the C call would misread: it is handed over as a bare pointer, so its
+    dtype, shape and packing are checked here.  None in `shape` = any extent."""
+    if t is None:
+        if optional:
+            return
+        raise ValueError(f"{name} is missing")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: unsupported dtype {t.dtype}")
+    if t.dim() != len(shape) or any(e is not None and t.shape[i] != e for i, e in enumerate(shape)):
+        raise ValueError(f"{name}: shape {tuple(t.shape)} does not match {shape}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
+def _kv_operand(name: str, rows: KvRows, device):
+    n, dev = rows.n, device
+    _operand(name + ".fp8", rows.fp8, (torch.uint8,), (n, None), dev)
+    _operand(name + ".rope", rows.rope, (torch.bfloat16,), (n, None), dev)
+    _operand(name + ".scale", rows.scale, (torch.float32,), (n,), dev)
+
+
+def _row_map(pages, page_rows, off, device):
+    """The page table or offsets of a latent cache, checked: (B, pages, max_pages, page_rows, off)."""
+    if (pages is None) == (off is None):
+        raise ValueError("give either pages or off")
+    if pages is not None:
+        _operand("pages", pages, (torch.int32,), (None, None), device)
+        return pages.shape[0], _ptr(pages), pages.shape[1], int(page_rows), None
+    _operand("off", off, (torch.int64,), (None,), device)
+    return off.shape[0], None, 0, 0, _ptr(off)
+
+
+class _current:
+    """Makes the operands' device current for a call (the library launches on the current one)."""
+
+    def __init__(self, device):
+        self.guard = None
+        if device.type != "cuda":
+            raise ValueError(f"the operands are on {device}: they have to be on a GPU")
+        if device.index is not None and device.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *e):
+        if self.guard is not None:
+            self.guard.__exit__(*e)
+
+
+def latent_append(x, pos, out: KvRows, g=None, eps: float = 1e-6, base: float = 0.0, seq=None, pages=None,
+                  page_rows: int = 0, off=None, stream=None):
+    """Write the rows x [n, R + rd] (fp32/bf16) into the latent cache ``out`` at position pos[i] of
+    sequence seq[i] (None: of sequence i): RMSNorm of the latent part (when g is given), rotation of
+    the rest by pos (when base is not 0), quantise on write."""
+    dev = x.device
+    _operand("x", x, (torch.float32, torch.bfloat16), (None, out.c))
+    n = x.shape[0]
+    _operand("pos", pos, (torch.int64,), (n,), dev)
+    _operand("seq", seq, (torch.int32,), (n,), dev, optional=True)
+    _operand("g", g, (torch.float32,), (out.c - out.rope_dims,), dev, optional=True)
+    _kv_operand("out", out, dev)
+    B, p, mp, pr, of = _row_map(pages, page_rows, off, dev)
+    with _current(dev):
+        st = _lib.latent_append(_ptr(x), _dtype_code(x), n, _ptr(g), float(eps), float(base), _ptr(pos), _ptr(seq), B, p, mp,
+                                pr, of, ctypes.byref(out._c()), _stream(stream))
+    _check("latent_append", st)
+    return out
+
+
+def latent_gather(rows: KvRows, cu, n: int | None = None, start=None, pages=None, page_rows: int = 0, off=None, lat=None,
+                  rope=None, dtype=torch.bfloat16, stream=None):
+    """Positions start[b] .. start[b] + cu[b+1] - cu[b] - 1 of every sequence, dequantised and packed at
+    rows cu[b] ..; returns (lat [n, R], rope [n, rd]).  With lat and rope None both are allocated with n
+    rows of ``dtype``; with one of them given only that one is written."""
+    dev = rows.fp8.device
+    _kv_operand("rows", rows, dev)
+    B, p, mp, pr, of = _row_map(pages, page_rows, off, dev)
+    _operand("cu", cu, (torch.int64,), (B + 1,), dev)
+    _operand("start", start, (torch.int64,), (B,), dev, optional=True)
+    R, rd = rows.c - rows.rope_dims, rows.rope_dims
+    if lat is None and rope is None:
+        if n is None:
+            raise ValueError("n (output rows) is needed without lat and rope")
+        lat = torch.empty((n, R), dtype=dtype, device=dev)
+        rope = torch.empty((n, rd), dtype=dtype, device=dev)
+    n = (lat if lat is not None else rope).shape[0]
+    dt = (lat if lat is not None else rope).dtype
+    _operand("lat", lat, (torch.float32, torch.bfloat16), (n, R), dev, optional=True)
+    _operand("rope", rope, (dt,), (n, rd), dev, optional=True)
+    with _current(dev):
+        st = _lib.latent_gather(ctypes.byref(rows._c()), _ptr(cu), _ptr(start), B, p, mp, pr, of, n, _ptr(lat), _ptr(rope),
+                                CSA_F32 if dt == torch.float32 else CSA_BF16, _stream(stream))
+    _check("latent_gather", st)
+    return lat, rope
+
+
+def latent_attn_decode_workspace_size(B: int, Lq: int, H: int, R: int, max_len: int) -> int:
+    return int(_lib.latent_attn_decode_workspace_size(B, Lq, H, R, max_len))
+
+
+def latent_attn_decode(q, rows: KvRows, pos, scale: float, max_len: int, pages=None, page_rows: int = 0, off=None, o=None,
+                       lse=None, workspace=None, stream=None):
+    """Absorbed latent attention of Lq new tokens per sequence, q [B, Lq, H, R + rd] bf16, over the latent
+    cache; token j sits at pos[b] + j and sees every position up to its own.  Returns o [B, Lq, H, R]."""
+    dev = q.device
+    _operand("q", q, (torch.bfloat16,), (None, None, None, rows.c))
+    B, Lq, H, _ = q.shape
+    R = rows.c - rows.rope_dims
+    _kv_operand("rows", rows, dev)
+    _operand("pos", pos, (torch.int64,), (B,), dev)
+    nb, p, mp, pr, of = _row_map(pages, page_rows, off, dev)
+    if nb != B:
+        raise ValueError(f"{B} sequences, but a row map of {nb}")
+    if o is None:
+        o = torch.empty((B, Lq, H, R), dtype=torch.bfloat16, device=dev)
+    _operand("o", o, (torch.bfloat16,), (B, Lq, H, R), dev)
+    _operand("lse", lse, (torch.float32,), (B, Lq, H), dev, optional=True)
+    with _current(dev):
+        if workspace is None:
+            workspace = torch.empty((latent_attn_decode_workspace_size(B, Lq, H, R, max_len),), dtype=torch.uint8, device=dev)
+        _operand("workspace", workspace, (torch.uint8,), (None,), dev)
+        st = _lib.latent_attn_decode(_ptr(q), ctypes.byref(rows._c()), _ptr(pos), p, mp, pr, of, float(scale), B, Lq, H,
+                                     int(max_len), _ptr(o), _ptr(lse), _ptr(workspace), workspace.numel(), _stream(stream))
+    _check("latent_attn_decode", st)
+    return o
+
+
+def latent_attn_prefill(q, kv, k_rope, cu_q, cu_k, max_q: int, scale: float, causal: bool = True, o=None, lse=None,
+                        stream=None):
+    """Expanded latent attention over packed sequences: q [Tq, H, dn + dr], kv [Tk, H, dn + dv] (a head's
+    unrotated key, then its value), k_rope [Tk, dr] shared by the heads.  Returns o [Tq, H, dv]."""
+    dev, dt = q.device, q.dtype
+    _operand("q", q, (torch.float32, torch.bfloat16), (None, None, None))
+    Tq, H, dk = q.shape
+    _operand("kv", kv, (dt,), (None, H, None), dev)
+    Tk = kv.shape[0]
+    _operand("k_rope", k_rope, (dt,), (Tk, None), dev)
+    dr = k_rope.shape[1]
+    dn = dk - dr
+    dv = kv.shape[2] - dn
+    _operand("cu_q", cu_q, (torch.int64,), (None,), dev)
+    B = cu_q.shape[0] - 1
+    _operand("cu_k", cu_k, (torch.int64,), (B + 1,), dev)
+    if o is None:
+        o = torch.empty((Tq, H, dv), dtype=dt, device=dev) if dv > 0 else None
+    _operand("o", o, (dt,), (Tq, H, dv), dev)
+    _operand("lse", lse, (torch.float32,), (Tq, H), dev, optional=True)
+    with _current(dev):
+        st = _lib.latent_attn_prefill(_ptr(q), _ptr(kv), _ptr(k_rope), _ptr(cu_q), _ptr(cu_k), B, Tq, Tk, H, dn, dr, dv,
+                                      int(max_q), float(scale), 1 if causal else 0, _dtype_code(q), _ptr(o), _ptr(lse),
+                                      _stream(stream))
+    _check("latent_attn_prefill", st)
+    return o
+
+
 def csa_device_error(stream=None) -> int:
     v = ctypes.c_int32(0)
     _check("csa_device_error", _lib.csa_device_error(_stream(stream), ctypes.byref(v)))
@@ -455,6 +626,8 @@ CSA_PATH_PREFILL_GENERIC = 5
 CSA_PATH_DECODE_TC = 6
 CSA_PATH_DECODE_GENERIC = 7
 CSA_PATH_PREFILL_KEYS_TC = 8
+CSA_PATH_LATENT_DECODE_GENERIC = 9
+CSA_PATH_LATENT_PREFILL_GENERIC = 10
 
 
 def csa_set_wait_limit_ns(ns: int) -> int:

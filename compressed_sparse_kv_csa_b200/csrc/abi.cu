@@ -6,6 +6,7 @@
 #include <cstring>
 
 #include "common.cuh"
+#include "latent.cuh"
 
 namespace csa {
 __device__ int g_dev_error = 0;
@@ -524,6 +525,127 @@ int csa_decode_glue(const void *o, const void *P, const void *Rm, int64_t R, int
     const cudaError_t e = launch_decode_glue(o, P, Rm, R, c, d, q_next, qI ? &q4 : nullptr, dev_error_word(), S(stream));
     if (e == cudaErrorInvalidValue) return CSA_ERR_INVALID_ARG;
     return status_of(e);
+}
+
+} // extern "C"
+
+// ------------------------------------------------------------------------------------------
+// latent attention
+// ------------------------------------------------------------------------------------------
+
+namespace {
+
+// The rows of a latent cache: c = R + rope_dims with both parts present.
+bool latent_rows_ok(const csa_kv_rows *rows)
+{
+    return rows && rows->n >= 0 && rows->rope_dims > 0 && rows->rope_dims < rows->c && kv_rows_ok(rows, 0, rows->c);
+}
+
+bool row_map_ok(const int32_t *pages, int32_t max_pages, int32_t page_rows, const int64_t *off)
+{
+    return pages ? max_pages >= 1 && page_rows >= 1 : off != nullptr;
+}
+
+RowMap row_map(const int32_t *pages, int32_t max_pages, int32_t page_rows, const int64_t *off, int64_t n)
+{
+    return RowMap{pages, off, max_pages, page_rows, n};
+}
+
+constexpr int64_t kMaxLen = (int64_t)1 << 30;
+
+bool latent_decode_shape_ok(int64_t B, int32_t Lq, int32_t H, int32_t R, int32_t rd, int64_t max_len)
+{
+    return Lq <= 64 && H <= 128 && R <= 512 && R % 32 == 0 && rd <= 128 && max_len <= kMaxLen &&
+           B <= ((int64_t)1 << 31) / 64 / 128;
+}
+
+} // namespace
+
+extern "C" {
+
+int latent_append(const void *x, int32_t in_dtype, int64_t n, const float *g, float eps, double base, const int64_t *pos,
+                  const int32_t *seq, int64_t B, const int32_t *pages, int32_t max_pages, int32_t page_rows,
+                  const int64_t *off, const csa_kv_rows *out, void *stream)
+{
+    if (!x || !pos || n < 0 || B < 0 || !dtype_ok(in_dtype) || !aligned16(x)) return CSA_ERR_INVALID_ARG;
+    if (!latent_rows_ok(out) || !row_map_ok(pages, max_pages, page_rows, off)) return CSA_ERR_INVALID_ARG;
+    if (!seq && n > B) return CSA_ERR_INVALID_ARG;
+    if (g && (!aligned16(g) || !(eps >= 0.f) || !std::isfinite(eps))) return CSA_ERR_INVALID_ARG;
+    if (base != 0.0 && !(base > 1.0 && std::isfinite(base))) return CSA_ERR_INVALID_ARG;
+    if (out->c - out->rope_dims > 1024 || out->rope_dims > 256) return CSA_ERR_UNSUPPORTED;
+    if (n == 0) return CSA_OK;
+    const LatentAppendArgs a{x, n, B, g, eps, base, pos, seq, row_map(pages, max_pages, page_rows, off, out->n),
+                             to_dev(*out), dev_error_word()};
+    return status_of(launch_latent_append(a, in_dtype, S(stream)));
+}
+
+int latent_gather(const csa_kv_rows *rows, const int64_t *cu, const int64_t *start, int64_t B, const int32_t *pages,
+                  int32_t max_pages, int32_t page_rows, const int64_t *off, int64_t n_out, void *lat, void *rope,
+                  int32_t out_dtype, void *stream)
+{
+    if (!cu || B < 0 || n_out < 0 || (!lat && !rope) || !dtype_ok(out_dtype)) return CSA_ERR_INVALID_ARG;
+    if (!latent_rows_ok(rows) || !row_map_ok(pages, max_pages, page_rows, off)) return CSA_ERR_INVALID_ARG;
+    if ((lat && !aligned16(lat)) || (rope && !aligned16(rope))) return CSA_ERR_INVALID_ARG;
+    if (rows->c - rows->rope_dims > 1024 || rows->rope_dims > 256 || n_out > ((int64_t)1 << 36)) return CSA_ERR_UNSUPPORTED;
+    if (n_out == 0 || B == 0) return CSA_OK;
+    const LatentGatherArgs a{to_dev(*rows), cu, start, B, n_out, row_map(pages, max_pages, page_rows, off, rows->n),
+                             lat, rope, dev_error_word()};
+    return status_of(launch_latent_gather(a, out_dtype, S(stream)));
+}
+
+size_t latent_attn_decode_workspace_size(int64_t B, int32_t Lq, int32_t H, int32_t R, int64_t max_len)
+{
+    if (B <= 0 || Lq <= 0 || H <= 0 || R <= 0 || max_len < 0 || !latent_decode_shape_ok(B, Lq, H, R, 16, max_len)) return 0;
+    int grid;
+    return round_up(latent_decode_generic_workspace(B, Lq, H, R, max_len, &grid)) + kAlign;
+}
+
+int latent_attn_decode(const void *q, const csa_kv_rows *rows, const int64_t *pos, const int32_t *pages, int32_t max_pages,
+                       int32_t page_rows, const int64_t *off, float scale, int64_t B, int32_t Lq, int32_t H,
+                       int64_t max_len, void *o, float *lse, void *ws, size_t ws_bytes, void *stream)
+{
+    if (!q || !pos || !o || B < 0 || Lq < 1 || H < 1 || max_len < 0 || !std::isfinite(scale)) return CSA_ERR_INVALID_ARG;
+    if (!latent_rows_ok(rows) || !row_map_ok(pages, max_pages, page_rows, off)) return CSA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(o)) return CSA_ERR_INVALID_ARG;
+    const int32_t rd = rows->rope_dims, R = rows->c - rd;
+    if (!latent_decode_shape_ok(B, Lq, H, R, rd, max_len)) return CSA_ERR_UNSUPPORTED;
+    if (B == 0) return CSA_OK;
+    if (!ws || ws_bytes < latent_attn_decode_workspace_size(B, Lq, H, R, max_len)) return CSA_ERR_WORKSPACE;
+    LatentDecodeArgs a{};
+    a.q = (const uint16_t *)q;
+    a.rows = to_dev(*rows);
+    a.pos = pos;
+    a.map = row_map(pages, max_pages, page_rows, off, rows->n);
+    a.scale = scale;
+    a.B = B;
+    a.Lq = Lq;
+    a.H = H;
+    a.max_len = max_len;
+    a.o = (uint16_t *)o;
+    a.lse = lse;
+    a.part = reinterpret_cast<float *>((reinterpret_cast<uintptr_t>(ws) + kAlign - 1) / kAlign * kAlign);
+    a.err = dev_error_word();
+    latent_decode_generic_workspace(B, Lq, H, R, max_len, &a.grid);
+    note_path(CSA_PATH_LATENT_DECODE_GENERIC);
+    return status_of(launch_latent_decode_generic(a, S(stream)));
+}
+
+int latent_attn_prefill(const void *q, const void *kv, const void *k_rope, const int64_t *cu_q, const int64_t *cu_k, int64_t B,
+                        int64_t Tq, int64_t Tk, int32_t H, int32_t dn, int32_t dr, int32_t dv, int64_t max_q, float scale,
+                        int32_t causal, int32_t dtype, void *o, float *lse, void *stream)
+{
+    if (!q || !cu_q || !cu_k || !o || B < 0 || Tq < 0 || Tk < 0 || max_q < 0 || !dtype_ok(dtype)) return CSA_ERR_INVALID_ARG;
+    if (Tk > 0 && (!kv || !k_rope)) return CSA_ERR_INVALID_ARG;
+    if (H < 1 || dn < 1 || dr < 1 || dv < 1 || !std::isfinite(scale)) return CSA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(kv) || !aligned16(k_rope) || !aligned16(o)) return CSA_ERR_INVALID_ARG;
+    if (H > 128 || dn % 16 || dr % 16 || dv % 16 || dn + dr > 256 || dv > 256) return CSA_ERR_UNSUPPORTED;
+    if (max_q > Tq) max_q = Tq;
+    if (Tq >= ((int64_t)1 << 31) || Tk >= ((int64_t)1 << 31) || B * ((max_q + 31) / 32) >= ((int64_t)1 << 31)) return CSA_ERR_UNSUPPORTED;
+    if (B == 0 || Tq == 0 || max_q == 0) return CSA_OK;
+    const LatentPrefillArgs a{q, kv, k_rope, cu_q, cu_k, B, Tq, Tk, max_q, H, dn, dr, dv, scale, causal ? 1 : 0, o, lse,
+                              dev_error_word()};
+    note_path(CSA_PATH_LATENT_PREFILL_GENERIC);
+    return status_of(launch_latent_prefill_generic(a, dtype, S(stream)));
 }
 
 } // extern "C"

@@ -1,0 +1,156 @@
+// latent.cuh -- arguments and the work schedule shared by the latent attention kernels: a cache of
+// one row per token (R latent channels in FP8 with a row scale, rd rotated channels in BF16;
+// csa_kv_rows with c = R + rd, rope_dims = rd), written by latent_append, read back by
+// latent_gather and attended by latent_attn_decode (absorbed form); latent_attn_prefill attends
+// the expanded keys and values.
+#pragma once
+
+#include "common.cuh"
+
+namespace csa {
+
+// Where the row of position s of sequence b lies: through a page table, or at off[b] + s.
+struct RowMap {
+    const int32_t *pages; // [B, max_pages] or null
+    const int64_t *off;   // [B] when pages is null
+    int max_pages, page_rows;
+    int64_t n; // rows of the cache
+
+    // Row of position s, or -1 when the table or the cache does not hold it.
+    __device__ __forceinline__ int64_t row(int64_t b, int64_t s) const
+    {
+        const int64_t r = paged_row(pages, max_pages, page_rows, b, s, pages ? 0 : off[b]);
+        return r >= 0 && r < n ? r : -1;
+    }
+};
+
+struct LatentAppendArgs {
+    const void *x;
+    int64_t n, B;
+    const float *g;
+    float eps;
+    double base; // 0: the rotated part is stored as given
+    const int64_t *pos;
+    const int32_t *seq; // null: row i belongs to sequence i
+    RowMap map;
+    KvRowsDev out;
+    int *err;
+};
+cudaError_t launch_latent_append(const LatentAppendArgs &a, int in_dtype, cudaStream_t st);
+
+struct LatentGatherArgs {
+    KvRowsDev rows;
+    const int64_t *cu, *start;
+    int64_t B, n_out;
+    RowMap map;
+    void *lat, *rope;
+    int *err;
+};
+cudaError_t launch_latent_gather(const LatentGatherArgs &a, int out_dtype, cudaStream_t st);
+
+struct LatentDecodeArgs {
+    const uint16_t *q; // [B, Lq, H, R + rd] bf16
+    KvRowsDev rows;
+    const int64_t *pos; // position of each sequence's first new token
+    RowMap map;
+    float scale;
+    int64_t B;
+    int Lq, H;
+    int64_t max_len;
+    uint16_t *o; // [B, Lq, H, R] bf16
+    float *lse;  // [B, Lq, H] or null
+    float *part; // partials: 2 slots per CTA of RB rows, R + 2 floats each
+    int grid;    // CTAs of the split
+    int *err;
+};
+
+// Positions token j of a sequence sees (0 .. result - 1).
+__device__ __forceinline__ int64_t latent_visible(const LatentDecodeArgs &a, int64_t b, int j)
+{
+    int64_t p = a.pos[b];
+    p = (p < a.max_len ? p : a.max_len) + j + 1;
+    return p < 0 ? 0 : (p < a.max_len ? p : a.max_len);
+}
+
+// The split of a decode call: every (sequence, block of RB query rows) is a run of key tiles, all
+// runs lie one behind another, and CTA i of G takes the tiles [i T / G, (i + 1) T / G) of them.  So
+// the work is even whatever the lengths are, and a CTA cuts at most the two runs at its ends: its
+// run that starts inside goes to slot 2i, the one that starts at its first tile but does not end
+// here to slot 2i + 1; a run that lies in one CTA is finished there.  A sequence that sees nothing
+// has one (empty) tile, so its rows are written too.
+template <int RB, int KT> struct LatentSplit {
+    static __device__ __forceinline__ int64_t tiles(const LatentDecodeArgs &a, int64_t b)
+    {
+        const int64_t t = (latent_visible(a, b, a.Lq - 1) + KT - 1) / KT;
+        return t < 1 ? 1 : t;
+    }
+    static __host__ __device__ __forceinline__ int64_t row_blocks(int Lq, int H) { return ((int64_t)Lq * H + RB - 1) / RB; }
+    // Tiles of the sequences [0, b1), one warp.
+    static __device__ __forceinline__ int64_t warp_total(const LatentDecodeArgs &a, int64_t b0, int64_t b1, int lane)
+    {
+        int64_t s = 0;
+        for (int64_t b = b0 + lane; b < b1; b += 32) s += tiles(a, b);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        return s;
+    }
+    // The sequence that holds tile `at` (in units of one row block's tiles scaled by nrb) and the
+    // tiles before it; one warp, every lane returns the same.
+    static __device__ __forceinline__ void warp_find(const LatentDecodeArgs &a, int64_t at, int64_t nrb, int lane,
+                                                     int64_t *b_out, int64_t *before)
+    {
+        int64_t base = 0;
+        for (int64_t b0 = 0; b0 < a.B; b0 += 32) {
+            int64_t v = b0 + lane < a.B ? tiles(a, b0 + lane) * nrb : 0, inc = v;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t u = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += u;
+            }
+            const unsigned hit = __ballot_sync(0xffffffffu, base + inc > at);
+            if (hit) {
+                const int l = __ffs(hit) - 1;
+                *b_out = b0 + l;
+                *before = base + __shfl_sync(0xffffffffu, inc - v, l);
+                return;
+            }
+            base += __shfl_sync(0xffffffffu, inc, 31);
+        }
+        *b_out = a.B;
+        *before = base;
+    }
+};
+
+// A CTA's walk over its runs.
+struct LatentRun {
+    int64_t b, t0, t1; // sequence, first tile and end of the part that lies here
+    int rb;            // row block
+    bool whole, first; // the run lies here entirely; its first tile lies here
+};
+
+cudaError_t launch_latent_decode_generic(LatentDecodeArgs a, cudaStream_t st);
+size_t latent_decode_generic_workspace(int64_t B, int Lq, int H, int R, int64_t max_len, int *grid);
+
+struct LatentPrefillArgs {
+    const void *q, *kv, *k_rope; // [Tq, H, dn + dr], [Tk, H, dn + dv], [Tk, dr]
+    const int64_t *cu_q, *cu_k;  // [B + 1]
+    int64_t B, Tq, Tk, max_q;
+    int H, dn, dr, dv;
+    float scale;
+    int causal;
+    void *o;    // [Tq, H, dv]
+    float *lse; // [Tq, H] or null
+    int *err;
+};
+
+// The rows of sequence b in a packed array of T rows.
+__device__ __forceinline__ void packed_range(const int64_t *cu, int64_t b, int64_t T, int64_t *beg, int64_t *end)
+{
+    const int64_t s = cu[b], e = cu[b + 1];
+    *beg = s < 0 ? 0 : (s < T ? s : T);
+    *end = e < *beg ? *beg : (e < T ? e : T);
+}
+
+cudaError_t launch_latent_prefill_generic(const LatentPrefillArgs &a, int dtype, cudaStream_t st);
+
+} // namespace csa

@@ -1,0 +1,324 @@
+// latent_generic.cu -- latent attention on the CUDA cores, for the shapes and types that the
+// tensor-core kernels do not take, and the merge of a split decode.
+//
+// Both kernels hold a tile of keys in shared memory as fp32.  Scores: lane = key, the query's
+// channels broadcast from shared memory, so a key's dot product needs no reduction over lanes (the
+// odd row stride keeps the 32 lanes in 32 banks).  Values: lane = channel (+ 32 i), a key's
+// probability by shuffle.  One pass with the running maximum and sum of the softmax (log2 domain,
+// fp32).  ALU-bound: (c + R) fused multiply-adds per query row and key.
+#include "latent.cuh"
+
+namespace csa {
+
+namespace {
+
+constexpr int kWarps = 8, kRowsPerWarp = 4;
+constexpr int kRB = kWarps * kRowsPerWarp; // query rows of a block
+constexpr int kKT = 32;                    // keys of a tile
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+using Split = LatentSplit<kRB, kKT>;
+
+// One tile of up to 32 keys for one query row: q [dk] and kt [32, ldk] in shared memory, score of
+// key `lane` masked by `seen`, values vt[j * ldv + ch], ch < dv.
+template <int NV>
+__device__ __forceinline__ void tile_step(const float *q, const float *kt, int ldk, int dk, const float *vt, int ldv, int dv,
+                                          float scale_log2, bool seen, int lane, float &m, float &l, float (&acc)[NV])
+{
+    float z = 0.f;
+    for (int d = 0; d < dk; ++d) z = fmaf(q[d], kt[lane * ldk + d], z);
+    z = seen ? z * scale_log2 : -INFINITY;
+    const float m_new = fmaxf(m, warp_max(z));
+    if (m_new == -INFINITY) return; // nothing seen so far
+    const float f = exp2f(m - m_new), p = seen ? exp2f(z - m_new) : 0.f;
+    m = m_new;
+    l = fmaf(l, f, warp_sum(p));
+#pragma unroll
+    for (int i = 0; i < NV; ++i) acc[i] *= f;
+    for (int j = 0; j < kKT; ++j) {
+        const float pj = __shfl_sync(0xffffffffu, p, j);
+        if (pj == 0.f) continue; // an unseen key's values are not touched, whatever they are
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (lane + 32 * i < dv) acc[i] = fmaf(pj, vt[j * ldv + lane + 32 * i], acc[i]);
+    }
+}
+
+// ---- absorbed form -------------------------------------------------------------------------
+
+constexpr int kMaxNV = 16; // R <= 512
+
+__global__ void __launch_bounds__(32 * kWarps) latent_decode_generic_kernel(LatentDecodeArgs a)
+{
+    extern __shared__ float sm[];
+    __shared__ int64_t s_at[3]; // sequence, tiles before it, tiles of the whole call
+    __shared__ int ok[kKT];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int rd = a.rows.rope_dims, R = a.rows.c - rd, c = a.rows.c, ld = c + 1;
+    float *kt = sm, *qs = sm + kKT * ld; // [kKT, ld], [kRB, c]
+    const int64_t nrb = Split::row_blocks(a.Lq, a.H), G = gridDim.x;
+    if (warp == 0) {
+        const int64_t T = Split::warp_total(a, 0, a.B, lane) * nrb;
+        int64_t b, before;
+        Split::warp_find(a, T * blockIdx.x / G, nrb, lane, &b, &before);
+        if (lane == 0) s_at[0] = b, s_at[1] = before, s_at[2] = T;
+    }
+    __syncthreads();
+    const int64_t T = s_at[2], end = T * (blockIdx.x + 1) / G;
+    int64_t at = T * blockIdx.x / G, b = s_at[0], before = s_at[1];
+    while (at < end && b < a.B) {
+        const int64_t tiles = Split::tiles(a, b);
+        const int rb = (int)((at - before) / tiles);
+        const int64_t t0 = (at - before) % tiles, t1 = min(tiles, t0 + end - at);
+        // the block's queries
+        const int row0 = rb * kRB, n_rows = min(kRB, a.Lq * a.H - row0);
+        __syncthreads();
+        for (int e = threadIdx.x; e < n_rows * c; e += 32 * kWarps)
+            qs[e] = bf16_to_f32(a.q[((int64_t)b * a.Lq * a.H + row0) * c + e]);
+        float m[kRowsPerWarp], l[kRowsPerWarp], acc[kRowsPerWarp][kMaxNV];
+#pragma unroll
+        for (int u = 0; u < kRowsPerWarp; ++u) {
+            m[u] = -INFINITY;
+            l[u] = 0.f;
+#pragma unroll
+            for (int i = 0; i < kMaxNV; ++i) acc[u][i] = 0.f;
+        }
+        const int64_t seen_all = latent_visible(a, b, a.Lq - 1);
+        for (int64_t t = t0; t < t1; ++t) {
+            __syncthreads();
+            for (int e = threadIdx.x; e < kKT * (c / 4); e += 32 * kWarps) {
+                const int j = e / (c / 4), ch = 4 * (e % (c / 4));
+                const int64_t s = t * kKT + j;
+                const int64_t row = s < seen_all ? a.map.row(b, s) : -1;
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (row >= 0) {
+                    if (ch < R) {
+                        const uint32_t u = *reinterpret_cast<const uint32_t *>(a.rows.fp8 + row * R + ch);
+                        const float sc = a.rows.scale[row];
+                        v = make_float4(e4m3_decode(u & 255) * sc, e4m3_decode((u >> 8) & 255) * sc,
+                                        e4m3_decode((u >> 16) & 255) * sc, e4m3_decode(u >> 24) * sc);
+                    } else {
+                        v = Ld4<uint16_t>::at(a.rows.rope, row * rd + (ch - R));
+                    }
+                }
+                float *d = kt + j * ld + ch;
+                d[0] = v.x, d[1] = v.y, d[2] = v.z, d[3] = v.w;
+                if (ch == 0) {
+                    ok[j] = row >= 0;
+                    if (s < seen_all && row < 0) flag_error(a.err, CSA_DEVERR_INDEX);
+                }
+            }
+            __syncthreads();
+#pragma unroll
+            for (int u = 0; u < kRowsPerWarp; ++u) {
+                const int r = warp * kRowsPerWarp + u;
+                if (r >= n_rows) continue;
+                const bool seen = ok[lane] && t * kKT + lane < latent_visible(a, b, (row0 + r) / a.H);
+                tile_step<kMaxNV>(qs + r * c, kt, ld, c, kt, ld, R, a.scale * kLog2e, seen, lane, m[u], l[u], acc[u]);
+            }
+        }
+        const bool first = t0 == 0, whole = first && t1 == tiles;
+#pragma unroll
+        for (int u = 0; u < kRowsPerWarp; ++u) {
+            const int r = warp * kRowsPerWarp + u;
+            if (r >= n_rows) continue;
+            if (whole) {
+                const int64_t row = (int64_t)b * a.Lq * a.H + row0 + r;
+                const float inv = l[u] != 0.f ? 1.f / l[u] : 0.f;
+#pragma unroll
+                for (int i = 0; i < kMaxNV; ++i)
+                    if (lane + 32 * i < R) a.o[row * R + lane + 32 * i] = f32_to_bf16_bits(acc[u][i] * inv);
+                if (a.lse && lane == 0) a.lse[row] = l[u] != 0.f ? (m[u] + log2f(l[u])) * kLn2 : -INFINITY;
+            } else {
+                float *p = a.part + ((2 * (int64_t)blockIdx.x + first) * kRB + r) * (R + 4);
+                if (lane == 0) p[0] = m[u], p[1] = l[u];
+#pragma unroll
+                for (int i = 0; i < kMaxNV; ++i)
+                    if (lane + 32 * i < R) p[4 + lane + 32 * i] = acc[u][i];
+            }
+        }
+        at += t1 - t0;
+        if (t1 == tiles && rb + 1 == nrb) {
+            before += tiles * nrb;
+            ++b;
+        }
+    }
+}
+
+// Merge of the parts of a run that the split cut: one CTA per query row.  With part i holding the
+// maximum m_i (log2 domain), the sum l_i and the unnormalised output O_i, the run's are
+// m = max m_i, l = sum 2^(m_i - m) l_i, O = sum 2^(m_i - m) O_i; the output is O / l.
+template <int RB, int KT>
+__global__ void __launch_bounds__(128) latent_merge_kernel(LatentDecodeArgs a, int64_t G, float o_factor)
+{
+    __shared__ int64_t s_at[3];
+    const int lane = threadIdx.x & 31;
+    const int64_t rows = (int64_t)a.Lq * a.H, b = blockIdx.x / rows;
+    const int r = (int)(blockIdx.x % rows), rb = r / RB;
+    const int R = a.rows.c - a.rows.rope_dims;
+    using Split = LatentSplit<RB, KT>;
+    const int64_t nrb = Split::row_blocks(a.Lq, a.H);
+    if (threadIdx.x < 32) {
+        const int64_t before = Split::warp_total(a, 0, b, lane), after = Split::warp_total(a, b, a.B, lane);
+        if (lane == 0) s_at[0] = before * nrb, s_at[1] = (before + after) * nrb;
+    }
+    __syncthreads();
+    const int64_t tiles = Split::tiles(a, b), T = s_at[1], s0 = s_at[0] + rb * tiles, s1 = s0 + tiles;
+    // the CTAs that hold tiles s0 and s1 - 1: the largest i with i T / G <= tile
+    int64_t i0 = (s0 * G + G - 1) / T, i1 = ((s1 - 1) * G + G - 1) / T;
+    while (i0 > 0 && T * i0 / G > s0) --i0;
+    while (i0 + 1 < G && T * (i0 + 1) / G <= s0) ++i0;
+    while (i1 > 0 && T * i1 / G > s1 - 1) --i1;
+    while (i1 + 1 < G && T * (i1 + 1) / G <= s1 - 1) ++i1;
+    if (i0 == i1) return; // finished by the CTA that holds it
+    const int64_t ld = R + 4;
+    auto part = [&](int64_t i) { return a.part + ((2 * i + (i == i0 ? 1 : 0)) * RB + (r % RB)) * ld; };
+    float m = -INFINITY;
+    for (int64_t i = i0; i <= i1; ++i)
+        if (T * i / G < T * (i + 1) / G) m = fmaxf(m, part(i)[0]);
+    float l = 0.f;
+    float4 acc[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (m > -INFINITY)
+        for (int64_t i = i0; i <= i1; ++i) {
+            if (T * i / G >= T * (i + 1) / G) continue; // a CTA without tiles has no part
+            const float *p = part(i);
+            const float f = exp2f(p[0] - m);
+            l = fmaf(f, p[1], l);
+            if (f == 0.f) continue;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int j = 4 * (threadIdx.x + 128 * k);
+                if (j < R) {
+                    const float4 v = *reinterpret_cast<const float4 *>(p + 4 + j);
+                    acc[k].x = fmaf(f, v.x, acc[k].x);
+                    acc[k].y = fmaf(f, v.y, acc[k].y);
+                    acc[k].z = fmaf(f, v.z, acc[k].z);
+                    acc[k].w = fmaf(f, v.w, acc[k].w);
+                }
+            }
+        }
+    const float inv = l != 0.f ? o_factor / l : 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int j = 4 * (threadIdx.x + 128 * k);
+        if (j < R) st4(a.o, (int64_t)blockIdx.x * R + j, make_float4(acc[k].x * inv, acc[k].y * inv, acc[k].z * inv, acc[k].w * inv));
+    }
+    if (a.lse && threadIdx.x == 0) a.lse[blockIdx.x] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+}
+
+// ---- expanded form -------------------------------------------------------------------------
+
+constexpr int kMaxNVp = 8; // dv <= 256
+
+template <typename T> __global__ void __launch_bounds__(32 * kWarps) latent_prefill_generic_kernel(LatentPrefillArgs a)
+{
+    extern __shared__ float sm[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int dk = a.dn + a.dr, ldk = dk + 1, h = blockIdx.y;
+    const int64_t per = (a.max_q + kRB - 1) / kRB, b = blockIdx.x / per;
+    float *kt = sm, *vt = kt + kKT * ldk, *qs = vt + kKT * a.dv; // [kKT, ldk], [kKT, dv], [kRB, dk]
+    int64_t q0, q1, k0, k1;
+    packed_range(a.cu_q, b, a.Tq, &q0, &q1);
+    packed_range(a.cu_k, b, a.Tk, &k0, &k1);
+    const int64_t nq = q1 - q0, nk = k1 - k0, lag = nk - nq;
+    const int64_t i0 = (blockIdx.x % per) * kRB;
+    if (i0 >= nq || i0 >= a.max_q) return;
+    const int n_rows = (int)min((int64_t)kRB, min(nq, a.max_q) - i0);
+    const T *q = static_cast<const T *>(a.q), *kv = static_cast<const T *>(a.kv), *kr = static_cast<const T *>(a.k_rope);
+    for (int e = threadIdx.x; e < n_rows * dk; e += 32 * kWarps)
+        qs[e] = ld1<T>(q, ((q0 + i0 + e / dk) * a.H + h) * dk + e % dk);
+    float m[kRowsPerWarp], l[kRowsPerWarp], acc[kRowsPerWarp][kMaxNVp];
+#pragma unroll
+    for (int u = 0; u < kRowsPerWarp; ++u) {
+        m[u] = -INFINITY;
+        l[u] = 0.f;
+#pragma unroll
+        for (int i = 0; i < kMaxNVp; ++i) acc[u][i] = 0.f;
+    }
+    const int64_t seen_all = a.causal ? max((int64_t)0, min(nk, i0 + n_rows + lag)) : nk;
+    for (int64_t t = 0; t < seen_all; t += kKT) {
+        const int n = (int)min((int64_t)kKT, seen_all - t);
+        __syncthreads();
+        for (int e = threadIdx.x; e < kKT * (dk + a.dv); e += 32 * kWarps) {
+            const int j = e / (dk + a.dv), ch = e % (dk + a.dv);
+            const int64_t row = k0 + t + j;
+            float v = 0.f;
+            if (j < n) v = ch >= a.dn && ch < dk ? ld1<T>(kr, row * a.dr + ch - a.dn)
+                                                 : ld1<T>(kv, (row * a.H + h) * (a.dn + a.dv) + (ch < a.dn ? ch : ch - a.dr));
+            if (ch < dk) kt[j * ldk + ch] = v;
+            else vt[j * a.dv + ch - dk] = v;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < kRowsPerWarp; ++u) {
+            const int r = warp * kRowsPerWarp + u;
+            if (r >= n_rows) continue;
+            const bool seen = lane < n && (!a.causal || t + lane <= i0 + r + lag);
+            tile_step<kMaxNVp>(qs + r * dk, kt, ldk, dk, vt, a.dv, a.dv, a.scale * kLog2e, seen, lane, m[u], l[u], acc[u]);
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < kRowsPerWarp; ++u) {
+        const int r = warp * kRowsPerWarp + u;
+        if (r >= n_rows) continue;
+        const int64_t row = (q0 + i0 + r) * a.H + h;
+        const float inv = l[u] != 0.f ? 1.f / l[u] : 0.f;
+#pragma unroll
+        for (int i = 0; i < kMaxNVp; ++i) {
+            const int ch = lane + 32 * i;
+            if (ch >= a.dv) continue;
+            if constexpr (sizeof(T) == 4) static_cast<float *>(a.o)[row * a.dv + ch] = acc[u][i] * inv;
+            else static_cast<uint16_t *>(a.o)[row * a.dv + ch] = f32_to_bf16_bits(acc[u][i] * inv);
+        }
+        if (a.lse && lane == 0) a.lse[row] = l[u] != 0.f ? (m[u] + log2f(l[u])) * kLn2 : -INFINITY;
+    }
+}
+
+} // namespace
+
+// Two CTAs of the split per SM at most (shared memory), as many as there are tiles when that is less.
+size_t latent_decode_generic_workspace(int64_t B, int Lq, int H, int R, int64_t max_len, int *grid)
+{
+    const int64_t tiles = (max_len + kKT - 1) / kKT, work = B * Split::row_blocks(Lq, H) * (tiles < 1 ? 1 : tiles);
+    const int64_t most = device_sms();
+    *grid = (int)(work < most ? work : most);
+    return (size_t)*grid * 2 * kRB * (R + 4) * sizeof(float);
+}
+
+template <int RB, int KT> static cudaError_t launch_merge(const LatentDecodeArgs &a, int grid, float o_factor, cudaStream_t st)
+{
+    if (grid < 2) return cudaSuccess; // one CTA cuts no run
+    latent_merge_kernel<RB, KT><<<(unsigned)(a.B * a.Lq * a.H), 128, 0, st>>>(a, grid, o_factor);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_latent_decode_generic(LatentDecodeArgs a, cudaStream_t st)
+{
+    const size_t smem = (size_t)(kKT * (a.rows.c + 1) + kRB * a.rows.c) * sizeof(float);
+    cudaError_t e = cudaFuncSetAttribute(latent_decode_generic_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    latent_decode_generic_kernel<<<(unsigned)a.grid, 32 * kWarps, smem, st>>>(a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return launch_merge<kRB, kKT>(a, a.grid, 1.f, st);
+}
+
+template <typename T> static cudaError_t prefill_generic(const LatentPrefillArgs &a, cudaStream_t st)
+{
+    const int dk = a.dn + a.dr;
+    const size_t smem = (size_t)(kKT * (dk + 1) + kKT * a.dv + kRB * dk) * sizeof(float);
+    cudaError_t e = cudaFuncSetAttribute(latent_prefill_generic_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    const int64_t blocks = a.B * ((a.max_q + kRB - 1) / kRB);
+    latent_prefill_generic_kernel<T><<<dim3((unsigned)blocks, (unsigned)a.H), 32 * kWarps, smem, st>>>(a);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_latent_prefill_generic(const LatentPrefillArgs &a, int dtype, cudaStream_t st)
+{
+    return dtype == CSA_F32 ? prefill_generic<float>(a, st) : prefill_generic<uint16_t>(a, st);
+}
+
+} // namespace csa

@@ -406,8 +406,99 @@ int csa_decode_glue(const void *o, const void *P, const void *Rm, int64_t R, int
 /* ----------------------------------------------------------------------------------------- */
 
 /*
+ * Latent attention: layers that keep one uncompressed latent row per token for all heads, next to
+ * the compressed layers above.  A cache row has c = R + rd channels, the R latent ones (key and
+ * value) in FP8 with a row scale and the rd rotated ones (key only) in BF16: a csa_kv_rows with
+ * rope_dims = rd > 0.  Position s (0-based) of sequence b is row
+ *     pages[b * max_pages + s / page_rows] * page_rows + s % page_rows   (pages != NULL)
+ *     off[b] + s                                                         (pages == NULL)
+ * of the cache.  A row outside the cache, or a page index >= max_pages, is refused: it is not
+ * touched and sets CSA_DEVERR_INDEX.
+ *
+ * latent_append -- write the rows x [n, c] (in_dtype) into the cache: row i belongs to position
+ * pos[i] of sequence seq[i] (seq NULL: of sequence i, n <= B).  pos[i] < 0 skips the row; seq[i]
+ * outside [0, B) is refused.  Per row, in fp32:
+ *   u = x[0:R];  u = u / sqrt(mean(u^2) + eps) * g                       when g != NULL (g [R] fp32)
+ *   v = x[R:c];  the pairs (2k, 2k+1) of v rotated counter-clockwise by   when base != 0
+ *       pos[i] * base^(-2k/rd)                                            (angles in fp64)
+ *   s = amax(|u|) / 448 (1 when that is not positive), fp8 = e4m3(u / s), rope = bf16(v)
+ * as csa_quantize_kv quantises.  The (sequence, position) pairs of one call have to be distinct: of
+ * rows written to the same place at once, an unspecified mixture remains.
+ * Errors: CSA_ERR_INVALID_ARG for a null x, pos or out, n < 0, B < 0, a bad dtype, x or g not 16-byte
+ * aligned, seq NULL with n > B, no pages and no off, pages with max_pages or page_rows < 1, a g with
+ * a negative or non-finite eps, a base that is neither 0 nor a finite number > 1, or rows that are
+ * not as above; CSA_ERR_UNSUPPORTED for R > 1024 or rd > 256.
+ */
+int latent_append(const void *x, int32_t in_dtype, int64_t n, const float *g, float eps, double base, const int64_t *pos,
+                  const int32_t *seq, int64_t B, const int32_t *pages, int32_t max_pages, int32_t page_rows,
+                  const int64_t *off, const csa_kv_rows *out, void *stream);
+
+/*
+ * latent_gather -- read ragged runs of positions back, dequantised and packed: output row cu[b] + j
+ * (0 <= j < cu[b+1] - cu[b]) is position start[b] + j of sequence b (start NULL: 0).  cu [B+1]
+ * int64, not decreasing.  lat [n_out, R] gets e4m3(fp8) * scale and rope [n_out, rd] the rotated
+ * part, in out_dtype; either may be NULL.  Output rows below cu[0], from cu[B] on, or past n_out are
+ * left as they were; a refused row comes out as zeros.  For the expanded form: lat times the
+ * up-projection is the kv of latent_attn_prefill, rope its k_rope.
+ * Errors: CSA_ERR_INVALID_ARG for null or misaligned (16 bytes) arrays, no output, B or n_out < 0, a
+ * bad dtype, a bad page table as above, or rows that are not as above; CSA_ERR_UNSUPPORTED for
+ * R > 1024, rd > 256 or n_out > 2^36.
+ */
+int latent_gather(const csa_kv_rows *rows, const int64_t *cu, const int64_t *start, int64_t B, const int32_t *pages,
+                  int32_t max_pages, int32_t page_rows, const int64_t *off, int64_t n_out, void *lat, void *rope,
+                  int32_t out_dtype, void *stream);
+
+/*
+ * latent_attn_decode -- attention over the cache in its absorbed form: Lq new tokens of each of B
+ * sequences, H heads, queries already multiplied by the key up-projection.  Token j of sequence b sits
+ * at position pos[b] + j and sees the positions s <= pos[b] + j, at most the first max_len (its own
+ * row included: append first).  With key(s) = [lat(s), rope(s)] and z = scale * q . key(s):
+ *   o[b,j,h,:] = sum_s e^z lat(s) / sum_s e^z,   lse[b,j,h] = ln sum_s e^z
+ * and o = 0, lse = -inf for a token that sees nothing (pos[b] + j < 0: padding).
+ *   q [B, Lq, H, c] bf16;  o [B, Lq, H, R] bf16;  lse [B, Lq, H] fp32 or NULL;  pos [B] int64
+ *   max_len  host-side bound of the positions (sizes the split)
+ *   ws       workspace of latent_attn_decode_workspace_size(...) bytes, queried with the device
+ *            current; calls that may overlap (two streams, two captured graphs) need one each
+ * A sequence's tokens are summed in an order that depends on the batch's lengths and the device's SM
+ * count, not on timing: the same call gives the same bits.
+ * Limits: R a multiple of 32 and <= 512, rd <= 128, H <= 128, Lq <= 64, max_len <= 2^30, B <= 2^18.
+ * Errors: CSA_ERR_INVALID_ARG for a null q, rows, pos or o, B < 0, Lq or H < 1, max_len < 0, a
+ * non-finite scale, q or o not 16-byte aligned, a bad page table or rows as above;
+ * CSA_ERR_UNSUPPORTED outside the limits; CSA_ERR_WORKSPACE when ws is NULL or too small.
+ */
+size_t latent_attn_decode_workspace_size(int64_t B, int32_t Lq, int32_t H, int32_t R, int64_t max_len);
+int latent_attn_decode(const void *q, const csa_kv_rows *rows, const int64_t *pos, const int32_t *pages, int32_t max_pages,
+                       int32_t page_rows, const int64_t *off, float scale, int64_t B, int32_t Lq, int32_t H,
+                       int64_t max_len, void *o, float *lse, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * latent_attn_prefill -- attention in the expanded form over packed sequences of different lengths:
+ * sequence b's queries are rows cu_q[b] .. cu_q[b+1]-1 of q, its keys rows cu_k[b] .. cu_k[b+1]-1 of
+ * kv and k_rope (cu_q, cu_k [B+1] int64, not decreasing; the keys are those the cache held before and
+ * the new tokens' own, so they may be more than the queries).  key(j,h) = [kv[j,h,0:dn], k_rope[j]],
+ * value(j,h) = kv[j,h,dn:], and query i (0-based) sees key j when j < n_k and, with causal != 0,
+ * j <= i + n_k - n_q (the last query sees every key).  With z = scale * q . key:
+ *   o = sum e^z value / sum e^z,   lse = ln sum e^z;   o = 0, lse = -inf where nothing is seen.
+ *   q [Tq, H, dn + dr], kv [Tk, H, dn + dv], k_rope [Tk, dr], o [Tq, H, dv] in `dtype` (CSA_F32 /
+ *   CSA_BF16); lse [Tq, H] fp32 or NULL.  max_q bounds the query counts (sizes the grid; queries past
+ *   it are not computed).  Rows of q outside the sequences get no output: o and lse keep what
+ *   they held.  Rows of kv and k_rope outside a sequence are not part of its result whatever they
+ *   hold; a non-finite value in a sequence's own rows may reach all of its outputs.
+ * Limits: dn, dr, dv multiples of 16, dn + dr <= 256, dv <= 256, H <= 128, Tq and Tk < 2^31.
+ * Errors: CSA_ERR_INVALID_ARG for a null q, cu_q, cu_k or o, a null kv or k_rope with Tk > 0, negative
+ * sizes, H, dn, dr or dv < 1, a bad dtype, a non-finite scale, or q, kv, k_rope or o not 16-byte aligned;
+ * CSA_ERR_UNSUPPORTED outside the limits.
+ */
+int latent_attn_prefill(const void *q, const void *kv, const void *k_rope, const int64_t *cu_q, const int64_t *cu_k, int64_t B,
+                        int64_t Tq, int64_t Tk, int32_t H, int32_t dn, int32_t dr, int32_t dv, int64_t max_q, float scale,
+                        int32_t causal, int32_t dtype, void *o, float *lse, void *stream);
+
+/* ----------------------------------------------------------------------------------------- */
+
+/*
  * The kernel path that served the calling host thread's last indexer_topk(_static),
- * hybrid_attn_prefill or hybrid_attn_decode call that launched work (CSA_PATH_NONE before any).
+ * hybrid_attn_prefill, hybrid_attn_decode, latent_attn_decode or latent_attn_prefill call that
+ * launched work (CSA_PATH_NONE before any).
  * Dispatch is by shape only: the tensor-core kernels take the 64-head x 512-channel attention
  * and the 64 x 128 indexer shapes, the CUDA-core kernels every other shape the limits allow.
  * A call whose shape belongs to a tensor-core kernel never moves to a CUDA-core one: if that
@@ -421,6 +512,8 @@ int csa_decode_glue(const void *o, const void *P, const void *Rm, int64_t R, int
 #define CSA_PATH_PREFILL_GENERIC 5
 #define CSA_PATH_DECODE_TC 6        /* 64 x 512: tcgen05 split-K attention + merge */
 #define CSA_PATH_DECODE_GENERIC 7
+#define CSA_PATH_LATENT_DECODE_GENERIC 9   /* latent decode on the CUDA cores */
+#define CSA_PATH_LATENT_PREFILL_GENERIC 10 /* latent prefill on the CUDA cores */
 #define CSA_PATH_PREFILL_KEYS_TC 8   /* bf16 64 x 512, W = 128, HCA: tcgen05 with keys on M (M = 128 MMAs) */
 int32_t csa_last_path(void);
 
