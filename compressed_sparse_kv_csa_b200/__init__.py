@@ -628,6 +628,7 @@ CSA_PATH_DECODE_GENERIC = 7
 CSA_PATH_PREFILL_KEYS_TC = 8
 CSA_PATH_LATENT_DECODE_GENERIC = 9
 CSA_PATH_LATENT_PREFILL_GENERIC = 10
+CSA_PATH_LATENT_PREFILL_TC = 11
 
 
 def csa_set_wait_limit_ns(ns: int) -> int:

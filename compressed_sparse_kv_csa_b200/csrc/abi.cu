@@ -640,10 +640,14 @@ int latent_attn_prefill(const void *q, const void *kv, const void *k_rope, const
     if (!aligned16(q) || !aligned16(kv) || !aligned16(k_rope) || !aligned16(o)) return CSA_ERR_INVALID_ARG;
     if (H > 128 || dn % 16 || dr % 16 || dv % 16 || dn + dr > 256 || dv > 256) return CSA_ERR_UNSUPPORTED;
     if (max_q > Tq) max_q = Tq;
-    if (Tq >= ((int64_t)1 << 31) || Tk >= ((int64_t)1 << 31) || B * ((max_q + 31) / 32) >= ((int64_t)1 << 31)) return CSA_ERR_UNSUPPORTED;
+    if (Tq >= ((int64_t)1 << 31) || Tk >= ((int64_t)1 << 31) || B * H * ((max_q + 31) / 32) >= ((int64_t)1 << 31)) return CSA_ERR_UNSUPPORTED;
     if (B == 0 || Tq == 0 || max_q == 0) return CSA_OK;
     const LatentPrefillArgs a{q, kv, k_rope, cu_q, cu_k, B, Tq, Tk, max_q, H, dn, dr, dv, scale, causal ? 1 : 0, o, lse,
                               dev_error_word()};
+    if (latent_prefill_tc_eligible(a, dtype)) {
+        note_path(CSA_PATH_LATENT_PREFILL_TC);
+        return status_of(launch_latent_prefill_tc(a, S(stream)));
+    }
     note_path(CSA_PATH_LATENT_PREFILL_GENERIC);
     return status_of(launch_latent_prefill_generic(a, dtype, S(stream)));
 }

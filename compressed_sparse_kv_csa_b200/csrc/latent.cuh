@@ -151,6 +151,8 @@ __device__ __forceinline__ void packed_range(const int64_t *cu, int64_t b, int64
     *end = e < *beg ? *beg : (e < T ? e : T);
 }
 
+bool latent_prefill_tc_eligible(const LatentPrefillArgs &a, int dtype);
+cudaError_t launch_latent_prefill_tc(const LatentPrefillArgs &a, cudaStream_t st);
 cudaError_t launch_latent_prefill_generic(const LatentPrefillArgs &a, int dtype, cudaStream_t st);
 
 } // namespace csa

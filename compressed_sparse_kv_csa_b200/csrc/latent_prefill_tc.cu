@@ -1,0 +1,457 @@
+// latent_prefill_tc.cu -- latent attention in its expanded form on tcgen05, for bf16 heads of
+// 128 + 64 key channels and 128 value channels over packed sequences.
+//
+// One pass over the keys with the running maximum and sum of the softmax (log2 domain, fp32).  A CTA
+// takes 256 consecutive queries of one head as two tiles of 128: while one tile's scores are turned
+// into probabilities, the tensor cores work on the other's.  Per tile of 128 keys and queries:
+//   S = Q K^T   M = 128, N = 128, K = 192, in TMEM (the key's last 64 channels come from k_rope,
+//               which all heads share)
+//   P = 2^(S scale log2e - m) in bf16, written over the first half of S in TMEM
+//   O += P V    M = 128, N = 128, K = 128, P read from TMEM, V read MN-major
+// TMEM: S0, S1, O0, O1 of 128 columns each.  The running maximum moves, and O is rescaled in TMEM, only
+// when a tile raises it by more than 8 (2^8 fits any of the sums' fp32); S of tile i complete implies
+// P V of tile i - 1 complete, since one thread issues both in order, so the rescale needs no wait.
+// Rounding P to bf16 (the type of V, which one MMA shares) costs 2^-9 relative a term; the sum is
+// taken over the unrounded fp32 values.
+//
+// Shared memory: Q 96 KB, and a ring of eight 16 KB slots of [128 rows x 64 channels] that the key
+// (three slots a tile) and value (two) boxes pass through in order, so that the loads run up to 1.6
+// tiles ahead.  Everything arrives by TMA.
+// Roles: warps 0-3 and 4-7 softmax, rescale and output of the two query tiles (one row a thread), warp 8
+// TMA, warp 9 MMA.  Bound by the tensor cores: 2 * 128 * 128 * 320 flops a tile pair.
+#include "latent.cuh"
+#include "tc_common.cuh"
+#include "tma_host.cuh"
+
+namespace csa {
+
+namespace {
+
+using namespace tc;
+
+constexpr int kDn = 128, kDr = 64, kDv = 128, kT = 128; // kT: queries and keys of a tile
+constexpr int kTmaWarp = 8, kMmaWarp = 9, kThreads = 384; // whole warpgroups, for the register split
+// A softmax thread holds a row of 128 scores.  Of the registers that the block is launched with (168 a
+// thread, checked on the host), the two softmax warpgroups take 208 a thread and the other leaves 88.
+constexpr int kRegs = 168, kRegsSoft = 208, kRegsRest = 88;
+static_assert(256 * kRegsSoft + 128 * kRegsRest <= kThreads * kRegs, "register split");
+constexpr uint32_t kSlot = 16384;
+constexpr int kSlots = 8;
+constexpr uint32_t OFF_Q = 0, OFF_RING = 2 * 3 * kSlot, OFF_BAR = OFF_RING + kSlots * kSlot, OFF_TMEM = OFF_BAR + 256;
+constexpr uint32_t SMEM_ALLOC = OFF_TMEM + 64 + 1024; // slack to align the base to 1024 bytes
+static_assert(SMEM_ALLOC <= 232448, "shared memory per block");
+enum { B_Q = 0, B_FULL, B_EMPTY = B_FULL + kSlots, B_S = B_EMPTY + kSlots, B_P = B_S + 2, B_O = B_P + 2, B_VTAIL = B_O + 2,
+       B_FINAL, NUM_BARS };
+static_assert(8 * NUM_BARS <= 256, "barrier space");
+constexpr uint32_t IDESC_S = idesc_bf16_f32(128, 128, false, false), IDESC_PV = idesc_bf16_f32(128, 128, false, true);
+constexpr uint32_t kColS = 0, kColO = 256; // + 128 t
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+struct Maps {
+    CUtensorMap q, kv, kr;
+};
+
+// What a CTA does: queries i0 .. of sequence rows [q0, q0 + nq), keys [k0, k0 + nk).
+struct Job {
+    int64_t q0, k0;
+    int h, i0, nq, nk, lag, n[2], tiles; // n[t]: key tiles of query tile t
+};
+
+__device__ __forceinline__ bool find_job(const LatentPrefillArgs &a, Job &j)
+{
+    // the query blocks that see the most keys first
+    const int per = (int)((a.max_q + 2 * kT - 1) / (2 * kT));
+    const int64_t bh = a.B * a.H, id = blockIdx.x;
+    const int64_t r = id % bh, b = r / a.H;
+    j.h = (int)(r % a.H);
+    j.i0 = (per - 1 - (int)(id / bh)) * 2 * kT;
+    int64_t q1, k1;
+    packed_range(a.cu_q, b, a.Tq, &j.q0, &q1);
+    packed_range(a.cu_k, b, a.Tk, &j.k0, &k1);
+    const int nq = (int)(q1 - j.q0);
+    j.nk = (int)(k1 - j.k0);
+    j.lag = j.nk - nq;
+    j.nq = nq < a.max_q ? nq : (int)a.max_q;
+    j.tiles = 0;
+    for (int t = 0; t < 2; ++t) {
+        const int first = j.i0 + t * kT, last = min(first + kT, j.nq); // queries of the tile
+        int64_t seen = first >= j.nq ? 0 : j.nk;
+        if (a.causal && first < j.nq) seen = min((int64_t)j.nk, (int64_t)last + j.lag);
+        j.n[t] = seen <= 0 ? 0 : (int)((seen + kT - 1) / kT);
+        j.tiles = max(j.tiles, j.n[t]);
+    }
+    return j.i0 < j.nq;
+}
+
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "setp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc),
+                 "r"(accumulate));
+}
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t pk_bf16(float lo, float hi)
+{
+    __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<uint32_t *>(&h);
+}
+
+template <int N> __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 x, y;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+struct Ring { // slot and phase of the next 16 KB box
+    int slot = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next()
+    {
+        if (++slot == kSlots) slot = 0, phase ^= 1;
+    }
+};
+
+// TMA (one warp).  The ring's order is K0 V0 K1 V1 ...
+__device__ __forceinline__ bool tma_role(const Job &j, const Maps &M, uint32_t base, int lane)
+{
+    const uint32_t bars = base + OFF_BAR;
+    auto bar = [&](int b) { return bars + 8u * (uint32_t)b; };
+    if (lane == 0) {
+        const int nt = j.i0 + kT < j.nq ? 2 : 1;
+        mbar_arrive_expect_tx(bar(B_Q), (uint32_t)nt * 3 * kSlot);
+        for (int t = 0; t < nt; ++t)
+            for (int s = 0; s < 3; ++s)
+                tma_load_3d(base + OFF_Q + (uint32_t)(3 * t + s) * kSlot, &M.q, 64 * s, j.h, (int)(j.q0 + j.i0 + t * kT), bar(B_Q));
+    }
+    Ring r;
+    uint32_t lap = 0; // the first lap's slots are empty
+    for (int i = 0; i < j.tiles; ++i) {
+        const int y = (int)(j.k0 + (int64_t)i * kT);
+        const int tail = j.nk - i * kT; // rows of the sequence in this tile, when less than kT
+        int v_slot[2];
+        for (int s = 0; s < 5; ++s) {
+            const int slot = r.slot;
+            if (lap && !mbar_wait(bar(B_EMPTY + slot), r.phase ^ 1)) return false;
+            const uint32_t dst = base + OFF_RING + (uint32_t)slot * kSlot;
+            if (s < 3) {
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(bar(B_FULL + slot), kSlot);
+                    if (s < 2) tma_load_3d(dst, &M.kv, 64 * s, j.h, y, bar(B_FULL + slot));
+                    else tma_load_2d(dst, &M.kr, 0, y, bar(B_FULL + slot));
+                }
+            } else {
+                v_slot[s - 3] = slot;
+            }
+            r.next();
+            if (r.slot == 0) lap = 1;
+        }
+        // the lower slot takes channels 0-63, so that the pair reads with one positive stride
+        const int lo = min(v_slot[0], v_slot[1]), hi = max(v_slot[0], v_slot[1]);
+        const uint32_t vlo = base + OFF_RING + (uint32_t)lo * kSlot, vhi = base + OFF_RING + (uint32_t)hi * kSlot;
+        if (tail >= kT) {
+            if (lane == 0) {
+                mbar_arrive_expect_tx(bar(B_FULL + lo), kSlot);
+                tma_load_3d(vlo, &M.kv, kDn, j.h, y, bar(B_FULL + lo));
+                mbar_arrive_expect_tx(bar(B_FULL + hi), kSlot);
+                tma_load_3d(vhi, &M.kv, kDn + 64, j.h, y, bar(B_FULL + hi));
+            }
+        } else {
+            // the sequence ends in this tile: the values behind it carry probability 0, but may hold
+            // anything (0 x NaN is NaN), so they are zeroed before the MMAs may read them
+            if (lane == 0) {
+                mbar_arrive_expect_tx(bar(B_VTAIL), 2 * kSlot);
+                tma_load_3d(vlo, &M.kv, kDn, j.h, y, bar(B_VTAIL));
+                tma_load_3d(vhi, &M.kv, kDn + 64, j.h, y, bar(B_VTAIL));
+            }
+            __syncwarp();
+            if (!__all_sync(0xffffffffu, mbar_wait(bar(B_VTAIL), 0))) return false;
+            for (int e = 8 * tail + lane; e < 8 * kT; e += 32)
+                for (int s = 0; s < 2; ++s)
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"((s ? vhi : vlo) + 16u * (uint32_t)e), "r"(0) : "memory");
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(bar(B_FULL + lo));
+                mbar_arrive(bar(B_FULL + hi));
+            }
+        }
+        __syncwarp();
+    }
+    return true;
+}
+
+// MMA issue (one thread).
+__device__ __forceinline__ bool mma_role(const Job &j, uint32_t base, uint32_t tmem)
+{
+    const uint32_t bars = base + OFF_BAR;
+    auto bar = [&](int b) { return bars + 8u * (uint32_t)b; };
+    if (!mbar_wait(bar(B_Q), 0)) return false;
+    tc_fence_after();
+    Ring r;
+    struct Box {
+        int slot[3];
+    };
+    auto take = [&](int n, Box &b) { // the ring's next n slots, loaded
+        for (int s = 0; s < n; ++s) {
+            if (!mbar_wait(bar(B_FULL + r.slot), r.phase)) return false;
+            b.slot[s] = r.slot;
+            r.next();
+        }
+        tc_fence_after();
+        return true;
+    };
+    auto free_slots = [&](int n, const Box &b) { // when the MMAs issued so far have read them
+        for (int s = 0; s < n; ++s) mma_commit(bar(B_EMPTY + b.slot[s]));
+    };
+    auto scores = [&](int t, const Box &k) {
+#pragma unroll
+        for (int s = 0; s < 3; ++s)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+                mma_bf16(tmem + kColS + 128u * t, sdesc_sw128(base + OFF_Q + (uint32_t)(3 * t + s) * kSlot + 32u * kk, 16, 1024),
+                         sdesc_sw128(base + OFF_RING + (uint32_t)k.slot[s] * kSlot + 32u * kk, 16, 1024), IDESC_S, (s | kk) != 0);
+        mma_commit(bar(B_S + t));
+    };
+    Box k, v;
+    if (j.tiles > 0) {
+        if (!take(3, k)) return false;
+        for (int t = 0; t < 2; ++t)
+            if (j.n[t] > 0) scores(t, k);
+        free_slots(3, k);
+    }
+    for (int i = 0; i < j.tiles; ++i) {
+        const uint32_t ph = (uint32_t)(i & 1);
+        if (!take(2, v)) return false;
+        const int lo = min(v.slot[0], v.slot[1]), hi = max(v.slot[0], v.slot[1]);
+        for (int t = 0; t < 2; ++t) {
+            if (i < j.n[t]) {
+                if (!mbar_wait(bar(B_P + t), ph)) return false;
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)
+                    mma_bf16_ts(tmem + kColO + 128u * t, tmem + kColS + 128u * t + 8u * kk,
+                                sdesc_sw128(base + OFF_RING + (uint32_t)lo * kSlot + 2048u * kk, (uint32_t)(hi - lo) * kSlot, 1024),
+                                IDESC_PV, (i | kk) != 0);
+                if (i + 1 == j.n[t]) mma_commit(bar(B_O + t));
+            }
+            if (t == 1) free_slots(2, v);
+            if (t == 0 && i + 1 < j.tiles && !take(3, k)) return false;
+            if (i + 1 < j.n[t]) scores(t, k);
+        }
+        if (i + 1 < j.tiles) free_slots(3, k);
+    }
+    return true;
+}
+
+// Softmax, rescale and output of query tile t: one row per thread.
+__device__ __forceinline__ bool softmax_role(const LatentPrefillArgs &a, const Job &j, uint32_t base, uint32_t tmem, int warp, int lane)
+{
+    const uint32_t bars = base + OFF_BAR;
+    auto bar = [&](int b) { return bars + 8u * (uint32_t)b; };
+    const int t = warp >> 2;
+    const uint32_t tw = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    const uint32_t tS = tw + kColS + 128u * t, tO = tw + kColO + 128u * t;
+    const int first = j.i0 + t * kT, i = first + 32 * (warp & 3) + lane; // this thread's query
+    // the last key it sees, and the last that every query of its tile sees
+    const int last = a.causal ? min(j.nk - 1, i + j.lag) : j.nk - 1;
+    const int last_all = a.causal ? min(j.nk - 1, first + j.lag) : j.nk - 1;
+    // scores are compared before they are scaled: a negative scale turns them round first, and a scale
+    // of 0 becomes one that is lost in any score (a hidden score is -inf, and 0 x -inf is NaN)
+    const bool turn = a.scale < 0.f;
+    const float sl2 = fmaxf(fabsf(a.scale) * kLog2e, 1e-37f);
+    float m = -INFINITY, l = 0.f; // maximum in use (scaled, log2 domain), sum
+    for (int c = 0; c < j.n[t]; ++c) {
+        if (!__all_sync(0xffffffffu, mbar_wait(bar(B_S + t), (uint32_t)(c & 1)))) return false;
+        tc_fence_after();
+        float s[kT];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) tmem_ld32(tS + 32u * g, *reinterpret_cast<uint32_t(*)[32]>(&s[32 * g]));
+        tmem_ld_wait();
+        if (turn) {
+#pragma unroll
+            for (int e = 0; e < kT; ++e) s[e] = -s[e];
+        }
+        if (c * kT + kT - 1 > last_all) {
+            const int n = last - c * kT; // the last visible key of the tile
+#pragma unroll
+            for (int e = 0; e < kT; ++e) s[e] = e <= n ? s[e] : -INFINITY;
+        }
+        float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int e = 4; e < kT; ++e) mx[e & 3] = fmaxf(mx[e & 3], s[e]);
+        const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
+        float f = 1.f;
+        if (mt > m + 8.f || m == -INFINITY) {
+            f = m == -INFINITY ? 0.f : ex2(m - mt); // O of a row that has seen nothing is 0 (or not yet written)
+            m = mt;
+        }
+        if (c > 0 && __any_sync(0xffffffffu, f != 1.f)) {
+            const float fo = l == 0.f ? 1.f : f; // a row without a key so far has O = 0: nothing to scale
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                uint32_t o[32];
+                tmem_ld32(tO + 32u * g, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fo);
+                tmem_st32(tO + 32u * g, o);
+            }
+            tmem_st_wait();
+        }
+        const float sub = m == -INFINITY ? 0.f : -m;
+        const float2 sl2v = make_float2(sl2, sl2), subv = make_float2(sub, sub);
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            uint32_t p[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+                float2 z = fma2(make_float2(s[64 * g + 2 * e], s[64 * g + 2 * e + 1]), sl2v, subv);
+                z.x = ex2(z.x);
+                z.y = ex2(z.y);
+                sum[e & 1] = add2(sum[e & 1], z);
+                p[e] = pk_bf16(z.x, z.y);
+            }
+            tmem_st32(tS + 32u * g, p);
+        }
+        l = fmaf(l, f, (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y));
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(bar(B_P + t));
+    }
+    if (j.n[t] > 0) {
+        if (!__all_sync(0xffffffffu, mbar_wait(bar(B_O + t), 0))) return false;
+        tc_fence_after();
+    }
+    const float inv = l != 0.f ? 1.f / l : 0.f;
+    const int64_t row = (j.q0 + i) * a.H + j.h;
+    uint4 *out = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.o) + row * kDv);
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+        uint32_t o[32];
+        if (j.n[t] > 0) {
+            tmem_ld32(tO + 32u * g, o);
+            tmem_ld_wait();
+        }
+        if (i < j.nq) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                uint32_t w[4] = {0, 0, 0, 0};
+                if (l != 0.f) {
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        w[u] = pk_bf16(__uint_as_float(o[8 * e + 2 * u]) * inv, __uint_as_float(o[8 * e + 2 * u + 1]) * inv);
+                }
+                out[4 * g + e] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+    }
+    if (a.lse && i < j.nq) a.lse[row] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    tc_fence_before();
+    return true;
+}
+
+__global__ void __launch_bounds__(kThreads, 1) latent_prefill_tc_kernel(LatentPrefillArgs a, const __grid_constant__ Maps maps)
+{
+    extern __shared__ uint8_t smem_raw[];
+    Job j;
+    if (!find_job(a, j)) return; // no queries here (the same on every thread)
+    const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+    uint8_t *sp = smem_raw + (base - raw);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        for (int b = 0; b < NUM_BARS; ++b) mbar_init(base + OFF_BAR + 8u * (uint32_t)b, b == B_P || b == B_P + 1 ? 128u : 1u);
+        mbar_init_fence();
+    }
+    if (warp == kMmaWarp) tmem_alloc(base + OFF_TMEM, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(sp + OFF_TMEM);
+    bool ok = true;
+    if (warp < kTmaWarp) {
+        regs_inc<kRegsSoft>();
+        ok = softmax_role(a, j, base, tmem, warp, lane);
+    } else {
+        regs_dec<kRegsRest>();
+        if (warp == kTmaWarp) ok = tma_role(j, maps, base, lane);
+        else if (warp == kMmaWarp && lane == 0) ok = mma_role(j, base, tmem);
+    }
+    if (!ok) flag_error(a.err, CSA_DEVERR_TIMEOUT);
+    if (warp == kMmaWarp && lane == 0) { // every MMA completes before TMEM is released
+        mma_commit(base + OFF_BAR + 8u * B_FINAL);
+        if (!mbar_wait(base + OFF_BAR + 8u * B_FINAL, 0)) flag_error(a.err, CSA_DEVERR_TIMEOUT);
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+// A packed bf16 array [rows, heads, cols] read in boxes of 64 columns of one head x 128 rows with the
+// 128-byte swizzle; rows outside read as zeros.
+bool encode_heads(CUtensorMap *m, const void *base, int64_t rows, int heads, int cols)
+{
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tma::encoder();
+    if (!enc || rows <= 0) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)heads, (cuuint64_t)rows};
+    const cuuint64_t strides[2] = {(cuuint64_t)cols * 2, (cuuint64_t)cols * 2 * heads};
+    const cuuint32_t box[3] = {64, 1, kT}, estr[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+} // namespace
+
+bool latent_prefill_tc_eligible(const LatentPrefillArgs &a, int dtype)
+{
+    return dtype == CSA_BF16 && a.dn == kDn && a.dr == kDr && a.dv == kDv && a.Tk > 0;
+}
+
+cudaError_t launch_latent_prefill_tc(const LatentPrefillArgs &a, cudaStream_t st)
+{
+    Maps maps;
+    if (!encode_heads(&maps.q, a.q, a.Tq, a.H, kDn + kDr) || !encode_heads(&maps.kv, a.kv, a.Tk, a.H, kDn + kDv) ||
+        !tma::encode_bf16_rows(&maps.kr, a.k_rope, (uint64_t)a.Tk, kDr, kT))
+        return cudaErrorNotSupported;
+    cudaError_t e = cudaFuncSetAttribute(latent_prefill_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_ALLOC);
+    if (e != cudaSuccess) return e;
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, latent_prefill_tc_kernel);
+    if (e != cudaSuccess) return e;
+    if (fa.numRegs != kRegs) return cudaErrorInvalidConfiguration; // the register split would wait for ever
+    const int64_t blocks = a.B * a.H * ((a.max_q + 2 * kT - 1) / (2 * kT));
+    if (blocks >= ((int64_t)1 << 31)) return cudaErrorInvalidValue;
+    latent_prefill_tc_kernel<<<(unsigned)blocks, kThreads, SMEM_ALLOC, st>>>(a, maps);
+    return cudaGetLastError();
+}
+
+} // namespace csa

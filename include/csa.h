@@ -484,7 +484,8 @@ int latent_attn_decode(const void *q, const csa_kv_rows *rows, const int64_t *po
  *   it are not computed).  Rows of q outside the sequences get no output: o and lse keep what
  *   they held.  Rows of kv and k_rope outside a sequence are not part of its result whatever they
  *   hold; a non-finite value in a sequence's own rows may reach all of its outputs.
- * Limits: dn, dr, dv multiples of 16, dn + dr <= 256, dv <= 256, H <= 128, Tq and Tk < 2^31.
+ * Limits: dn, dr, dv multiples of 16, dn + dr <= 256, dv <= 256, H <= 128, Tq and Tk < 2^31,
+ * B * H * ceil(max_q / 32) < 2^31.
  * Errors: CSA_ERR_INVALID_ARG for a null q, cu_q, cu_k or o, a null kv or k_rope with Tk > 0, negative
  * sizes, H, dn, dr or dv < 1, a bad dtype, a non-finite scale, or q, kv, k_rope or o not 16-byte aligned;
  * CSA_ERR_UNSUPPORTED outside the limits.
@@ -514,6 +515,7 @@ int latent_attn_prefill(const void *q, const void *kv, const void *k_rope, const
 #define CSA_PATH_DECODE_GENERIC 7
 #define CSA_PATH_LATENT_DECODE_GENERIC 9   /* latent decode on the CUDA cores */
 #define CSA_PATH_LATENT_PREFILL_GENERIC 10 /* latent prefill on the CUDA cores */
+#define CSA_PATH_LATENT_PREFILL_TC 11      /* latent prefill, bf16, 128 + 64 / 128 channels: tcgen05 */
 #define CSA_PATH_PREFILL_KEYS_TC 8   /* bf16 64 x 512, W = 128, HCA: tcgen05 with keys on M (M = 128 MMAs) */
 int32_t csa_last_path(void);
 

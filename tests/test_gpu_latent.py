@@ -388,6 +388,8 @@ RAGGED = [([1], [1]), ([128], [128]), ([129, 0, 1, 127], [129, 0, 1, 127]), ([5,
 @pytest.mark.parametrize("H", [1, 5])
 def test_prefill(C, nq, nk, causal, H):
     run_prefill(C, nq, nk, H, (128, 64, 128), BF16, causal, seed=H)
+    if sum(nq):
+        assert C.csa_last_path() == C.CSA_PATH_LATENT_PREFILL_TC
 
 
 @pytest.mark.parametrize("dims,dtype", [((128, 64, 128), F32), ((16, 16, 16), BF16), ((64, 32, 96), F32), ((192, 64, 256), BF16)])
