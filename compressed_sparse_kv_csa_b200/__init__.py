@@ -629,6 +629,7 @@ CSA_PATH_PREFILL_KEYS_TC = 8
 CSA_PATH_LATENT_DECODE_GENERIC = 9
 CSA_PATH_LATENT_PREFILL_GENERIC = 10
 CSA_PATH_LATENT_PREFILL_TC = 11
+CSA_PATH_LATENT_DECODE_TC = 12
 
 
 def csa_set_wait_limit_ns(ns: int) -> int:

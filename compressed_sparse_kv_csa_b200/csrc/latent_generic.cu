@@ -294,6 +294,8 @@ template <int RB, int KT> static cudaError_t launch_merge(const LatentDecodeArgs
     return cudaGetLastError();
 }
 
+cudaError_t launch_latent_merge_32x64(const LatentDecodeArgs &a, cudaStream_t st) { return launch_merge<32, 64>(a, a.grid, 1.f, st); }
+
 cudaError_t launch_latent_decode_generic(LatentDecodeArgs a, cudaStream_t st)
 {
     const size_t smem = (size_t)(kKT * (a.rows.c + 1) + kRB * a.rows.c) * sizeof(float);

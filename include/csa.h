@@ -454,7 +454,9 @@ int latent_gather(const csa_kv_rows *rows, const int64_t *cu, const int64_t *sta
  * at position pos[b] + j and sees the positions s <= pos[b] + j, at most the first max_len (its own
  * row included: append first).  With key(s) = [lat(s), rope(s)] and z = scale * q . key(s):
  *   o[b,j,h,:] = sum_s e^z lat(s) / sum_s e^z,   lse[b,j,h] = ln sum_s e^z
- * and o = 0, lse = -inf for a token that sees nothing (pos[b] + j < 0: padding).
+ * and o = 0, lse = -inf for a token that sees nothing (pos[b] + j < 0: padding).  Rows that no token of
+ * the call sees are not part of the result whatever they hold; a non-finite value in a row that one
+ * of a sequence's tokens sees may reach all of the sequence's tokens.
  *   q [B, Lq, H, c] bf16;  o [B, Lq, H, R] bf16;  lse [B, Lq, H] fp32 or NULL;  pos [B] int64
  *   max_len  host-side bound of the positions (sizes the split)
  *   ws       workspace of latent_attn_decode_workspace_size(...) bytes, queried with the device
@@ -516,6 +518,7 @@ int latent_attn_prefill(const void *q, const void *kv, const void *k_rope, const
 #define CSA_PATH_LATENT_DECODE_GENERIC 9   /* latent decode on the CUDA cores */
 #define CSA_PATH_LATENT_PREFILL_GENERIC 10 /* latent prefill on the CUDA cores */
 #define CSA_PATH_LATENT_PREFILL_TC 11      /* latent prefill, bf16, 128 + 64 / 128 channels: tcgen05 */
+#define CSA_PATH_LATENT_DECODE_TC 12       /* latent decode, 512 + 64 channels: tcgen05, FP8 operands */
 #define CSA_PATH_PREFILL_KEYS_TC 8   /* bf16 64 x 512, W = 128, HCA: tcgen05 with keys on M (M = 128 MMAs) */
 int32_t csa_last_path(void);
 

@@ -35,13 +35,15 @@ def append_rows(x, pos, R, g=None, eps=1e-6, base=0.0):
     return u, v
 
 
-def attend(q, k, v, seen, scale):
+def attend(q, k, v, seen, scale, v_scale=None):
     """One head: q [n, d], k [m, d], v [m, e], seen [n, m].  Returns o, lse, and what the error bound
-    needs: sum p|v| / sum p and the largest scale * sum |q||k| of a seen key."""
+    needs: sum p|v| / sum p, the largest scale * sum |q||k| of a seen key and, with the values' row
+    scales, the largest p v_scale of a seen key times sum |v| / v_scale."""
     o = torch.zeros((len(q), v.shape[1]), dtype=F64)
     lse = torch.full((len(q),), -torch.inf, dtype=F64)
     size = torch.zeros_like(o)
     mag = torch.zeros_like(lse)
+    small = torch.zeros_like(o)
     for i in range(len(q)):
         at = seen[i].nonzero()[:, 0]
         if not len(at):
@@ -51,18 +53,24 @@ def attend(q, k, v, seen, scale):
         p = torch.exp(z - lse[i])
         o[i], size[i] = p @ v[at], p @ v[at].abs()
         mag[i] = (k[at].abs() @ q[i].abs()).max() * abs(scale)
-    return o, lse, size, mag
+        if v_scale is not None:
+            small[i] = (p * v_scale[at]).max() * (v[at].abs() / v_scale[at][:, None]).sum(0)
+    return o, lse, size, mag, small
 
 
 def check_attention(o, lse, ref, dk, n_keys, p_step, name=""):
     """Kernel outputs against attend()'s.  A score is a sum of dk products in fp32 (off by at most dk
     half steps of the sum of their magnitudes, and 8 more for the scale and log2 e), so a probability
     is off by twice that relative; its own rounding to p_step and the fp32 sum over n_keys come on top,
-    and the output's rounding at the end."""
-    ro, rl, size, mag = ref
+    and the output's rounding at the end.  `small` is not zero where the probabilities times the row
+    scales, w, are held as 8-bit floats in two terms: with M their largest, the unit that they are
+    held in is at most 2^-4.5 M (it is set so that the largest becomes 2^4.5 to 2^5.5, and only a larger one,
+    or one that would matter beside the sum, sets it again), and below 2^-6 units they are off by up to
+    2^-14 units, so each by at most 2^-18.5 M beyond p_step."""
+    ro, rl, size, mag, small = ref
     dz = (dk + 8) * 2.0 ** -24 * mag
     tau = 2 * dz + p_step + (n_keys + 8) * 2.0 ** -24 + 2.0 ** -20
-    tol = STEP[o.dtype] * ro.abs() + tau[..., None] * size * 1.01 + 1e-30
+    tol = STEP[o.dtype] * ro.abs() + (tau[..., None] * size + 2.0 ** -18.5 * small) * 1.01 + 1e-30
     got = o.cpu().to(F64)
     assert torch.isfinite(got).all(), name
     bad = (got - ro).abs() > tol
@@ -77,7 +85,7 @@ def check_attention(o, lse, ref, dk, n_keys, p_step, name=""):
         assert (err <= lim).all(), (name, float((err / lim).max()))
 
 
-def decode(q, lat, rope, rows_of, pos, scale, max_len):
+def decode(q, lat, rope, rows_of, pos, scale, max_len, v_scale=None):
     """attend() over every (sequence, token, head): rows_of(b, s) is the cache row or None."""
     B, Lq, H, c = q.shape
     key = torch.cat([lat, rope], 1)
@@ -90,7 +98,8 @@ def decode(q, lat, rope, rows_of, pos, scale, max_len):
         at = torch.tensor([r if r is not None and 0 <= r < len(key) else 0 for r in at], dtype=torch.long)
         s = torch.arange(n)
         seen = torch.stack([ok & (s <= int(pos[b]) + j) for j in range(Lq)])  # [Lq, n]
-        r = attend(q[b].reshape(Lq * H, c), key[at], lat[at], seen[:, None].expand(Lq, H, n).reshape(Lq * H, n), scale)
+        r = attend(q[b].reshape(Lq * H, c), key[at], lat[at], seen[:, None].expand(Lq, H, n).reshape(Lq * H, n), scale,
+                   None if v_scale is None else v_scale.cpu().to(F64)[at])
         out.append([t.reshape(Lq, H, *t.shape[1:]) for t in r])
     return [torch.stack(t) for t in zip(*out)]
 
@@ -107,5 +116,5 @@ def prefill(q, kv, k_rope, cu_q, cu_k, dn, scale, causal):
         seen = (j <= i + nk - nq) if causal else torch.ones((nq, nk), dtype=torch.bool)
         for h in range(H):
             key = torch.cat([kv[c:d, h, :dn], k_rope[c:d]], 1)
-            o[a:b, h], lse[a:b, h], size[a:b, h], mag[a:b, h] = attend(q[a:b, h], key, kv[c:d, h, dn:], seen, scale)
-    return o, lse, size, mag
+            o[a:b, h], lse[a:b, h], size[a:b, h], mag[a:b, h], _ = attend(q[a:b, h], key, kv[c:d, h, dn:], seen, scale)
+    return o, lse, size, mag, torch.zeros_like(o)

@@ -9,7 +9,7 @@ import _latent_ref as L
 
 pytestmark = pytest.mark.gpu
 BF16, F32, I64, I32 = torch.bfloat16, torch.float32, torch.int64, torch.int32
-F16_STEP = 2.0 ** -11  # half a step of the decode kernel's probabilities (fp16 on the tensor cores)
+V_STEP = 2.0 ** -8  # half a step of the decode kernel's probabilities: 8 bits in two terms of 4 (on the tensor cores)
 NAN8 = 0x7f            # the E4M3 code of NaN
 
 
@@ -225,8 +225,8 @@ def run_decode(C, lens, H, Lq, R, rd, page, seed=0, spread=0.3, scale=None, max_
     o = C.latent_attn_decode(q.cuda(), rows, pos, scale, max_len, lse=lse, **kw)
     assert C.csa_device_error() == 0
     lat, rope = L.dequant(rows.fp8, rows.rope, rows.scale)
-    ref = L.decode(q, lat, rope, of, pos.tolist(), scale, max_len)
-    L.check_attention(o, lse, ref, R + rd, m, F16_STEP, f"{lens} H{H} Lq{Lq} R{R} page{page}")
+    ref = L.decode(q, lat, rope, of, pos.tolist(), scale, max_len, rows.scale)
+    L.check_attention(o, lse, ref, R + rd, m, V_STEP, f"{lens} H{H} Lq{Lq} R{R} page{page}")
     return o, lse
 
 
@@ -237,6 +237,7 @@ LENS = [1, 63, 64, 65, 0, 200, 128]
 @pytest.mark.parametrize("H,Lq", [(1, 1), (16, 1), (20, 3), (64, 1), (128, 1), (128, 2)])
 def test_decode(C, page, H, Lq):
     run_decode(C, LENS if H * Lq < 128 else LENS[:4], H, Lq, 512, 64, page, seed=H + Lq)
+    assert C.csa_last_path() == C.CSA_PATH_LATENT_DECODE_TC
 
 
 @pytest.mark.parametrize("R,rd", [(32, 16), (128, 32), (256, 64), (512, 128), (480, 64)])
@@ -318,8 +319,8 @@ def test_decode_refused_pages_are_skipped(C, R):
     o = C.latent_attn_decode(q.cuda(), rows, pos, 0.05, 64, pages=pages, page_rows=page, lse=lse)
     assert C.csa_device_error() == C.CSA_DEVERR_INDEX
     lat, rope = L.dequant(rows.fp8, rows.rope, rows.scale)
-    ref = L.decode(q, lat, rope, lambda b, s: L.row_of(pages.cpu(), page, None, b, s), pos.tolist(), 0.05, 64)
-    L.check_attention(o, lse, ref, R + 64, 64, F16_STEP)
+    ref = L.decode(q, lat, rope, lambda b, s: L.row_of(pages.cpu(), page, None, b, s), pos.tolist(), 0.05, 64, rows.scale)
+    L.check_attention(o, lse, ref, R + 64, 64, V_STEP)
 
 
 def test_decode_positions_out_of_any_range(C):
@@ -329,8 +330,8 @@ def test_decode_positions_out_of_any_range(C):
     o = C.latent_attn_decode(q.cuda(), rows, pos, 0.05, 20, off=ints(0, 20, 40))
     assert C.csa_device_error() == 0
     lat, rope = L.dequant(rows.fp8, rows.rope, rows.scale)
-    ref = L.decode(q, lat, rope, lambda b, s: 20 * b + s, [-100, 100, 5], 0.05, 20)
-    L.check_attention(o, None, ref, 576, 20, F16_STEP)
+    ref = L.decode(q, lat, rope, lambda b, s: 20 * b + s, [-100, 100, 5], 0.05, 20, rows.scale)
+    L.check_attention(o, None, ref, 576, 20, V_STEP)
 
 
 def test_decode_rows_behind_four_gigabytes(C):

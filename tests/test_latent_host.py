@@ -137,8 +137,8 @@ def test_forms_agree():
     U, W = torch.randn((H, dn, R), generator=g, dtype=L.F64) / 8, torch.randn((H, dv, R), generator=g, dtype=L.F64) / 8
     q = torch.randn((n, H, dn + rd), generator=g, dtype=L.F64)
     kv = torch.cat([torch.einsum("hdr,nr->nhd", U, lat), torch.einsum("hdr,nr->nhd", W, lat)], 2)
-    o, lse, _, _ = L.prefill(q, kv, rope, [0, n], [0, n], dn, 0.2, True)
+    o, lse, *_ = L.prefill(q, kv, rope, [0, n], [0, n], dn, 0.2, True)
     qa = torch.cat([torch.einsum("nhd,hdr->nhr", q[..., :dn], U), q[..., dn:]], 2)[None]  # Lq = n tokens from position 0
-    oa, la, _, _ = L.decode(qa, lat, rope, lambda b, s: s, [0], 0.2, n)
+    oa, la, *_ = L.decode(qa, lat, rope, lambda b, s: s, [0], 0.2, n)
     torch.testing.assert_close(torch.einsum("hdr,nhr->nhd", W, oa[0]), o, rtol=1e-10, atol=1e-10)
     torch.testing.assert_close(la[0], lse, rtol=1e-10, atol=1e-10)
