@@ -131,11 +131,11 @@ struct LatentRun {
 cudaError_t launch_latent_decode_generic(LatentDecodeArgs a, cudaStream_t st);
 size_t latent_decode_generic_workspace(int64_t B, int Lq, int H, int R, int64_t max_len, int *grid);
 
-// 512 + 64 channels on the tensor cores (blocks of 32 rows, tiles of 64 keys).
+// 512 + 64 channels on the tensor cores (blocks of 32 rows, tiles of 128 keys).
 bool latent_decode_tc_eligible(int R, int rd);
 size_t latent_decode_tc_workspace(int64_t B, int Lq, int H, int64_t max_len, int *grid);
 cudaError_t launch_latent_decode_tc(const LatentDecodeArgs &a, cudaStream_t st);
-cudaError_t launch_latent_merge_32x64(const LatentDecodeArgs &a, cudaStream_t st);
+cudaError_t launch_latent_merge_32x128(const LatentDecodeArgs &a, cudaStream_t st);
 
 struct LatentPrefillArgs {
     const void *q, *kv, *k_rope; // [Tq, H, dn + dr], [Tk, H, dn + dv], [Tk, dr]

@@ -148,64 +148,77 @@ __global__ void __launch_bounds__(32 * kWarps) latent_decode_generic_kernel(Late
 // Merge of the parts of a run that the split cut: one CTA per query row.  With part i holding the
 // maximum m_i (log2 domain), the sum l_i and the unnormalised output O_i, the run's are
 // m = max m_i, l = sum 2^(m_i - m) l_i, O = sum 2^(m_i - m) O_i; the output is O / l.
-template <int RB, int KT>
-__global__ void __launch_bounds__(128) latent_merge_kernel(LatentDecodeArgs a, int64_t G, float o_factor)
+constexpr int kMaxParts = 512;
+
+template <int RB, int KT> __global__ void __launch_bounds__(128) latent_merge_kernel(LatentDecodeArgs a, int64_t G)
 {
-    __shared__ int64_t s_at[3];
-    const int lane = threadIdx.x & 31;
+    __shared__ int64_t s_at[2];
+    __shared__ float red[4], weight[kMaxParts];
+    const int tid = threadIdx.x, lane = tid & 31;
     const int64_t rows = (int64_t)a.Lq * a.H, b = blockIdx.x / rows;
     const int r = (int)(blockIdx.x % rows), rb = r / RB;
     const int R = a.rows.c - a.rows.rope_dims;
     using Split = LatentSplit<RB, KT>;
     const int64_t nrb = Split::row_blocks(a.Lq, a.H);
-    if (threadIdx.x < 32) {
-        const int64_t before = Split::warp_total(a, 0, b, lane), after = Split::warp_total(a, b, a.B, lane);
-        if (lane == 0) s_at[0] = before * nrb, s_at[1] = (before + after) * nrb;
+    if (tid < 64) { // tiles before this sequence (warp 0), from it on (warp 1)
+        const int64_t s = tid < 32 ? Split::warp_total(a, 0, b, lane) : Split::warp_total(a, b, a.B, lane);
+        if (lane == 0) s_at[tid >> 5] = s * nrb;
     }
     __syncthreads();
-    const int64_t tiles = Split::tiles(a, b), T = s_at[1], s0 = s_at[0] + rb * tiles, s1 = s0 + tiles;
-    // the CTAs that hold tiles s0 and s1 - 1: the largest i with i T / G <= tile
-    int64_t i0 = (s0 * G + G - 1) / T, i1 = ((s1 - 1) * G + G - 1) / T;
-    while (i0 > 0 && T * i0 / G > s0) --i0;
-    while (i0 + 1 < G && T * (i0 + 1) / G <= s0) ++i0;
-    while (i1 > 0 && T * i1 / G > s1 - 1) --i1;
-    while (i1 + 1 < G && T * (i1 + 1) / G <= s1 - 1) ++i1;
+    const int64_t tiles = Split::tiles(a, b), T = s_at[0] + s_at[1], s0 = s_at[0] + rb * tiles, s1 = s0 + tiles - 1;
+    // the CTAs that hold the run's first and last tile: the largest i with floor(i T / G) <= tile
+    const int64_t i0 = ((s0 + 1) * G - 1) / T, i1 = ((s1 + 1) * G - 1) / T;
     if (i0 == i1) return; // finished by the CTA that holds it
     const int64_t ld = R + 4;
-    auto part = [&](int64_t i) { return a.part + ((2 * i + (i == i0 ? 1 : 0)) * RB + (r % RB)) * ld; };
-    float m = -INFINITY;
-    for (int64_t i = i0; i <= i1; ++i)
-        if (T * i / G < T * (i + 1) / G) m = fmaxf(m, part(i)[0]);
-    float l = 0.f;
-    float4 acc[4];
+    const int n = (int)(i1 - i0 + 1);
+    // part k: slot 2 i + 1 where the run begins, slot 2 i behind; a CTA without tiles has none
+    const float *first = a.part + ((2 * i0 + 1) * RB + (r % RB)) * ld, *rest = a.part + (2 * i0 * RB + (r % RB)) * ld;
+    auto part = [&](int k) { return k == 0 ? first : rest + (int64_t)k * 2 * RB * ld; };
+    float m = -INFINITY, ml[kMaxParts / 128][2];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (m > -INFINITY)
-        for (int64_t i = i0; i <= i1; ++i) {
-            if (T * i / G >= T * (i + 1) / G) continue; // a CTA without tiles has no part
-            const float *p = part(i);
-            const float f = exp2f(p[0] - m);
-            l = fmaf(f, p[1], l);
-            if (f == 0.f) continue;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int j = 4 * (threadIdx.x + 128 * k);
-                if (j < R) {
-                    const float4 v = *reinterpret_cast<const float4 *>(p + 4 + j);
-                    acc[k].x = fmaf(f, v.x, acc[k].x);
-                    acc[k].y = fmaf(f, v.y, acc[k].y);
-                    acc[k].z = fmaf(f, v.z, acc[k].z);
-                    acc[k].w = fmaf(f, v.w, acc[k].w);
-                }
-            }
+    for (int u = 0; u < kMaxParts / 128; ++u) {
+        const int k = tid + 128 * u;
+        ml[u][0] = -INFINITY, ml[u][1] = 0.f;
+        if (k < n && T * (i0 + k) / G < T * (i0 + k + 1) / G) {
+            const float2 v = *reinterpret_cast<const float2 *>(part(k));
+            ml[u][0] = v.x, ml[u][1] = v.y;
+            m = fmaxf(m, v.x);
         }
-    const float inv = l != 0.f ? o_factor / l : 0.f;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const int j = 4 * (threadIdx.x + 128 * k);
-        if (j < R) st4(a.o, (int64_t)blockIdx.x * R + j, make_float4(acc[k].x * inv, acc[k].y * inv, acc[k].z * inv, acc[k].w * inv));
     }
-    if (a.lse && threadIdx.x == 0) a.lse[blockIdx.x] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    m = warp_max(m);
+    if (lane == 0) red[tid >> 5] = m;
+    __syncthreads();
+    m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+    float l = 0.f;
+#pragma unroll
+    for (int u = 0; u < kMaxParts / 128; ++u) {
+        const int k = tid + 128 * u;
+        if (k >= n) break;
+        const float w = ml[u][0] == -INFINITY ? 0.f : exp2f(ml[u][0] - m);
+        weight[k] = w;
+        l = fmaf(w, ml[u][1], l);
+    }
+    l = warp_sum(l);
+    __syncthreads();
+    if (lane == 0) red[tid >> 5] = l;
+    __syncthreads();
+    l = (red[0] + red[1]) + (red[2] + red[3]);
+    const float inv = l != 0.f ? 1.f / l : 0.f;
+    for (int j = 4 * tid; j < R; j += 512) {
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int k = 0; k < n; ++k) {
+            const float w = weight[k];
+            if (w == 0.f) continue; // nothing was seen there, or nothing was written
+            const float4 v = __ldcs(reinterpret_cast<const float4 *>(part(k) + 4 + j));
+            acc.x = fmaf(w, v.x, acc.x);
+            acc.y = fmaf(w, v.y, acc.y);
+            acc.z = fmaf(w, v.z, acc.z);
+            acc.w = fmaf(w, v.w, acc.w);
+        }
+        st4(a.o, (int64_t)blockIdx.x * R + j, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+    }
+    if (a.lse && tid == 0) a.lse[blockIdx.x] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
 }
 
 // ---- expanded form -------------------------------------------------------------------------
@@ -287,14 +300,15 @@ size_t latent_decode_generic_workspace(int64_t B, int Lq, int H, int R, int64_t 
     return (size_t)*grid * 2 * kRB * (R + 4) * sizeof(float);
 }
 
-template <int RB, int KT> static cudaError_t launch_merge(const LatentDecodeArgs &a, int grid, float o_factor, cudaStream_t st)
+template <int RB, int KT> static cudaError_t launch_merge(const LatentDecodeArgs &a, int grid, cudaStream_t st)
 {
     if (grid < 2) return cudaSuccess; // one CTA cuts no run
-    latent_merge_kernel<RB, KT><<<(unsigned)(a.B * a.Lq * a.H), 128, 0, st>>>(a, grid, o_factor);
+    if (grid > kMaxParts) return cudaErrorInvalidValue;
+    latent_merge_kernel<RB, KT><<<(unsigned)(a.B * a.Lq * a.H), 128, 0, st>>>(a, grid);
     return cudaGetLastError();
 }
 
-cudaError_t launch_latent_merge_32x64(const LatentDecodeArgs &a, cudaStream_t st) { return launch_merge<32, 64>(a, a.grid, 1.f, st); }
+cudaError_t launch_latent_merge_32x128(const LatentDecodeArgs &a, cudaStream_t st) { return launch_merge<32, 128>(a, a.grid, st); }
 
 cudaError_t launch_latent_decode_generic(LatentDecodeArgs a, cudaStream_t st)
 {
@@ -304,7 +318,7 @@ cudaError_t launch_latent_decode_generic(LatentDecodeArgs a, cudaStream_t st)
     latent_decode_generic_kernel<<<(unsigned)a.grid, 32 * kWarps, smem, st>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_merge<kRB, kKT>(a, a.grid, 1.f, st);
+    return launch_merge<kRB, kKT>(a, a.grid, st);
 }
 
 template <typename T> static cudaError_t prefill_generic(const LatentPrefillArgs &a, cudaStream_t st)
