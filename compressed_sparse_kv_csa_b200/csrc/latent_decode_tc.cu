@@ -15,18 +15,22 @@
 // still to come could matter beside what has been summed: behind a key that outweighs all others the
 // reference comes down again, and the many small ones keep their 8 bits.
 //
-// A work item's rows are 32 (head, token) pairs, stacked to the 64 rows of a weight-stationary MMA
-// (tcgen05.mma.ws), rows 32 g + 16 part + r with part 0 = hi, 1 = lo: one pass over the keys serves both
-// terms, and hi and lo of a score lie in lanes l and l + 16 of one warp.  M = 64 with .ws spreads the
-// accumulator's column halves over all 128 lanes and reads 10 KB of shared memory for N = 256 in 80
-// cycles (3273 multiply-adds a cycle at 16 bits, measured; without .ws 128 cycles, 2045).
-// Per tile of 128 keys: S_n (N = 128, K = 512, FP8), S_r (N = 128, K = 64, BF16), O (+)= v code (two N = 256,
-// K = 128, FP8, the codes read MN-major): 28 MMAs.
+// A work item's rows are 32 (head, token) pairs.  All MMAs are weight-stationary (tcgen05.mma.ws), which spread
+// a small accumulator over all 128 lanes and are bound by what they read of shared memory, 128 bytes a cycle
+// (M = 64, N = 256 at 16 bits: 80 cycles, measured; without .ws 128).  Per tile of 128 keys
+//   S_n (M = 32, N = 128, K = 512, FP8), once for hi and once for lo of q into the same accumulator,
+//   S_r (M = 32, N = 128, K = 64, BF16),
+//   O (+)= v code (M = 64: hi and lo rows of v; two N = 256, K = 128; the codes read MN-major): 44 MMAs, 2,280
+// cycles.  S has row l of the block in lane l of every warp, so a score needs no exchange; one exchange a
+// tile, of the rows' largest v, lets the eight softmax warps decide alike whether a reference moves.
 //
-// Roles: warps 0-7 softmax and output, warps 8-9 copy the keys (cp.async, 16 bytes a lane, any page
-// size; rows that are not to be seen arrive as zeros), warp 10 MMA.  Two stages of 80 KB.  Bound by HBM for up to 32 query rows a key.
+// Roles: warps 0-7 softmax and output; warp 8 copies the keys by TMA, in boxes of a page or of 128 rows (with
+// pages that no box fits, warps 8 and 9 by cp.async); warp 10 MMA.  Two stages of 80 KB.  Rows that are not to
+// be seen are zeros in shared memory: the probability 0 times whatever they held would not be 0.
+// Bound by HBM for up to 32 query rows a key, by the chain load - S - softmax - O over two stages above.
 #include "latent.cuh"
 #include "tc_common.cuh"
+#include "tma_host.cuh"
 
 namespace csa {
 
@@ -36,25 +40,25 @@ using namespace tc;
 
 constexpr int kR = 512, kRd = 64, kRB = 32, kKT = 128, kStages = 2;
 constexpr int kSoftThreads = 256, kProdWarp0 = 8, kMmaWarp = 10, kThreads = 11 * 32;
-// operand tiles of 128-byte rows, 128-byte swizzle: 64 query rows, 128 keys
-constexpr uint32_t kQSlice = 8192, kSlice = 16384;
-constexpr uint32_t OFF_Q = 0;                         // 4 slices of 128 latent channels, 1 of the rotated ones
-constexpr uint32_t OFF_P = 5 * kQSlice;               // v: two buffers
-constexpr uint32_t OFF_K = 7 * kQSlice;               // kStages x 5 slices
-constexpr uint32_t OFF_SC = OFF_K + kStages * 5 * kSlice;
-constexpr uint32_t OFF_XCH = OFF_SC + kStages * kKT * 4;     // [2 buffers][4 key quarters][32 rows] float2
-constexpr uint32_t OFF_BAR = OFF_XCH + 2 * 4 * 32 * 8;
+// operand tiles of 128-byte rows, 128-byte swizzle: 32 query rows, 64 rows of v, 128 keys
+constexpr uint32_t kQSlice = 4096, kPTile = 8192, kSlice = 16384;
+constexpr uint32_t OFF_P = 0;                         // v: two buffers (and the exchange of a run's output)
+constexpr uint32_t OFF_K = 2 * kPTile;                // kStages x 5 slices: 4 of 128 latent channels, 1 of the rotated ones
+constexpr uint32_t OFF_Q = OFF_K + kStages * 5 * kSlice; // 4 slices hi, 4 slices lo, 1 of the rotated channels
+constexpr uint32_t OFF_SC = OFF_Q + 9 * kQSlice;
+constexpr uint32_t OFF_XCH = OFF_SC + kStages * kKT * 4;     // [2 buffers][8 warps][32 rows]
+constexpr uint32_t OFF_BAR = OFF_XCH + 2 * 8 * 32 * 4;
 constexpr uint32_t OFF_AT = OFF_BAR + 160;            // where the CTA's walk begins (3 x int64)
 constexpr uint32_t OFF_TMEM = OFF_AT + 32;
 constexpr uint32_t SMEM_ALLOC = OFF_TMEM + 64 + 1024;
 static_assert(SMEM_ALLOC <= 232448, "shared memory per block");
-enum { B_KFULL = 0, B_KEMPTY = B_KFULL + kStages, B_S = B_KEMPTY + kStages, B_P = B_S + 2, B_Q = B_P + 2, B_ALL, B_ROWS, B_FINAL = B_ROWS + 2, NUM_BARS };
+enum { B_KFULL = 0, B_KEMPTY = B_KFULL + kStages, B_S = B_KEMPTY + kStages, B_P = B_S + 2, B_Q = B_P + 2, B_ALL, B_TAIL, B_FINAL, NUM_BARS };
 static_assert(8 * NUM_BARS <= 160, "barrier space");
-// TMEM columns: O (two N = 256 accumulators, 128 columns each), S_n and S_r (two buffers of 64 each)
-constexpr uint32_t kColO = 0, kColSn = 256, kColSr = 384, kTmemCols = 512;
-constexpr uint32_t IDESC_SN = (1u << 4) | ((uint32_t)(kKT >> 3) << 17) | (4u << 24);                              // E4M3 x E4M3
-constexpr uint32_t IDESC_SR = idesc_bf16_f32(64, kKT, false, false);
-constexpr uint32_t IDESC_O = (1u << 4) | (1u << 16) | ((uint32_t)(256 >> 3) << 17) | (4u << 24); // B MN-major
+// TMEM columns: O (two N = 256 accumulators, 128 columns each), S_n and S_r (two buffers of 32 each)
+constexpr uint32_t kColO = 0, kColSn = 256, kColSr = 320, kTmemCols = 512;
+constexpr uint32_t IDESC_SN = (1u << 4) | ((uint32_t)(kKT >> 3) << 17) | (2u << 24); // M = 32, E4M3 x E4M3
+constexpr uint32_t IDESC_SR = idesc_bf16_f32(32, kKT, false, false);
+constexpr uint32_t IDESC_O = (1u << 4) | (1u << 16) | ((uint32_t)(256 >> 3) << 17) | (4u << 24); // M = 64, B MN-major
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr uint32_t kNoKey = 0xffffffffu; // in place of a row's scale: the key is not to be seen
 constexpr float kTop = 448.f, kLow = 1.f / 16.f, kSmallestScale = 7.8886090522101181e-31f; // 2^-100
@@ -104,18 +108,18 @@ __device__ __forceinline__ float2 e4m3x2_value(uint32_t c)
 }
 
 // 16 values as hi and lo * lo_scale, 16 E4M3 codes each.
-__device__ __forceinline__ void split16(const float (&v)[16], float lo_scale, uint32_t (&hi)[4], uint32_t (&lo)[4])
+__device__ __forceinline__ void split16(const float2 (&v)[8], float lo_scale, uint32_t (&hi)[4], uint32_t (&lo)[4])
 {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         hi[i] = lo[i] = 0;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const float a = v[4 * i + 2 * h], b = v[4 * i + 2 * h + 1];
-            const uint32_t c = e4m3x2(a, b);
+            const float2 a = v[2 * i + h];
+            const uint32_t c = e4m3x2(a.x, a.y);
             const float2 x = e4m3x2_value(c);
             hi[i] |= c << (16 * h);
-            lo[i] |= e4m3x2((a - x.x) * lo_scale, (b - x.y) * lo_scale) << (16 * h);
+            lo[i] |= e4m3x2((a.x - x.x) * lo_scale, (a.y - x.y) * lo_scale) << (16 * h);
         }
     }
 }
@@ -148,11 +152,104 @@ struct Ctx {
     __device__ __forceinline__ uint32_t stage(uint32_t n) const { return base + OFF_K + (n % kStages) * 5u * kSlice; }
 };
 
-// Keys (warps 8-9): warp w copies rows 64 w .. 64 w + 63 of a tile, 8 lanes a row of 128 bytes.
-__device__ __forceinline__ bool producer_role(const LatentDecodeArgs &a, const Ctx &c, Walk walk, int warp, int lane)
+struct Maps {
+    CUtensorMap lat, rope;
+    int box; // rows of a box; 0: copied by cp.async
+};
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, uint32_t bytes) // 16 bytes, or zeros
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+// The scale of key row r of a stage; kNoKey where there is none.
+__device__ __forceinline__ void copy_scale(const LatentDecodeArgs &a, uint32_t dst, int64_t row)
+{
+    if (row < 0) asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst), "r"(kNoKey) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(a.rows.scale + row) : "memory");
+}
+
+// Keys by TMA (warp 8).  A box is a page, or 128 rows of a larger page or of a contiguous run.
+__device__ __forceinline__ bool tma_role(const LatentDecodeArgs &a, const Maps &M, const Ctx &c, Walk walk, int lane)
 {
     LatentRun run;
-    uint32_t n = 0; // tiles so far
+    uint32_t n = 0, tails = 0; // tiles so far, those with rows that are not to be seen
+    bool ok = true;
+    const int boxes = kKT / M.box;
+    while (ok && walk.next(a, run)) {
+        const int64_t seen = latent_visible(a, run.b, a.Lq - 1);
+        auto resolve = [&](int64_t t, int64_t (&row)[4]) { // keys 32 k + lane of a tile
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int64_t s = t * kKT + 32 * k + lane;
+                row[k] = s < seen ? a.map.row(run.b, s) : -1;
+                if (s < seen && row[k] < 0) flag_error(a.err, CSA_DEVERR_INDEX);
+            }
+        };
+        int64_t ahead[4];
+        resolve(run.t0, ahead);
+        for (int64_t t = run.t0; t < run.t1; ++t, ++n) {
+            int64_t row[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) row[k] = ahead[k];
+            if (t + 1 < run.t1) resolve(t + 1, ahead); // page lookups beside this tile's copies
+            if (n >= kStages && !__all_sync(0xffffffffu, mbar_wait(c.bar(B_KEMPTY + n % kStages), ((n / kStages) & 1) ^ 1))) {
+                ok = false;
+                break;
+            }
+            const uint32_t st = c.stage(n), full = c.bar(B_KFULL + n % kStages);
+            const bool tail = __any_sync(0xffffffffu, row[0] < 0 || row[1] < 0 || row[2] < 0 || row[3] < 0);
+            const uint32_t bar = tail ? c.bar(B_TAIL) : full;
+            // box i begins at key i * box: lane (i * box) % 32, k = i * box / 32
+            uint32_t bytes = 0;
+            for (int i = 0; i < boxes; ++i) {
+                const int j = i * M.box, k = j >> 5;
+                const int64_t mine = k == 0 ? row[0] : k == 1 ? row[1] : k == 2 ? row[2] : row[3];
+                if (__shfl_sync(0xffffffffu, mine, j & 31) >= 0) bytes += (uint32_t)M.box * 640u;
+            }
+            if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+            __syncwarp();
+            for (int i = 0; i < boxes; ++i) {
+                const int j = i * M.box, k = j >> 5;
+                const int64_t mine = k == 0 ? row[0] : k == 1 ? row[1] : k == 2 ? row[2] : row[3];
+                const int64_t first = __shfl_sync(0xffffffffu, mine, j & 31);
+                if (first >= 0 && lane < 5) {
+                    const uint32_t dst = st + (uint32_t)lane * kSlice + (uint32_t)j * 128u;
+                    if (lane < 4) tma_load_2d(dst, &M.lat, 128 * lane, (int32_t)first, bar);
+                    else tma_load_2d(dst, &M.rope, 0, (int32_t)first, bar);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                copy_scale(a, c.base + OFF_SC + (n % kStages) * kKT * 4 + 4u * (uint32_t)(32 * k + lane), row[k]);
+            if (tail) { // rows that are not to be seen: zeros, written once no box is on its way
+                if (!__all_sync(0xffffffffu, mbar_wait(bar, tails & 1))) {
+                    ok = false;
+                    break;
+                }
+                ++tails;
+                const uint32_t zero = 0;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (row[k] < 0)
+                        for (int e = 0; e < 5 * 8; ++e)
+                            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(st + (uint32_t)(e >> 3) * kSlice + (uint32_t)(32 * k + lane) * 128u + 16u * (e & 7)), "r"(zero) : "memory");
+                fence_proxy_async_smem();
+                if (lane == 0) mbar_arrive(full);
+            }
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full) : "memory"); // for the scales
+            mbar_arrive(full);                                                                           // and the plain stores
+        }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory"); // nothing is in flight when the block ends
+    return ok;
+}
+
+// Keys by cp.async (warps 8-9): warp w copies rows 64 w .. 64 w + 63 of a tile, 8 lanes a row of 128 bytes.
+__device__ __forceinline__ bool copy_role(const LatentDecodeArgs &a, const Ctx &c, Walk walk, int warp, int lane)
+{
+    LatentRun run;
+    uint32_t n = 0;
     bool ok = true;
     while (ok && walk.next(a, run)) {
         const int64_t seen = latent_visible(a, run.b, a.Lq - 1);
@@ -166,12 +263,12 @@ __device__ __forceinline__ bool producer_role(const LatentDecodeArgs &a, const C
         int64_t mine[2] = {resolve(run.t0, 0), resolve(run.t0, 1)};
         for (int64_t t = run.t0; t < run.t1; ++t, ++n) {
             const int64_t cur[2] = {mine[0], mine[1]};
-            if (t + 1 < run.t1) mine[0] = resolve(t + 1, 0), mine[1] = resolve(t + 1, 1); // page lookups beside this tile's copies
+            if (t + 1 < run.t1) mine[0] = resolve(t + 1, 0), mine[1] = resolve(t + 1, 1);
             if (n >= kStages && !__all_sync(0xffffffffu, mbar_wait(c.bar(B_KEMPTY + n % kStages), ((n / kStages) & 1) ^ 1))) {
                 ok = false;
                 break;
             }
-            const uint32_t st = c.stage(n), sc = c.base + OFF_SC + (n % kStages) * kKT * 4;
+            const uint32_t st = c.stage(n);
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 const int r = 64 * warp + 4 * i + (lane >> 3);
@@ -180,17 +277,12 @@ __device__ __forceinline__ bool producer_role(const LatentDecodeArgs &a, const C
                 const uint32_t bytes = row < 0 ? 0u : 16u, dst = st + sw128((uint32_t)r, 16u * (uint32_t)(lane & 7));
                 const uint8_t *f8 = a.rows.fp8 + src * kR + 16 * (lane & 7);
 #pragma unroll
-                for (int s = 0; s < 4; ++s)
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + (uint32_t)s * kSlice), "l"(f8 + 128 * s), "r"(bytes)
-                                 : "memory");
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + 4 * kSlice),
-                             "l"(a.rows.rope + src * kRd + 8 * (lane & 7)), "r"(bytes)
-                             : "memory");
-                if ((lane & 7) == 0) {
-                    if (row < 0) asm volatile("st.shared.u32 [%0], %1;" ::"r"(sc + 4u * (uint32_t)r), "r"(kNoKey) : "memory");
-                    else asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(sc + 4u * (uint32_t)r), "l"(a.rows.scale + row) : "memory");
-                }
+                for (int s = 0; s < 4; ++s) copy16(dst + (uint32_t)s * kSlice, f8 + 128 * s, bytes);
+                copy16(dst + 4 * kSlice, a.rows.rope + src * kRd + 8 * (lane & 7), bytes);
             }
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                copy_scale(a, c.base + OFF_SC + (n % kStages) * kKT * 4 + 4u * (uint32_t)(64 * warp + 32 * h + lane), cur[h]);
             asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(c.bar(B_KFULL + n % kStages)) : "memory");
             mbar_arrive(c.bar(B_KFULL + n % kStages)); // and for the plain stores
         }
@@ -226,7 +318,7 @@ __device__ __forceinline__ bool mma_role(const LatentDecodeArgs &a, const Ctx &c
         for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                mma_ws<true>(c.tmem + kColO + 128u * h, sdesc_sw128(c.base + OFF_P + kQSlice * (k & 1) + 32u * kk, 16, 1024),
+                mma_ws<true>(c.tmem + kColO + 128u * h, sdesc_sw128(c.base + OFF_P + kPTile * (k & 1) + 32u * kk, 16, 1024),
                              sdesc_sw128(st + 2u * h * kSlice + 4096u * kk, kSlice, 1024), IDESC_O, !first || kk > 0);
         mma_commit(c.bar(B_KEMPTY + k % kStages));
         return true;
@@ -247,18 +339,18 @@ __device__ __forceinline__ bool mma_role(const LatentDecodeArgs &a, const Ctx &c
                 pending = false;
             }
             if (!mbar_wait(full, full_ph)) return false;
-            fence_proxy_async_smem(); // the copies were the generic proxy's
+            fence_proxy_async_smem(); // cp.async writes for the generic proxy
             tc_fence_after();
             const uint32_t st = c.stage(n);
 #pragma unroll
-            for (int s = 0; s < 4; ++s)
+            for (int s = 0; s < 8; ++s) // hi of q, then lo
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    mma_ws<true>(c.tmem + kColSn + 64u * (n & 1), sdesc_sw128(c.base + OFF_Q + s * kQSlice + 32u * kk, 16, 1024),
-                                 sdesc_sw128(st + s * kSlice + 32u * kk, 16, 1024), IDESC_SN, (s | kk) != 0);
+                    mma_ws<true>(c.tmem + kColSn + 32u * (n & 1), sdesc_sw128(c.base + OFF_Q + s * kQSlice + 32u * kk, 16, 1024),
+                                 sdesc_sw128(st + (s & 3) * kSlice + 32u * kk, 16, 1024), IDESC_SN, (s | kk) != 0);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-                mma_ws<false>(c.tmem + kColSr + 64u * (n & 1), sdesc_sw128(c.base + OFF_Q + 4 * kQSlice + 32u * kk, 16, 1024),
+                mma_ws<false>(c.tmem + kColSr + 32u * (n & 1), sdesc_sw128(c.base + OFF_Q + 8 * kQSlice + 32u * kk, 16, 1024),
                               sdesc_sw128(st + 4 * kSlice + 32u * kk, 16, 1024), IDESC_SR, kk != 0);
             mma_commit(c.bar(B_S + (n & 1)));
             if (pending && !output(n - 1, pending_first)) return false;
@@ -281,8 +373,7 @@ struct Meet {
     }
 };
 
-// Queries of a run into shared memory, as hi and lo rows; *factor is the factor that takes a score of this lane's
-// row (16 (warp & 1) + (lane & 15)) to the log2 domain.
+// Queries of a run into shared memory, as hi and lo; *factor takes a score of this lane's row to the log2 domain.
 __device__ __forceinline__ bool load_queries(const LatentDecodeArgs &a, const Ctx &c, const LatentRun &run, int warp, int lane,
                                              Meet &all, float *factor)
 {
@@ -305,22 +396,20 @@ __device__ __forceinline__ bool load_queries(const LatentDecodeArgs &a, const Ct
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = 4 * warp + i;
-        float x[16];
+        float2 x[8];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const uint32_t y[4] = {u[i][h].x, u[i][h].y, u[i][h].z, u[i][h].w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                x[8 * h + 2 * e] = __uint_as_float(y[e] << 16);
-                x[8 * h + 2 * e + 1] = __uint_as_float(y[e] & 0xffff0000u);
-            }
+            for (int e = 0; e < 4; ++e) x[4 * h + e] = make_float2(__uint_as_float(y[e] << 16), __uint_as_float(y[e] & 0xffff0000u));
         }
         float am = 0.f;
         bool finite = true;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            am = fmaxf(am, fabsf(x[e]));
-            finite = finite && fabsf(x[e]) < INFINITY;
+        for (int e = 0; e < 8; ++e) {
+            const float y = fmaxf(fabsf(x[e].x), fabsf(x[e].y));
+            am = fmaxf(am, y);
+            finite = finite && fabsf(x[e].x) < INFINITY && fabsf(x[e].y) < INFINITY;
         }
         const float rx = __uint_as_float(w[i] << 16), ry = __uint_as_float(w[i] & 0xffff0000u);
         am = warp_max(am);
@@ -332,128 +421,177 @@ __device__ __forceinline__ bool load_queries(const LatentDecodeArgs &a, const Ct
         if (ar < INFINITY) k = min(k, 100 - er);
         const float up = exp2i(k);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] *= up;
+        for (int e = 0; e < 8; ++e) x[e].x *= up, x[e].y *= up;
         uint32_t hi[4], lo[4];
         split16(x, 1.f, hi, lo);
-        const uint32_t row = 32u * (uint32_t)(r >> 4) + (uint32_t)(r & 15);
+        const uint32_t row = (uint32_t)r;
         // lane holds channels 16 lane .. 16 lane + 15: byte 16 (lane & 7) of slice lane / 8
         sts4(c.base + OFF_Q + (uint32_t)(lane >> 3) * kQSlice + sw128(row, 16u * (uint32_t)(lane & 7)), hi);
-        sts4(c.base + OFF_Q + (uint32_t)(lane >> 3) * kQSlice + sw128(row + 16, 16u * (uint32_t)(lane & 7)), lo);
+        sts4(c.base + OFF_Q + (uint32_t)(lane >> 3) * kQSlice + sw128(row, 16u * (uint32_t)(lane & 7)) + 4 * kQSlice, lo);
         const uint32_t rr = uint32_t(f32_to_bf16_bits(rx * up)) | (uint32_t(f32_to_bf16_bits(ry * up)) << 16);
-        asm volatile("st.shared.u32 [%0], %1;" ::"r"(c.base + OFF_Q + 4 * kQSlice + sw128(row, 4u * (uint32_t)lane)), "r"(rr) : "memory");
-        asm volatile("st.shared.u32 [%0], %1;" ::"r"(c.base + OFF_Q + 4 * kQSlice + sw128(row + 16, 4u * (uint32_t)lane)), "r"(0) : "memory");
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(c.base + OFF_Q + 8 * kQSlice + sw128(row, 4u * (uint32_t)lane)), "r"(rr) : "memory");
         // a row that is not finite makes NaN of its scores
         const float f = finite ? a.scale * kLog2e * exp2i(-k) : NAN;
         if (lane == 0) asm volatile("st.shared.f32 [%0], %1;" ::"r"(c.base + OFF_XCH + 4u * (uint32_t)r), "f"(f) : "memory");
     }
     fence_proxy_async_smem();
     if (!all.sync()) return false;
-    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(*factor) : "r"(c.base + OFF_XCH + 4u * (uint32_t)(16 * (warp & 1) + (lane & 15))) : "memory");
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(*factor) : "r"(c.base + OFF_XCH + 4u * (uint32_t)lane) : "memory");
     return all.sync(); // the factors are read before the place is used again
 }
 
-// Softmax and output (warps 0-7).  Warp w has rows 16 g .. 16 g + 15 (g = w & 1) and quarter `kq` of a tile's 128
-// keys; its lanes l and l + 16 hold the hi and lo parts of row 16 g + (l & 15) for the 32 keys, and after an
-// exchange the whole scores of 16 keys each.  Warps w and w + 4 reach the same lanes of TMEM, and take one
-// half of O's columns each.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float2 (&r)[8])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : "=f"(r[0].x), "=f"(r[0].y), "=f"(r[1].x), "=f"(r[1].y), "=f"(r[2].x), "=f"(r[2].y), "=f"(r[3].x), "=f"(r[3].y),
+                   "=f"(r[4].x), "=f"(r[4].y), "=f"(r[5].x), "=f"(r[5].y), "=f"(r[6].x), "=f"(r[6].y), "=f"(r[7].x), "=f"(r[7].y)
+                 : "r"(taddr));
+}
+
+// Softmax and output (warps 0-7).  Lane l of every warp has row l of the block; warp w has keys 32 (w % 4) +
+// 16 (w / 4) .. + 15 of a tile.  Of O, warps 0, 2 (+ 4) reach the hi rows and warps 1, 3 (+ 4) the lo rows of two
+// column halves, warps 0-3 in the first accumulator and warps 4-7 in the second.
 __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, const Ctx &c, Walk walk, int warp, int lane)
 {
-    const int g = warp & 1, half = (warp >> 1) & 1, sub = warp >> 2, kq = 2 * half + sub;
-    const int part = lane >> 4, r16 = lane & 15, row = 16 * g + r16;
-    const uint32_t tw = c.tmem + ((uint32_t)(32 * (warp & 3)) << 16), tO = tw + kColO + 128u * (uint32_t)sub;
-    Meet all{c.bar(B_ALL), 0}, four{c.bar(B_ROWS + g), 0}; // the eight warps; those that share the rows
-    struct Others {
-        float2 v[3];
+    const int quad = warp & 3, sub = warp >> 2, key = 32 * quad + 16 * sub;
+    const uint32_t tw = c.tmem + ((uint32_t)(32 * quad) << 16), tO = tw + kColO + 128u * (uint32_t)sub;
+    Meet all{c.bar(B_ALL), 0};
+    // one value of the row from each warp, in the warps' order, so that all reduce them alike
+    auto put = [&](uint32_t buf, float v) {
+        asm volatile("st.shared.f32 [%0], %1;" ::"r"(c.base + OFF_XCH + 1024u * buf + 128u * (uint32_t)warp + 4u * (uint32_t)lane), "f"(v) : "memory");
+        return all.sync();
     };
-    auto swap_row = [&](uint32_t buf, float2 v, Others &o) { // a value of the row from the warps with its other keys
-        const uint32_t at = c.base + OFF_XCH + 8u * (uint32_t)row + 1024u * buf;
-        if (part == 0) asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(at + 256u * (uint32_t)kq), "f"(v.x), "f"(v.y) : "memory");
-        if (!four.sync()) return false;
+    auto get = [&](uint32_t buf, float (&v)[8]) {
 #pragma unroll
-        for (int i = 0; i < 3; ++i)
-            asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(o.v[i].x), "=f"(o.v[i].y) : "r"(at + 256u * (uint32_t)((kq + 1 + i) & 3)) : "memory");
-        return true;
+        for (int i = 0; i < 8; ++i)
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[i]) : "r"(c.base + OFF_XCH + 1024u * buf + 128u * i + 4u * (uint32_t)lane) : "memory");
     };
+    auto max8 = [](const float (&v)[8]) {
+        return fmaxf(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])), fmaxf(fmaxf(v[4], v[5]), fmaxf(v[6], v[7])));
+    };
+    auto sum8 = [](const float (&v)[8]) { return ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7])); };
     LatentRun run;
     uint32_t n = 0;
     while (walk.next(a, run)) {
-        float cq;
+        float cq, other[8];
         if (!load_queries(a, c, run, warp, lane, all, &cq)) return false;
         mbar_arrive(c.bar(B_Q));
-        const int rr = run.rb * kRB + row, n_rows = a.Lq * a.H;
+        const int rr = run.rb * kRB + lane, n_rows = a.Lq * a.H;
         const bool valid = rr < n_rows;
         const int64_t seen = valid ? latent_visible(a, run.b, rr / a.H) : 0;
+        const int64_t seen_least = latent_visible(a, run.b, run.rb * kRB / a.H); // by every row of the block
         float ref = 0.f, l = 0.f, vs = 0.f; // reference, sum of p and of v over this thread's keys
         bool begun = seen <= run.t0 * kKT;  // the row has a reference, or needs none here
         for (int64_t t = run.t0; t < run.t1; ++t, ++n) {
             const uint32_t buf = n & 1;
-            if (!__all_sync(0xffffffffu, mbar_wait(c.bar(B_S + buf), (n >> 1) & 1))) return false;
+            if (!__all_sync(0xffffffffu, mbar_wait(c.bar(B_S + buf), (n >> 1) & 1) && mbar_wait(c.bar(B_KFULL + n % kStages), (n / kStages) & 1)))
+                return false;
             tc_fence_after();
-            uint32_t sn[32], sr[32];
-            tmem_ld32(tw + kColSn + 64u * buf + 32u * (uint32_t)sub, sn);
-            tmem_ld32(tw + kColSr + 64u * buf + 32u * (uint32_t)sub, sr);
-            const uint32_t sc = c.base + OFF_SC + (n % kStages) * kKT * 4 + 128u * (uint32_t)kq;
-            float s[32];
+            float2 sn[8], z[8], s[8], v[8];
+            tmem_ld16(tw + kColSn + 32u * buf + 16u * (uint32_t)sub, sn);
+            tmem_ld16(tw + kColSr + 32u * buf + 16u * (uint32_t)sub, z);
+            const uint32_t sc = c.base + OFF_SC + (n % kStages) * kKT * 4 + 4u * (uint32_t)key;
+            bool odd = (t + 1) * kKT > seen_least; // some key may not be seen by some row
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
+            for (int e = 0; e < 4; ++e) {
                 asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                             : "=f"(s[4 * e]), "=f"(s[4 * e + 1]), "=f"(s[4 * e + 2]), "=f"(s[4 * e + 3])
+                             : "=f"(s[2 * e].x), "=f"(s[2 * e].y), "=f"(s[2 * e + 1].x), "=f"(s[2 * e + 1].y)
                              : "r"(sc + 16u * e)
                              : "memory");
-            tmem_ld_wait();
-            // this thread's 16 keys: 32 kq + 16 part + e
-            float z[16], sk[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const float t0 = fmaf(__uint_as_float(sn[e]), s[e], __uint_as_float(sr[e]));
-                const float t1 = fmaf(__uint_as_float(sn[16 + e]), s[16 + e], __uint_as_float(sr[16 + e]));
-                z[e] = (part ? t1 : t0) + __shfl_xor_sync(0xffffffffu, part ? t0 : t1, 16);
-                sk[e] = part ? s[16 + e] : s[e];
             }
-            const int n_seen = (int)max((int64_t)0, min((int64_t)16, seen - (t * kKT + 32 * kq + 16 * part)));
-            uint32_t open = 0; // bit e: key e is seen
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                z[e] *= cq;
-                const bool ok = __float_as_uint(sk[e]) != kNoKey && e < n_seen;
-                open |= ok ? 1u << e : 0u;
-                sk[e] = ok ? sk[e] : 0.f;
-            }
-            float v[16], top = 0.f, pt = 0.f, vt = 0.f;
-            auto weigh = [&]() {
-                top = pt = vt = 0.f;
+            for (int e = 0; e < 8; ++e) odd |= __float_as_uint(s[e].x) == kNoKey || __float_as_uint(s[e].y) == kNoKey;
+            uint32_t open = 0xffffu; // bit e: key e is seen
+            if (odd) {               // (the same on every lane, but for rows that are not there)
+                const int n_seen = (int)max((int64_t)0, min((int64_t)16, seen - (t * kKT + key)));
+                open = (1u << n_seen) - 1u;
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const float p = (open >> e & 1u) ? ex2(z[e] - ref) : 0.f;
-                    pt += p;
-                    v[e] = p * sk[e];
-                    vt += v[e];
-                    top = fmaxf(top, p * fmaxf(sk[e], kSmallestScale));
+                for (int e = 0; e < 8; ++e) {
+                    if (__float_as_uint(s[e].x) == kNoKey) open &= ~(1u << (2 * e)), s[e].x = 0.f;
+                    if (__float_as_uint(s[e].y) == kNoKey) open &= ~(2u << (2 * e)), s[e].y = 0.f;
                 }
+            }
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 8; ++e) z[e] = fma2(sn[e], s[e], z[e]); // log2 domain: times cq
+            if (odd) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) { // an unseen key's score: finite, whatever it was
+                    if (!(open >> (2 * e) & 1u)) z[e].x = 0.f;
+                    if (!(open >> (2 * e) & 2u)) z[e].y = 0.f;
+                }
+            }
+            float top, pt, vt;
+            auto weigh = [&]() {
+                const float2 mul = make_float2(cq, cq), sub2 = make_float2(-ref, -ref);
+                float2 ps = make_float2(0.f, 0.f), ws = ps;
+                top = 0.f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    float2 p = fma2(z[e], mul, sub2);
+                    p.x = ex2(p.x);
+                    p.y = ex2(p.y);
+                    if (odd) {
+                        p.x = open >> (2 * e) & 1u ? p.x : 0.f;
+                        p.y = open >> (2 * e) & 2u ? p.y : 0.f;
+                    }
+                    ps = add2(ps, p);
+                    v[e] = mul2(p, s[e]);
+                    ws = add2(ws, v[e]);
+                    top = fmaxf(top, fmaxf(v[e].x, v[e].y));
+                }
+                pt = ps.x + ps.y;
+                vt = ws.x + ws.y;
             };
             weigh();
-            float2 mine = make_float2(begun ? top : INFINITY, vs);
-            mine.x = fmaxf(mine.x, __shfl_xor_sync(0xffffffffu, mine.x, 16));
-            mine.y += __shfl_xor_sync(0xffffffffu, mine.y, 16);
-            Others other;
-            if (!swap_row(buf, mine, other)) return false;
-            // (in the order of the quarters' pairs, so that all four warps get the same sum)
-            const float row_top = fmaxf(fmaxf(mine.x, other.v[0].x), fmaxf(other.v[1].x, other.v[2].x));
-            const float row_vs = kq & 1 ? (mine.y + other.v[2].y) + (other.v[0].y + other.v[1].y) : (mine.y + other.v[0].y) + (other.v[1].y + other.v[2].y);
-            const float left = (float)(run.t1 - t) * kKT;
-            const bool raise = row_top > kTop;
-            const bool lower = row_top < kLow && row_top > 1e-30f && left * row_top > row_vs * (1.f / 256.f);
-            // (the warps of the rows see the same values, so they take this branch together)
-            if (__any_sync(0xffffffffu, raise || lower)) {
-                float zt = -INFINITY; // the row's largest z + log2 s of this tile
+            // a row without a reference, or whose p leave fp32 (scales far below those that it was set by), takes one
+            if (!put(buf, begun && !(pt > 1e37f) ? top : INFINITY)) return false;
+            get(buf, other);
+            const float row_top = max8(other);
+            const bool raise = row_top > kTop, low = row_top < kLow && row_top > 1e-30f;
+            if (__any_sync(0xffffffffu, raise || low)) { // (every warp sees the same rows and values)
+                float zt = -INFINITY;                    // the row's largest z + log2 s of this tile
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    if (open >> e & 1u) zt = fmaxf(zt, z[e] + __log2f(fmaxf(sk[e], kSmallestScale)));
-                zt = fmaxf(zt, __shfl_xor_sync(0xffffffffu, zt, 16));
-                if (!four.sync() || !swap_row(buf, make_float2(zt, 0.f), other)) return false; // (the place is read before it is used again)
-                zt = fmaxf(fmaxf(zt, other.v[0].x), fmaxf(other.v[1].x, other.v[2].x));
+                for (int e = 0; e < 8; ++e) {
+                    if (open >> (2 * e) & 1u) zt = fmaxf(zt, fmaf(z[e].x, cq, __log2f(fmaxf(s[e].x, kSmallestScale))));
+                    if (open >> (2 * e) & 2u) zt = fmaxf(zt, fmaf(z[e].y, cq, __log2f(fmaxf(s[e].y, kSmallestScale))));
+                }
+                if (!put(buf ^ 1, zt)) return false;
+                get(buf ^ 1, other);
+                zt = max8(other);
+                if (!put(buf, vs)) return false;
+                get(buf, other);
+                const float left = (float)(run.t1 - t) * kKT;
+                const bool move = raise || (low && left * row_top > sum8(other) * (1.f / 256.f));
                 float f = 1.f;
-                if ((raise || lower) && zt > -INFINITY) {
+                if (move && zt > -INFINITY) {
                     const float next = rintf(zt) - 3.f; // a whole number: O and the sums move by an exact power of two
                     f = begun ? ex2(ref - next) : 0.f;
                     ref = next;
@@ -481,38 +619,52 @@ __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, const Ct
             vs += vt;
             uint32_t hi[4], lo[4];
             split16(v, 16.f, hi, lo);
-            const uint32_t col = 32u * (uint32_t)kq + 16u * (uint32_t)part;
-            sts4(c.base + OFF_P + kQSlice * buf + sw128((uint32_t)(32 * g + r16), col), hi);
-            sts4(c.base + OFF_P + kQSlice * buf + sw128((uint32_t)(32 * g + 16 + r16), col), lo);
+            const uint32_t at = c.base + OFF_P + kPTile * buf + sw128((uint32_t)lane, (uint32_t)key);
+            sts4(at, hi);
+            sts4(at + 32 * 128, lo);
             fence_proxy_async_smem();
             tc_fence_before();
             mbar_arrive(c.bar(B_P + buf));
         }
-        // the run's last O, and the row's sum over the eight threads that share it
+        // the run's last O, and the row's sum over the eight warps
         if (!__all_sync(0xffffffffu, mbar_wait(c.bar(B_KEMPTY + (n - 1) % kStages), ((n - 1) / kStages) & 1))) return false;
         tc_fence_after();
-        l += __shfl_xor_sync(0xffffffffu, l, 16);
-        Others other;
-        if (!four.sync() || !swap_row(0, make_float2(l, 0.f), other)) return false;
-        l = kq & 1 ? (l + other.v[2].x) + (other.v[0].x + other.v[1].x) : (l + other.v[0].x) + (other.v[1].x + other.v[2].x);
+        if (!all.sync() || !put(0, l)) return false;
+        get(0, other);
+        l = sum8(other);
         const int64_t out_row = run.b * n_rows + rr;
         const float inv = l != 0.f ? 1.f / l : 0.f;
-        float *rec = a.part + ((2 * (int64_t)blockIdx.x + run.first) * kRB + row) * (kR + 4);
+        float *rec = a.part + ((2 * (int64_t)blockIdx.x + run.first) * kRB + lane) * (kR + 4);
+        const int lo_warp = quad & 1;
+        // hi + lo / 16: of each 32 columns a hi warp finishes the first 16 and its lo warp the others; what they hand over
+        // passes through the buffers of v
+        const uint32_t mine = c.base + OFF_P + 2048u * (uint32_t)warp + 16u * (uint32_t)lane, theirs = c.base + OFF_P + 2048u * (uint32_t)(warp ^ 1) + 16u * (uint32_t)lane;
 #pragma unroll 1
         for (int k = 0; k < 4; ++k) {
             uint32_t o[32];
             tmem_ld32(tO + 32u * k, o);
             tmem_ld_wait();
-            float x[16]; // channels 256 sub + 128 half + 32 k + 16 part + e
+            if (k > 0 && !all.sync()) return false; // the values before these have been read
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const float a0 = __uint_as_float(o[e]), a1 = __uint_as_float(o[16 + e]);
-                const float got = __shfl_xor_sync(0xffffffffu, part ? a0 : a1, 16);
-                x[e] = part ? fmaf(a1, 1.f / 16.f, got) : fmaf(got, 1.f / 16.f, a0); // hi + lo / 16
+            for (int e = 0; e < 4; ++e) {
+                uint32_t w[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) w[u] = lo_warp ? o[4 * e + u] : o[16 + 4 * e + u];
+                sts4(mine + 512u * e, w);
             }
-            const int ch = 256 * sub + 128 * half + 32 * k + 16 * part;
-            if (!valid) continue;
-            if (run.whole) {
+            if (!all.sync()) return false;
+            float x[16]; // channels 256 sub + 128 (quad / 2) + 32 k + 16 lo_warp + e
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float y[4];
+                asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(y[0]), "=f"(y[1]), "=f"(y[2]), "=f"(y[3]) : "r"(theirs + 512u * e) : "memory");
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    x[4 * e + u] = lo_warp ? fmaf(__uint_as_float(o[16 + 4 * e + u]), 1.f / 16.f, y[u])
+                                           : fmaf(y[u], 1.f / 16.f, __uint_as_float(o[4 * e + u]));
+            }
+            const int ch = 256 * sub + 128 * (quad >> 1) + 32 * k + 16 * lo_warp;
+            if (valid && run.whole) {
                 uint32_t w[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
@@ -520,13 +672,13 @@ __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, const Ct
                 uint4 *d = reinterpret_cast<uint4 *>(a.o + out_row * kR + ch);
                 d[0] = make_uint4(w[0], w[1], w[2], w[3]);
                 d[1] = make_uint4(w[4], w[5], w[6], w[7]);
-            } else {
+            } else if (valid) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     *reinterpret_cast<float4 *>(rec + 4 + ch + 4 * e) = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
             }
         }
-        if (valid && kq == 0 && part == 0) {
+        if (valid && warp == 0) {
             if (run.whole) {
                 if (a.lse) a.lse[out_row] = l != 0.f ? (ref + log2f(l)) * kLn2 : -INFINITY;
             } else {
@@ -535,12 +687,12 @@ __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, const Ct
             }
         }
         tc_fence_before();
-        if (!all.sync()) return false; // the sums are read before the place is used again
+        if (!all.sync()) return false; // everything shared is read before it is used again
     }
     return true;
 }
 
-__global__ void __launch_bounds__(kThreads, 1) latent_decode_tc_kernel(LatentDecodeArgs a)
+__global__ void __launch_bounds__(kThreads, 1) latent_decode_tc_kernel(LatentDecodeArgs a, const __grid_constant__ Maps maps)
 {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
@@ -556,9 +708,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_tc_kernel(LatentDec
     } else if (tid == 32) {
         for (int b = 0; b < NUM_BARS; ++b) {
             uint32_t count = 1;
-            if (b >= B_KFULL && b < B_KFULL + kStages) count = 128; // each producer thread's copies, and itself
+            if (b >= B_KFULL && b < B_KFULL + kStages) count = maps.box ? 65 : 128; // each copying thread's copies, and itself; TMA
             if (b == B_P || b == B_P + 1 || b == B_Q || b == B_ALL) count = kSoftThreads;
-            if (b == B_ROWS || b == B_ROWS + 1) count = kSoftThreads / 2;
             mbar_init(base + OFF_BAR + 8u * (uint32_t)b, count);
         }
         mbar_init_fence();
@@ -572,8 +723,9 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_tc_kernel(LatentDec
     const Walk walk{T * blockIdx.x / G, T * (blockIdx.x + 1) / G, s_at[0], s_at[1], nrb};
     bool ok = true;
     if (warp < kProdWarp0) ok = softmax_role(a, c, walk, warp, lane);
-    else if (warp < kMmaWarp) ok = producer_role(a, c, walk, warp - kProdWarp0, lane);
-    else if (lane == 0) ok = mma_role(a, c, walk);
+    else if (warp < kMmaWarp && !maps.box) ok = copy_role(a, c, walk, warp - kProdWarp0, lane);
+    else if (warp == kProdWarp0) ok = tma_role(a, maps, c, walk, lane);
+    else if (warp == kMmaWarp && lane == 0) ok = mma_role(a, c, walk);
     if (!ok) flag_error(a.err, CSA_DEVERR_TIMEOUT);
     if (warp == kMmaWarp && lane == 0) { // every MMA completes before TMEM is released
         mma_commit(c.bar(B_FINAL));
@@ -598,11 +750,31 @@ size_t latent_decode_tc_workspace(int64_t B, int Lq, int H, int64_t max_len, int
     return (size_t)*grid * 2 * kRB * (kR + 4) * sizeof(float);
 }
 
+// Boxes of 128 bytes x `rows` rows of a row-major byte matrix, 128-byte swizzle; rows outside read as zeros.
+static bool encode_bytes(CUtensorMap *m, const void *base, int64_t rows, uint64_t row_bytes, uint32_t box_rows)
+{
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tma::encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)row_bytes, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)row_bytes};
+    const cuuint32_t box[2] = {128, box_rows}, estr[2] = {1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 cudaError_t launch_latent_decode_tc(const LatentDecodeArgs &a, cudaStream_t st)
 {
+    // a box is 128 rows of a contiguous run or of pages of whole tiles, or a page of 8, 16, 32 or 64 rows (a swizzle
+    // atom is 8 rows); other pages are copied row by row: 3,700 cycles of issue a tile where a box takes one
+    Maps maps{};
+    const int pr = a.map.page_rows;
+    maps.box = !a.map.pages || pr % kKT == 0 ? kKT : (pr == 8 || pr == 16 || pr == 32 || pr == 64) ? pr : 0;
+    if (a.rows.n < 1 || a.rows.n >= ((int64_t)1 << 31)) maps.box = 0; // TMA coordinates are int32
+    if (maps.box && (!encode_bytes(&maps.lat, a.rows.fp8, a.rows.n, kR, (uint32_t)maps.box) ||
+                     !encode_bytes(&maps.rope, a.rows.rope, a.rows.n, 2 * kRd, (uint32_t)maps.box)))
+        return cudaErrorNotSupported;
     cudaError_t e = cudaFuncSetAttribute(latent_decode_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_ALLOC);
     if (e != cudaSuccess) return e;
-    latent_decode_tc_kernel<<<(unsigned)a.grid, kThreads, SMEM_ALLOC, st>>>(a);
+    latent_decode_tc_kernel<<<(unsigned)a.grid, kThreads, SMEM_ALLOC, st>>>(a, maps);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     return launch_latent_merge_32x128(a, st);
