@@ -18,11 +18,12 @@
 // A work item's rows are 32 (head, token) pairs.  All MMAs are weight-stationary (tcgen05.mma.ws), which spread
 // a small accumulator over all 128 lanes and are bound by what they read of shared memory, 128 bytes a cycle
 // (M = 64, N = 256 at 16 bits: 80 cycles, measured; without .ws 128).  Per tile of 128 keys
-//   S_n (M = 32, N = 128, K = 512, FP8), once for hi and once for lo of q into the same accumulator,
-//   S_r (M = 32, N = 128, K = 64, BF16),
-//   O (+)= v code (M = 64: hi and lo rows of v; two N = 256, K = 128; the codes read MN-major): 44 MMAs, 2,280
-// cycles.  S has row l of the block in lane l of every warp, so a score needs no exchange; one exchange a
-// tile, of the rows' largest v, lets the eight softmax warps decide alike whether a reference moves.
+//   S_n (M = 64: hi and lo rows of q, N = 128, K = 512, FP8), S_r (M = 64, N = 128, K = 64, BF16),
+//   O (+)= v code (M = 64: hi and lo rows of v; two N = 256, K = 128; the codes read MN-major): 28 MMAs, 1,600
+// cycles.  Rows 32 g + 16 part + r of an operand are part 0 (hi) and 1 (lo) of row 16 g + r, so the two parts of a
+// score lie in lanes l and l + 16 of one warp and meet by shuffle.  (Two passes with M = 32 need no shuffle, but
+// 680 more cycles of the chain below; measured 5,100 cycles a tile.)  One exchange a tile, of the rows' largest v,
+// lets the softmax warps decide alike whether a reference moves.
 //
 // Roles: warps 0-7 softmax and output; warp 8 copies the keys by TMA, in boxes of a page or of 128 rows (with
 // pages that no box fits, warps 8 and 9 by cp.async); warp 10 MMA.  Two stages of 80 KB.  Rows that are not to
@@ -40,24 +41,24 @@ using namespace tc;
 
 constexpr int kR = 512, kRd = 64, kRB = 32, kKT = 128, kStages = 2;
 constexpr int kSoftThreads = 256, kProdWarp0 = 8, kMmaWarp = 10, kThreads = 11 * 32;
-// operand tiles of 128-byte rows, 128-byte swizzle: 32 query rows, 64 rows of v, 128 keys
-constexpr uint32_t kQSlice = 4096, kPTile = 8192, kSlice = 16384;
-constexpr uint32_t OFF_P = 0;                         // v: two buffers (and the exchange of a run's output)
+// operand tiles of 128-byte rows, 128-byte swizzle: 64 rows of q and v, 128 keys
+constexpr uint32_t kQSlice = 8192, kPTile = 8192, kSlice = 16384;
+constexpr uint32_t OFF_P = 0;                         // v: two buffers
 constexpr uint32_t OFF_K = 2 * kPTile;                // kStages x 5 slices: 4 of 128 latent channels, 1 of the rotated ones
-constexpr uint32_t OFF_Q = OFF_K + kStages * 5 * kSlice; // 4 slices hi, 4 slices lo, 1 of the rotated channels
-constexpr uint32_t OFF_SC = OFF_Q + 9 * kQSlice;
-constexpr uint32_t OFF_XCH = OFF_SC + kStages * kKT * 4;     // [2 buffers][8 warps][32 rows]
-constexpr uint32_t OFF_BAR = OFF_XCH + 2 * 8 * 32 * 4;
+constexpr uint32_t OFF_Q = OFF_K + kStages * 5 * kSlice; // 4 slices, 1 of the rotated channels
+constexpr uint32_t OFF_SC = OFF_Q + 5 * kQSlice;
+constexpr uint32_t OFF_XCH = OFF_SC + kStages * kKT * 4;     // [2 buffers][4 key quarters][32 rows]
+constexpr uint32_t OFF_BAR = OFF_XCH + 2 * 4 * 32 * 4;
 constexpr uint32_t OFF_AT = OFF_BAR + 160;            // where the CTA's walk begins (3 x int64)
 constexpr uint32_t OFF_TMEM = OFF_AT + 32;
 constexpr uint32_t SMEM_ALLOC = OFF_TMEM + 64 + 1024;
 static_assert(SMEM_ALLOC <= 232448, "shared memory per block");
-enum { B_KFULL = 0, B_KEMPTY = B_KFULL + kStages, B_S = B_KEMPTY + kStages, B_P = B_S + 2, B_Q = B_P + 2, B_ALL, B_TAIL, B_FINAL, NUM_BARS };
+enum { B_KFULL = 0, B_KEMPTY = B_KFULL + kStages, B_S = B_KEMPTY + kStages, B_P = B_S + 2, B_Q = B_P + 2, B_ALL, B_ROWS, B_TAIL = B_ROWS + 2, B_FINAL, NUM_BARS };
 static_assert(8 * NUM_BARS <= 160, "barrier space");
-// TMEM columns: O (two N = 256 accumulators, 128 columns each), S_n and S_r (two buffers of 32 each)
-constexpr uint32_t kColO = 0, kColSn = 256, kColSr = 320, kTmemCols = 512;
-constexpr uint32_t IDESC_SN = (1u << 4) | ((uint32_t)(kKT >> 3) << 17) | (2u << 24); // M = 32, E4M3 x E4M3
-constexpr uint32_t IDESC_SR = idesc_bf16_f32(32, kKT, false, false);
+// TMEM columns: O (two N = 256 accumulators, 128 columns each), S_n and S_r (two buffers of 64 each)
+constexpr uint32_t kColO = 0, kColSn = 256, kColSr = 384, kTmemCols = 512;
+constexpr uint32_t IDESC_SN = (1u << 4) | ((uint32_t)(kKT >> 3) << 17) | (4u << 24); // M = 64, E4M3 x E4M3
+constexpr uint32_t IDESC_SR = idesc_bf16_f32(64, kKT, false, false);
 constexpr uint32_t IDESC_O = (1u << 4) | (1u << 16) | ((uint32_t)(256 >> 3) << 17) | (4u << 24); // M = 64, B MN-major
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr uint32_t kNoKey = 0xffffffffu; // in place of a row's scale: the key is not to be seen
@@ -65,18 +66,27 @@ constexpr float kTop = 448.f, kLow = 1.f / 16.f, kSmallestScale = 7.888609052210
 
 using Split = LatentSplit<kRB, kKT>;
 
-template <bool F8> __device__ __forceinline__ void mma_ws(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+// A descriptor as two words, so that a step along an operand is one 32-bit addition (the issuing thread's
+// instructions between two MMAs bound the chain as much as the MMAs do).
+struct Desc {
+    uint32_t lo, hi;
+    __device__ __forceinline__ explicit Desc(uint64_t d) : lo((uint32_t)d), hi((uint32_t)(d >> 32)) {}
+    __device__ __forceinline__ Desc(uint32_t l, uint32_t h) : lo(l), hi(h) {}
+    __device__ __forceinline__ Desc at(uint32_t bytes) const { return Desc(lo + (bytes >> 4), hi); }
+};
+
+template <bool F8> __device__ __forceinline__ void mma_ws(uint32_t d, Desc a, Desc b, uint32_t idesc, uint32_t accumulate)
 {
     if constexpr (F8)
-        asm volatile("{\n\t.reg .pred p;\n\t"
-                     "setp.ne.b32 p, %4, 0;\n\t"
-                     "tcgen05.mma.ws.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
-                     "r"(accumulate));
+        asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\t"
+                     "setp.ne.b32 p, %6, 0;\n\tmov.b64 x, {%1, %2};\n\tmov.b64 y, {%3, %4};\n\t"
+                     "tcgen05.mma.ws.cta_group::1.kind::f8f6f4 [%0], x, y, %5, p;\n\t}" ::"r"(d), "r"(a.lo), "r"(a.hi), "r"(b.lo), "r"(b.hi),
+                     "r"(idesc), "r"(accumulate));
     else
-        asm volatile("{\n\t.reg .pred p;\n\t"
-                     "setp.ne.b32 p, %4, 0;\n\t"
-                     "tcgen05.mma.ws.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
-                     "r"(accumulate));
+        asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\t"
+                     "setp.ne.b32 p, %6, 0;\n\tmov.b64 x, {%1, %2};\n\tmov.b64 y, {%3, %4};\n\t"
+                     "tcgen05.mma.ws.cta_group::1.kind::f16 [%0], x, y, %5, p;\n\t}" ::"r"(d), "r"(a.lo), "r"(a.hi), "r"(b.lo), "r"(b.hi),
+                     "r"(idesc), "r"(accumulate));
 }
 
 __device__ __forceinline__ float ex2(float x)
@@ -175,7 +185,6 @@ __device__ __forceinline__ bool tma_role(const LatentDecodeArgs &a, const Maps &
     LatentRun run;
     uint32_t n = 0, tails = 0; // tiles so far, those with rows that are not to be seen
     bool ok = true;
-    const int boxes = kKT / M.box;
     while (ok && walk.next(a, run)) {
         const int64_t seen = latent_visible(a, run.b, a.Lq - 1);
         auto resolve = [&](int64_t t, int64_t (&row)[4]) { // keys 32 k + lane of a tile
@@ -200,24 +209,29 @@ __device__ __forceinline__ bool tma_role(const LatentDecodeArgs &a, const Maps &
             const uint32_t st = c.stage(n), full = c.bar(B_KFULL + n % kStages);
             const bool tail = __any_sync(0xffffffffu, row[0] < 0 || row[1] < 0 || row[2] < 0 || row[3] < 0);
             const uint32_t bar = tail ? c.bar(B_TAIL) : full;
-            // box i begins at key i * box: lane (i * box) % 32, k = i * box / 32
-            uint32_t bytes = 0;
-            for (int i = 0; i < boxes; ++i) {
-                const int j = i * M.box, k = j >> 5;
-                const int64_t mine = k == 0 ? row[0] : k == 1 ? row[1] : k == 2 ? row[2] : row[3];
-                if (__shfl_sync(0xffffffffu, mine, j & 31) >= 0) bytes += (uint32_t)M.box * 640u;
-            }
-            if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
-            __syncwarp();
-            for (int i = 0; i < boxes; ++i) {
-                const int j = i * M.box, k = j >> 5;
-                const int64_t mine = k == 0 ? row[0] : k == 1 ? row[1] : k == 2 ? row[2] : row[3];
-                const int64_t first = __shfl_sync(0xffffffffu, mine, j & 31);
-                if (first >= 0 && lane < 5) {
-                    const uint32_t dst = st + (uint32_t)lane * kSlice + (uint32_t)j * 128u;
-                    if (lane < 4) tma_load_2d(dst, &M.lat, 128 * lane, (int32_t)first, bar);
-                    else tma_load_2d(dst, &M.rope, 0, (int32_t)first, bar);
+            if (M.box == kKT) { // one box: lane 0 has its first row
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(bar, row[0] < 0 ? 0u : kKT * 640u);
+                    if (row[0] >= 0) {
+                        tma_load_3d(st, &M.lat, 0, (int32_t)row[0], 0, bar);
+                        tma_load_2d(st + 4 * kSlice, &M.rope, 0, (int32_t)row[0], bar);
+                    }
                 }
+            } else { // the lane that has a box's first row loads it
+                uint32_t bytes = 0;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    bytes += (uint32_t)__popc(__ballot_sync(0xffffffffu, row[k] >= 0 && lane % M.box == 0 && (32 * k) % M.box == 0)) * (uint32_t)M.box * 640u;
+                if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+                __syncwarp();
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (row[k] >= 0 && lane % M.box == 0 && (32 * k) % M.box == 0) {
+                        const uint32_t dst = st + (uint32_t)(32 * k + lane) * 128u;
+#pragma unroll
+                        for (int s = 0; s < 4; ++s) tma_load_3d(dst + (uint32_t)s * kSlice, &M.lat, 0, (int32_t)row[k], s, bar);
+                        tma_load_2d(dst + 4 * kSlice, &M.rope, 0, (int32_t)row[k], bar);
+                    }
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k)
@@ -310,16 +324,17 @@ __device__ __forceinline__ bool mma_role(const LatentDecodeArgs &a, const Ctx &c
     LatentRun run;
     uint32_t n = 0, runs = 0;
     bool pending = false, pending_first = false;
+    const Desc q_desc(sdesc_sw128(c.base + OFF_Q, 16, 1024)), k_desc(sdesc_sw128(c.base + OFF_K, 16, 1024));
+    const Desc p_desc(sdesc_sw128(c.base + OFF_P, 16, 1024)), v_desc(sdesc_sw128(c.base + OFF_K, kSlice, 1024));
     auto output = [&](uint32_t k, bool first) { // O (+)= v code of tile k
         if (!mbar_wait(c.bar(B_P + (k & 1)), (k >> 1) & 1)) return false;
         tc_fence_after();
-        const uint32_t st = c.stage(k);
+        const Desc dp = p_desc.at(kPTile * (k & 1)), dv = v_desc.at((k % kStages) * 5 * kSlice);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                mma_ws<true>(c.tmem + kColO + 128u * h, sdesc_sw128(c.base + OFF_P + kPTile * (k & 1) + 32u * kk, 16, 1024),
-                             sdesc_sw128(st + 2u * h * kSlice + 4096u * kk, kSlice, 1024), IDESC_O, !first || kk > 0);
+                mma_ws<true>(c.tmem + kColO + 128u * h, dp.at(32u * kk), dv.at(2u * h * kSlice + 4096u * kk), IDESC_O, !first || kk > 0);
         mma_commit(c.bar(B_KEMPTY + k % kStages));
         return true;
     };
@@ -341,17 +356,16 @@ __device__ __forceinline__ bool mma_role(const LatentDecodeArgs &a, const Ctx &c
             if (!mbar_wait(full, full_ph)) return false;
             fence_proxy_async_smem(); // cp.async writes for the generic proxy
             tc_fence_after();
-            const uint32_t st = c.stage(n);
+            const Desc dk = k_desc.at((n % kStages) * 5 * kSlice);
+            const uint32_t buf = 64u * (n & 1);
 #pragma unroll
-            for (int s = 0; s < 8; ++s) // hi of q, then lo
+            for (int s = 0; s < 4; ++s)
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    mma_ws<true>(c.tmem + kColSn + 32u * (n & 1), sdesc_sw128(c.base + OFF_Q + s * kQSlice + 32u * kk, 16, 1024),
-                                 sdesc_sw128(st + (s & 3) * kSlice + 32u * kk, 16, 1024), IDESC_SN, (s | kk) != 0);
+                    mma_ws<true>(c.tmem + kColSn + buf, q_desc.at(s * kQSlice + 32u * kk), dk.at(s * kSlice + 32u * kk), IDESC_SN, (s | kk) != 0);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-                mma_ws<false>(c.tmem + kColSr + 32u * (n & 1), sdesc_sw128(c.base + OFF_Q + 8 * kQSlice + 32u * kk, 16, 1024),
-                              sdesc_sw128(st + 4 * kSlice + 32u * kk, 16, 1024), IDESC_SR, kk != 0);
+                mma_ws<false>(c.tmem + kColSr + buf, q_desc.at(4 * kQSlice + 32u * kk), dk.at(4 * kSlice + 32u * kk), IDESC_SR, kk != 0);
             mma_commit(c.bar(B_S + (n & 1)));
             if (pending && !output(n - 1, pending_first)) return false;
             pending = true;
@@ -424,19 +438,20 @@ __device__ __forceinline__ bool load_queries(const LatentDecodeArgs &a, const Ct
         for (int e = 0; e < 8; ++e) x[e].x *= up, x[e].y *= up;
         uint32_t hi[4], lo[4];
         split16(x, 1.f, hi, lo);
-        const uint32_t row = (uint32_t)r;
+        const uint32_t row = 32u * (uint32_t)(r >> 4) + (uint32_t)(r & 15);
         // lane holds channels 16 lane .. 16 lane + 15: byte 16 (lane & 7) of slice lane / 8
         sts4(c.base + OFF_Q + (uint32_t)(lane >> 3) * kQSlice + sw128(row, 16u * (uint32_t)(lane & 7)), hi);
-        sts4(c.base + OFF_Q + (uint32_t)(lane >> 3) * kQSlice + sw128(row, 16u * (uint32_t)(lane & 7)) + 4 * kQSlice, lo);
+        sts4(c.base + OFF_Q + (uint32_t)(lane >> 3) * kQSlice + sw128(row + 16, 16u * (uint32_t)(lane & 7)), lo);
         const uint32_t rr = uint32_t(f32_to_bf16_bits(rx * up)) | (uint32_t(f32_to_bf16_bits(ry * up)) << 16);
-        asm volatile("st.shared.u32 [%0], %1;" ::"r"(c.base + OFF_Q + 8 * kQSlice + sw128(row, 4u * (uint32_t)lane)), "r"(rr) : "memory");
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(c.base + OFF_Q + 4 * kQSlice + sw128(row, 4u * (uint32_t)lane)), "r"(rr) : "memory");
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(c.base + OFF_Q + 4 * kQSlice + sw128(row + 16, 4u * (uint32_t)lane)), "r"(0) : "memory");
         // a row that is not finite makes NaN of its scores
         const float f = finite ? a.scale * kLog2e * exp2i(-k) : NAN;
         if (lane == 0) asm volatile("st.shared.f32 [%0], %1;" ::"r"(c.base + OFF_XCH + 4u * (uint32_t)r), "f"(f) : "memory");
     }
     fence_proxy_async_smem();
     if (!all.sync()) return false;
-    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(*factor) : "r"(c.base + OFF_XCH + 4u * (uint32_t)lane) : "memory");
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(*factor) : "r"(c.base + OFF_XCH + 4u * (uint32_t)(16 * (warp & 1) + (lane & 15))) : "memory");
     return all.sync(); // the factors are read before the place is used again
 }
 
@@ -467,43 +482,48 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
     return d;
 }
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float2 (&r)[8])
+__device__ __forceinline__ void tmem_ld32_pairs(uint32_t taddr, float2 (&r)[16])
 {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
                  : "=f"(r[0].x), "=f"(r[0].y), "=f"(r[1].x), "=f"(r[1].y), "=f"(r[2].x), "=f"(r[2].y), "=f"(r[3].x), "=f"(r[3].y),
-                   "=f"(r[4].x), "=f"(r[4].y), "=f"(r[5].x), "=f"(r[5].y), "=f"(r[6].x), "=f"(r[6].y), "=f"(r[7].x), "=f"(r[7].y)
+                   "=f"(r[4].x), "=f"(r[4].y), "=f"(r[5].x), "=f"(r[5].y), "=f"(r[6].x), "=f"(r[6].y), "=f"(r[7].x), "=f"(r[7].y),
+                   "=f"(r[8].x), "=f"(r[8].y), "=f"(r[9].x), "=f"(r[9].y), "=f"(r[10].x), "=f"(r[10].y), "=f"(r[11].x), "=f"(r[11].y),
+                   "=f"(r[12].x), "=f"(r[12].y), "=f"(r[13].x), "=f"(r[13].y), "=f"(r[14].x), "=f"(r[14].y), "=f"(r[15].x), "=f"(r[15].y)
                  : "r"(taddr));
 }
 
-// Softmax and output (warps 0-7).  Lane l of every warp has row l of the block; warp w has keys 32 (w % 4) +
-// 16 (w / 4) .. + 15 of a tile.  Of O, warps 0, 2 (+ 4) reach the hi rows and warps 1, 3 (+ 4) the lo rows of two
-// column halves, warps 0-3 in the first accumulator and warps 4-7 in the second.
+// Softmax and output (warps 0-7).  Warp w has rows 16 g .. 16 g + 15 (g = w & 1) and quarter kq of a tile's 128
+// keys; its lanes l and l + 16 hold the hi and lo parts of row 16 g + (l & 15) for the 32 keys, and after an
+// exchange the whole scores of 16 keys each.  Warps w and w + 4 reach the same lanes of TMEM, and take one of
+// O's two accumulators each.
 __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, const Ctx &c, Walk walk, int warp, int lane)
 {
-    const int quad = warp & 3, sub = warp >> 2, key = 32 * quad + 16 * sub;
-    const uint32_t tw = c.tmem + ((uint32_t)(32 * quad) << 16), tO = tw + kColO + 128u * (uint32_t)sub;
-    Meet all{c.bar(B_ALL), 0};
-    // one value of the row from each warp, in the warps' order, so that all reduce them alike
+    const int g = warp & 1, half = (warp >> 1) & 1, sub = warp >> 2, kq = 2 * half + sub;
+    const int part = lane >> 4, r16 = lane & 15, row = 16 * g + r16, key = 32 * kq + 16 * part;
+    const uint32_t tw = c.tmem + ((uint32_t)(32 * (warp & 3)) << 16), tO = tw + kColO + 128u * (uint32_t)sub;
+    Meet all{c.bar(B_ALL), 0}, rows{c.bar(B_ROWS + g), 0}; // the eight warps; those that share the rows
+    // one value of the row from each quarter of the keys, in the quarters' order, so that all reduce them alike
+    const uint32_t xch = c.base + OFF_XCH + 4u * (uint32_t)row;
     auto put = [&](uint32_t buf, float v) {
-        asm volatile("st.shared.f32 [%0], %1;" ::"r"(c.base + OFF_XCH + 1024u * buf + 128u * (uint32_t)warp + 4u * (uint32_t)lane), "f"(v) : "memory");
-        return all.sync();
+        if (part == 0) asm volatile("st.shared.f32 [%0], %1;" ::"r"(xch + 512u * buf + 128u * (uint32_t)kq), "f"(v) : "memory");
+        return rows.sync();
     };
-    auto get = [&](uint32_t buf, float (&v)[8]) {
+    auto get = [&](uint32_t buf, float (&v)[4]) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[i]) : "r"(c.base + OFF_XCH + 1024u * buf + 128u * i + 4u * (uint32_t)lane) : "memory");
+        for (int i = 0; i < 4; ++i) asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[i]) : "r"(xch + 512u * buf + 128u * i) : "memory");
     };
-    auto max8 = [](const float (&v)[8]) {
-        return fmaxf(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])), fmaxf(fmaxf(v[4], v[5]), fmaxf(v[6], v[7])));
-    };
-    auto sum8 = [](const float (&v)[8]) { return ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7])); };
+    auto max4 = [](const float (&v)[4]) { return fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])); };
+    auto sum4 = [](const float (&v)[4]) { return (v[0] + v[1]) + (v[2] + v[3]); };
+    auto other_part = [](float v) { return __shfl_xor_sync(0xffffffffu, v, 16); };
     LatentRun run;
     uint32_t n = 0;
     while (walk.next(a, run)) {
-        float cq, other[8];
+        float cq, other[4];
         if (!load_queries(a, c, run, warp, lane, all, &cq)) return false;
         mbar_arrive(c.bar(B_Q));
-        const int rr = run.rb * kRB + lane, n_rows = a.Lq * a.H;
+        const int rr = run.rb * kRB + row, n_rows = a.Lq * a.H;
         const bool valid = rr < n_rows;
         const int64_t seen = valid ? latent_visible(a, run.b, rr / a.H) : 0;
         const int64_t seen_least = latent_visible(a, run.b, run.rb * kRB / a.H); // by every row of the block
@@ -514,22 +534,33 @@ __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, const Ct
             if (!__all_sync(0xffffffffu, mbar_wait(c.bar(B_S + buf), (n >> 1) & 1) && mbar_wait(c.bar(B_KFULL + n % kStages), (n / kStages) & 1)))
                 return false;
             tc_fence_after();
-            float2 sn[8], z[8], s[8], v[8];
-            tmem_ld16(tw + kColSn + 32u * buf + 16u * (uint32_t)sub, sn);
-            tmem_ld16(tw + kColSr + 32u * buf + 16u * (uint32_t)sub, z);
-            const uint32_t sc = c.base + OFF_SC + (n % kStages) * kKT * 4 + 4u * (uint32_t)key;
+            float2 z[8], s[8], v[8];
             bool odd = (t + 1) * kKT > seen_least; // some key may not be seen by some row
+            {
+                float2 sn[16], sr[16], sk[16];
+                tmem_ld32_pairs(tw + kColSn + 64u * buf + 32u * (uint32_t)sub, sn);
+                tmem_ld32_pairs(tw + kColSr + 64u * buf + 32u * (uint32_t)sub, sr);
+                const uint32_t sc = c.base + OFF_SC + (n % kStages) * kKT * 4 + 128u * (uint32_t)kq;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                             : "=f"(s[2 * e].x), "=f"(s[2 * e].y), "=f"(s[2 * e + 1].x), "=f"(s[2 * e + 1].y)
-                             : "r"(sc + 16u * e)
-                             : "memory");
+                for (int e = 0; e < 8; ++e)
+                    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                 : "=f"(sk[2 * e].x), "=f"(sk[2 * e].y), "=f"(sk[2 * e + 1].x), "=f"(sk[2 * e + 1].y)
+                                 : "r"(sc + 16u * e)
+                                 : "memory");
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) sn[e] = fma2(sn[e], sk[e], sr[e]);
+                // hi and lo of a score meet: this lane takes the first or the last 16 keys
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float2 send = part ? sn[e] : sn[8 + e], keep = part ? sn[8 + e] : sn[e];
+                    s[e] = part ? sk[8 + e] : sk[e];
+                    z[e] = add2(keep, make_float2(other_part(send.x), other_part(send.y)));
+                    odd |= __float_as_uint(s[e].x) == kNoKey || __float_as_uint(s[e].y) == kNoKey;
+                }
             }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) odd |= __float_as_uint(s[e].x) == kNoKey || __float_as_uint(s[e].y) == kNoKey;
             uint32_t open = 0xffffu; // bit e: key e is seen
-            if (odd) {               // (the same on every lane, but for rows that are not there)
+            if (odd) {
                 const int n_seen = (int)max((int64_t)0, min((int64_t)16, seen - (t * kKT + key)));
                 open = (1u << n_seen) - 1u;
 #pragma unroll
@@ -538,9 +569,6 @@ __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, const Ct
                     if (__float_as_uint(s[e].y) == kNoKey) open &= ~(2u << (2 * e)), s[e].y = 0.f;
                 }
             }
-            tmem_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 8; ++e) z[e] = fma2(sn[e], s[e], z[e]); // log2 domain: times cq
             if (odd) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) { // an unseen key's score: finite, whatever it was
@@ -572,24 +600,25 @@ __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, const Ct
             };
             weigh();
             // a row without a reference, or whose p leave fp32 (scales far below those that it was set by), takes one
-            if (!put(buf, begun && !(pt > 1e37f) ? top : INFINITY)) return false;
+            top = begun && !(pt > 1e37f) ? top : INFINITY;
+            if (!put(buf, fmaxf(top, other_part(top)))) return false;
             get(buf, other);
-            const float row_top = max8(other);
+            const float row_top = max4(other);
             const bool raise = row_top > kTop, low = row_top < kLow && row_top > 1e-30f;
-            if (__any_sync(0xffffffffu, raise || low)) { // (every warp sees the same rows and values)
-                float zt = -INFINITY;                    // the row's largest z + log2 s of this tile
+            if (__any_sync(0xffffffffu, raise || low)) { // (the warps of the rows see the same values)
+                float zt = -INFINITY; // the row's largest z + log2 s of this tile
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     if (open >> (2 * e) & 1u) zt = fmaxf(zt, fmaf(z[e].x, cq, __log2f(fmaxf(s[e].x, kSmallestScale))));
                     if (open >> (2 * e) & 2u) zt = fmaxf(zt, fmaf(z[e].y, cq, __log2f(fmaxf(s[e].y, kSmallestScale))));
                 }
-                if (!put(buf ^ 1, zt)) return false;
+                if (!put(buf ^ 1, fmaxf(zt, other_part(zt)))) return false;
                 get(buf ^ 1, other);
-                zt = max8(other);
-                if (!put(buf, vs)) return false;
+                zt = max4(other);
+                if (!put(buf, vs + other_part(vs))) return false;
                 get(buf, other);
                 const float left = (float)(run.t1 - t) * kKT;
-                const bool move = raise || (low && left * row_top > sum8(other) * (1.f / 256.f));
+                const bool move = raise || (low && left * row_top > sum4(other) * (1.f / 256.f));
                 float f = 1.f;
                 if (move && zt > -INFINITY) {
                     const float next = rintf(zt) - 3.f; // a whole number: O and the sums move by an exact power of two
@@ -619,9 +648,9 @@ __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, const Ct
             vs += vt;
             uint32_t hi[4], lo[4];
             split16(v, 16.f, hi, lo);
-            const uint32_t at = c.base + OFF_P + kPTile * buf + sw128((uint32_t)lane, (uint32_t)key);
-            sts4(at, hi);
-            sts4(at + 32 * 128, lo);
+            const uint32_t at = c.base + OFF_P + kPTile * buf;
+            sts4(at + sw128((uint32_t)(32 * g + r16), (uint32_t)key), hi);
+            sts4(at + sw128((uint32_t)(32 * g + 16 + r16), (uint32_t)key), lo);
             fence_proxy_async_smem();
             tc_fence_before();
             mbar_arrive(c.bar(B_P + buf));
@@ -629,41 +658,24 @@ __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, const Ct
         // the run's last O, and the row's sum over the eight warps
         if (!__all_sync(0xffffffffu, mbar_wait(c.bar(B_KEMPTY + (n - 1) % kStages), ((n - 1) / kStages) & 1))) return false;
         tc_fence_after();
-        if (!all.sync() || !put(0, l)) return false;
+        if (!rows.sync() || !put(0, l + other_part(l))) return false;
         get(0, other);
-        l = sum8(other);
+        l = sum4(other);
         const int64_t out_row = run.b * n_rows + rr;
         const float inv = l != 0.f ? 1.f / l : 0.f;
-        float *rec = a.part + ((2 * (int64_t)blockIdx.x + run.first) * kRB + lane) * (kR + 4);
-        const int lo_warp = quad & 1;
-        // hi + lo / 16: of each 32 columns a hi warp finishes the first 16 and its lo warp the others; what they hand over
-        // passes through the buffers of v
-        const uint32_t mine = c.base + OFF_P + 2048u * (uint32_t)warp + 16u * (uint32_t)lane, theirs = c.base + OFF_P + 2048u * (uint32_t)(warp ^ 1) + 16u * (uint32_t)lane;
+        float *rec = a.part + ((2 * (int64_t)blockIdx.x + run.first) * kRB + row) * (kR + 4);
 #pragma unroll 1
         for (int k = 0; k < 4; ++k) {
             uint32_t o[32];
             tmem_ld32(tO + 32u * k, o);
             tmem_ld_wait();
-            if (k > 0 && !all.sync()) return false; // the values before these have been read
+            float x[16]; // hi + lo / 16 of channels 256 sub + 128 half + 32 k + 16 part + e
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                uint32_t w[4];
-#pragma unroll
-                for (int u = 0; u < 4; ++u) w[u] = lo_warp ? o[4 * e + u] : o[16 + 4 * e + u];
-                sts4(mine + 512u * e, w);
+            for (int e = 0; e < 16; ++e) {
+                const float a0 = __uint_as_float(o[e]), a1 = __uint_as_float(o[16 + e]), got = other_part(part ? a0 : a1);
+                x[e] = part ? fmaf(a1, 1.f / 16.f, got) : fmaf(got, 1.f / 16.f, a0);
             }
-            if (!all.sync()) return false;
-            float x[16]; // channels 256 sub + 128 (quad / 2) + 32 k + 16 lo_warp + e
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float y[4];
-                asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(y[0]), "=f"(y[1]), "=f"(y[2]), "=f"(y[3]) : "r"(theirs + 512u * e) : "memory");
-#pragma unroll
-                for (int u = 0; u < 4; ++u)
-                    x[4 * e + u] = lo_warp ? fmaf(__uint_as_float(o[16 + 4 * e + u]), 1.f / 16.f, y[u])
-                                           : fmaf(y[u], 1.f / 16.f, __uint_as_float(o[4 * e + u]));
-            }
-            const int ch = 256 * sub + 128 * (quad >> 1) + 32 * k + 16 * lo_warp;
+            const int ch = 256 * sub + 128 * half + 32 * k + 16 * part;
             if (valid && run.whole) {
                 uint32_t w[8];
 #pragma unroll
@@ -678,7 +690,7 @@ __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, const Ct
                     *reinterpret_cast<float4 *>(rec + 4 + ch + 4 * e) = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
             }
         }
-        if (valid && warp == 0) {
+        if (valid && kq == 0 && part == 0) {
             if (run.whole) {
                 if (a.lse) a.lse[out_row] = l != 0.f ? (ref + log2f(l)) * kLn2 : -INFINITY;
             } else {
@@ -710,6 +722,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_tc_kernel(LatentDec
             uint32_t count = 1;
             if (b >= B_KFULL && b < B_KFULL + kStages) count = maps.box ? 65 : 128; // each copying thread's copies, and itself; TMA
             if (b == B_P || b == B_P + 1 || b == B_Q || b == B_ALL) count = kSoftThreads;
+            if (b == B_ROWS || b == B_ROWS + 1) count = kSoftThreads / 2;
             mbar_init(base + OFF_BAR + 8u * (uint32_t)b, count);
         }
         mbar_init_fence();
@@ -750,15 +763,17 @@ size_t latent_decode_tc_workspace(int64_t B, int Lq, int H, int64_t max_len, int
     return (size_t)*grid * 2 * kRB * (kR + 4) * sizeof(float);
 }
 
-// Boxes of 128 bytes x `rows` rows of a row-major byte matrix, 128-byte swizzle; rows outside read as zeros.
-static bool encode_bytes(CUtensorMap *m, const void *base, int64_t rows, uint64_t row_bytes, uint32_t box_rows)
+// A row-major byte matrix [rows, slices * 128] seen as [slices][rows][128], read in boxes of box_rows rows of
+// box_slices slices with the 128-byte swizzle; rows outside read as zeros.
+static bool encode_slices(CUtensorMap *m, const void *base, int64_t rows, uint32_t slices, uint32_t box_rows, uint32_t box_slices)
 {
     PFN_cuTensorMapEncodeTiled_v12000 enc = tma::encoder();
     if (!enc) return false;
-    const cuuint64_t dims[2] = {(cuuint64_t)row_bytes, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)row_bytes};
-    const cuuint32_t box[2] = {128, box_rows}, estr[2] = {1, 1};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    const cuuint64_t dims[3] = {128, (cuuint64_t)rows, slices}, strides[2] = {(cuuint64_t)slices * 128, 128};
+    const cuuint32_t box[3] = {128, box_rows, box_slices}, estr[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, slices > 1 ? 3 : 2, const_cast<void *>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 cudaError_t launch_latent_decode_tc(const LatentDecodeArgs &a, cudaStream_t st)
@@ -769,8 +784,8 @@ cudaError_t launch_latent_decode_tc(const LatentDecodeArgs &a, cudaStream_t st)
     const int pr = a.map.page_rows;
     maps.box = !a.map.pages || pr % kKT == 0 ? kKT : (pr == 8 || pr == 16 || pr == 32 || pr == 64) ? pr : 0;
     if (a.rows.n < 1 || a.rows.n >= ((int64_t)1 << 31)) maps.box = 0; // TMA coordinates are int32
-    if (maps.box && (!encode_bytes(&maps.lat, a.rows.fp8, a.rows.n, kR, (uint32_t)maps.box) ||
-                     !encode_bytes(&maps.rope, a.rows.rope, a.rows.n, 2 * kRd, (uint32_t)maps.box)))
+    if (maps.box && (!encode_slices(&maps.lat, a.rows.fp8, a.rows.n, kR / 128, (uint32_t)maps.box, maps.box == kKT ? kR / 128 : 1) ||
+                     !encode_slices(&maps.rope, a.rows.rope, a.rows.n, 1, (uint32_t)maps.box, 1)))
         return cudaErrorNotSupported;
     cudaError_t e = cudaFuncSetAttribute(latent_decode_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_ALLOC);
     if (e != cudaSuccess) return e;
