@@ -22,6 +22,23 @@ struct RowMap {
         const int64_t r = paged_row(pages, max_pages, page_rows, b, s, pages ? 0 : off[b]);
         return r >= 0 && r < n ? r : -1;
     }
+    // The same in two steps for positions below 2^31 (32-bit division), the load apart from its use: nothing touches
+    // the loaded page number, so nothing waits for it.  `first` is the sequence's off[b] (0 with pages).
+    __device__ __forceinline__ int64_t first(int64_t b) const { return pages ? 0 : off[b]; }
+    __device__ __forceinline__ int32_t page(int64_t b, uint32_t s) const
+    {
+        int32_t p = -1;
+        if (pages) {
+            const uint32_t i = s / (uint32_t)page_rows;
+            if (i < (uint32_t)max_pages) p = __ldg(pages + b * max_pages + i);
+        }
+        return p;
+    }
+    __device__ __forceinline__ int64_t row(int32_t page, int64_t first, uint32_t s) const
+    {
+        const int64_t r = pages ? (page < 0 ? -1 : (int64_t)page * page_rows + s % (uint32_t)page_rows) : first + s;
+        return r >= 0 && r < n ? r : -1;
+    }
 };
 
 struct LatentAppendArgs {

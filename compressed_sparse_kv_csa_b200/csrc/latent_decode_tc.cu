@@ -164,7 +164,10 @@ struct Ctx {
 
 struct Maps {
     CUtensorMap lat, rope;
-    int box; // rows of a box; 0: copied by cp.async
+    int box;             // rows of a box; 0: copied by cp.async
+    uint32_t page_tiles; // box = 128: tiles of a page
+    int shift;           // box < 128: log2 of the page's rows
+    uint32_t n_pages;    // pages that the cache has (a last partial one counts)
 };
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, uint32_t bytes) // 16 bytes, or zeros
@@ -187,27 +190,56 @@ __device__ __forceinline__ bool tma_role(const LatentDecodeArgs &a, const Maps &
     bool ok = true;
     while (ok && walk.next(a, run)) {
         const int64_t seen = latent_visible(a, run.b, a.Lq - 1);
-        auto resolve = [&](int64_t t, int64_t (&row)[4]) { // keys 32 k + lane of a tile
+        // Page numbers are loaded two tiles ahead of their use, and nothing touches them before: behind a busy memory a
+        // lookup takes as long as a tile.  Every instruction counts here: the copies of a tile wait for this warp.
+        const int64_t base = a.map.first(run.b); // without pages: the row of position 0
+        const int32_t *table = a.map.pages + (a.map.pages ? run.b * a.map.max_pages : 0);
+        const uint32_t max_pages = (uint32_t)a.map.max_pages, rows_n = (uint32_t)a.rows.n;
+        auto fetch = [&](int64_t t, int32_t (&page)[4]) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const int64_t s = t * kKT + 32 * k + lane;
-                row[k] = s < seen ? a.map.row(run.b, s) : -1;
-                if (s < seen && row[k] < 0) flag_error(a.err, CSA_DEVERR_INDEX);
+                page[k] = -1;
+                const uint32_t i = M.box == kKT ? (uint32_t)t / M.page_tiles : ((uint32_t)t * kKT + 32 * k + lane) >> M.shift;
+                if (a.map.pages && (k == 0 || M.box < kKT) && t < run.t1 && i < max_pages) page[k] = __ldg(table + i);
             }
         };
-        int64_t ahead[4];
-        resolve(run.t0, ahead);
+        int32_t now[4], next[4];
+        fetch(run.t0, now);
+        fetch(run.t0 + 1, next);
         for (int64_t t = run.t0; t < run.t1; ++t, ++n) {
-            int64_t row[4];
+            int32_t row[4];
+            const int n_seen = (int)min((int64_t)kKT, seen - t * kKT); // keys of this tile
+            if (M.box == kKT) {
+                // one run of rows: r0 .. r0 + 127
+                const int64_t r0 = !a.map.pages ? base + t * kKT
+                                   : (uint32_t)now[0] < M.n_pages ? (int64_t)now[0] * a.map.page_rows + (uint32_t)t % M.page_tiles * kKT : -kKT;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) row[k] = ahead[k];
-            if (t + 1 < run.t1) resolve(t + 1, ahead); // page lookups beside this tile's copies
+                for (int k = 0; k < 4; ++k) {
+                    const int64_t r = r0 + 32 * k + lane;
+                    row[k] = 32 * k + lane < n_seen && (uint64_t)r < rows_n ? (int32_t)r : -1;
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t in_page = ((uint32_t)(32 * k) + lane) & ((1u << M.shift) - 1u);
+                    const uint32_t r = ((uint32_t)now[k] << M.shift) + in_page;
+                    row[k] = 32 * k + lane < n_seen && (uint32_t)now[k] < M.n_pages && r < rows_n ? (int32_t)r : -1;
+                }
+            }
+            const bool tail = __any_sync(0xffffffffu, row[0] < 0 || row[1] < 0 || row[2] < 0 || row[3] < 0);
+            if (tail) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (row[k] < 0 && 32 * k + lane < n_seen) flag_error(a.err, CSA_DEVERR_INDEX);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) now[k] = next[k];
+            fetch(t + 2, next);
             if (n >= kStages && !__all_sync(0xffffffffu, mbar_wait(c.bar(B_KEMPTY + n % kStages), ((n / kStages) & 1) ^ 1))) {
                 ok = false;
                 break;
             }
             const uint32_t st = c.stage(n), full = c.bar(B_KFULL + n % kStages);
-            const bool tail = __any_sync(0xffffffffu, row[0] < 0 || row[1] < 0 || row[2] < 0 || row[3] < 0);
             const uint32_t bar = tail ? c.bar(B_TAIL) : full;
             if (M.box == kKT) { // one box: lane 0 has its first row
                 if (lane == 0) {
@@ -267,10 +299,11 @@ __device__ __forceinline__ bool copy_role(const LatentDecodeArgs &a, const Ctx &
     bool ok = true;
     while (ok && walk.next(a, run)) {
         const int64_t seen = latent_visible(a, run.b, a.Lq - 1);
+        const int64_t first = a.map.first(run.b);
         auto resolve = [&](int64_t t, int h) { // row of the key that this lane looks up
             const int64_t s = t * kKT + 64 * warp + 32 * h + lane;
             if (s >= seen) return (int64_t)-1;
-            const int64_t row = a.map.row(run.b, s);
+            const int64_t row = a.map.row(a.map.page(run.b, (uint32_t)s), first, (uint32_t)s);
             if (row < 0) flag_error(a.err, CSA_DEVERR_INDEX);
             return row;
         };
@@ -387,26 +420,36 @@ struct Meet {
     }
 };
 
-// Queries of a run into shared memory, as hi and lo; *factor takes a score of this lane's row to the log2 domain.
-__device__ __forceinline__ bool load_queries(const LatentDecodeArgs &a, const Ctx &c, const LatentRun &run, int warp, int lane,
-                                             Meet &all, float *factor)
-{
-    const int n_rows = min(kRB, a.Lq * a.H - run.rb * kRB);
-    const uint16_t *q = a.q + (run.b * a.Lq * a.H + run.rb * kRB) * (int64_t)(kR + kRd);
+// A warp's 4 rows of a run's queries, on their way from memory: they are asked for before the output of the run
+// before is written.
+struct Queries {
     uint4 u[4][2];
     uint32_t w[4];
+    __device__ __forceinline__ void fetch(const LatentDecodeArgs &a, const LatentRun &run, int warp, int lane)
+    {
+        const int n_rows = min(kRB, a.Lq * a.H - run.rb * kRB);
+        const uint16_t *q = a.q + (run.b * a.Lq * a.H + run.rb * kRB) * (int64_t)(kR + kRd);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) { // all loads of the warp's 4 rows in flight together
-        const int r = 4 * warp + i;
-        u[i][0] = u[i][1] = make_uint4(0, 0, 0, 0);
-        w[i] = 0;
-        if (r < n_rows) {
-            const uint16_t *p = q + (int64_t)r * (kR + kRd);
-            u[i][0] = __ldg(reinterpret_cast<const uint4 *>(p + 16 * lane));
-            u[i][1] = __ldg(reinterpret_cast<const uint4 *>(p + 16 * lane + 8));
-            w[i] = __ldg(reinterpret_cast<const uint32_t *>(p + kR + 2 * lane));
+        for (int i = 0; i < 4; ++i) {
+            const int r = 4 * warp + i;
+            u[i][0] = u[i][1] = make_uint4(0, 0, 0, 0);
+            w[i] = 0;
+            if (r < n_rows) {
+                const uint16_t *p = q + (int64_t)r * (kR + kRd);
+                u[i][0] = __ldg(reinterpret_cast<const uint4 *>(p + 16 * lane));
+                u[i][1] = __ldg(reinterpret_cast<const uint4 *>(p + 16 * lane + 8));
+                w[i] = __ldg(reinterpret_cast<const uint32_t *>(p + kR + 2 * lane));
+            }
         }
     }
+};
+
+// Into shared memory, as hi and lo; *factor takes a score of this lane's row to the log2 domain.
+__device__ __forceinline__ bool store_queries(const LatentDecodeArgs &a, const Ctx &c, const Queries &in, int warp, int lane, Meet &all,
+                                              float *factor)
+{
+    const uint4(&u)[4][2] = in.u;
+    const uint32_t(&w)[4] = in.w;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = 4 * warp + i;
@@ -517,11 +560,15 @@ __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, const Ct
     auto max4 = [](const float (&v)[4]) { return fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])); };
     auto sum4 = [](const float (&v)[4]) { return (v[0] + v[1]) + (v[2] + v[3]); };
     auto other_part = [](float v) { return __shfl_xor_sync(0xffffffffu, v, 16); };
-    LatentRun run;
+    LatentRun run, next_run;
+    Queries queries;
     uint32_t n = 0;
-    while (walk.next(a, run)) {
+    bool more = walk.next(a, next_run);
+    if (more) queries.fetch(a, next_run, warp, lane);
+    while (more) {
+        run = next_run;
         float cq, other[4];
-        if (!load_queries(a, c, run, warp, lane, all, &cq)) return false;
+        if (!store_queries(a, c, queries, warp, lane, all, &cq)) return false;
         mbar_arrive(c.bar(B_Q));
         const int rr = run.rb * kRB + row, n_rows = a.Lq * a.H;
         const bool valid = rr < n_rows;
@@ -655,6 +702,8 @@ __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, const Ct
             tc_fence_before();
             mbar_arrive(c.bar(B_P + buf));
         }
+        more = walk.next(a, next_run);
+        if (more) queries.fetch(a, next_run, warp, lane);
         // the run's last O, and the row's sum over the eight warps
         if (!__all_sync(0xffffffffu, mbar_wait(c.bar(B_KEMPTY + (n - 1) % kStages), ((n - 1) / kStages) & 1))) return false;
         tc_fence_after();
@@ -782,8 +831,15 @@ cudaError_t launch_latent_decode_tc(const LatentDecodeArgs &a, cudaStream_t st)
     // atom is 8 rows); other pages are copied row by row: 3,700 cycles of issue a tile where a box takes one
     Maps maps{};
     const int pr = a.map.page_rows;
+    maps.page_tiles = 1;
     maps.box = !a.map.pages || pr % kKT == 0 ? kKT : (pr == 8 || pr == 16 || pr == 32 || pr == 64) ? pr : 0;
     if (a.rows.n < 1 || a.rows.n >= ((int64_t)1 << 31)) maps.box = 0; // TMA coordinates are int32
+    if (maps.box && a.map.pages) {
+        maps.n_pages = (uint32_t)((a.rows.n + pr - 1) / pr);
+        if (maps.box == kKT) maps.page_tiles = (uint32_t)(pr / kKT);
+        else
+            while ((1 << maps.shift) < pr) ++maps.shift;
+    }
     if (maps.box && (!encode_slices(&maps.lat, a.rows.fp8, a.rows.n, kR / 128, (uint32_t)maps.box, maps.box == kKT ? kR / 128 : 1) ||
                      !encode_slices(&maps.rope, a.rows.rope, a.rows.n, 1, (uint32_t)maps.box, 1)))
         return cudaErrorNotSupported;
