@@ -597,9 +597,9 @@ int latent_gather(const csa_kv_rows *rows, const int64_t *cu, const int64_t *sta
 size_t latent_attn_decode_workspace_size(int64_t B, int32_t Lq, int32_t H, int32_t R, int64_t max_len)
 {
     if (B <= 0 || Lq <= 0 || H <= 0 || R <= 0 || max_len < 0 || !latent_decode_shape_ok(B, Lq, H, R, 16, max_len)) return 0;
-    int grid; // the rotated channels are not known here: the larger of the two kernels' needs
-    size_t need = latent_decode_generic_workspace(B, Lq, H, R, max_len, &grid);
-    if (R == 512) need = std::max(need, latent_decode_tc_workspace(B, Lq, H, max_len, &grid));
+    int grid, par; // the rotated channels are not known here: the larger of the two kernels' needs
+    size_t need = latent_decode_generic_workspace(B, Lq, H, R, max_len, &grid, &par);
+    if (R == 512) need = std::max(need, latent_decode_tc_workspace(B, Lq, H, max_len, &grid, &par));
     return round_up(need) + kAlign;
 }
 
@@ -629,11 +629,11 @@ int latent_attn_decode(const void *q, const csa_kv_rows *rows, const int64_t *po
     a.part = reinterpret_cast<float *>((reinterpret_cast<uintptr_t>(ws) + kAlign - 1) / kAlign * kAlign);
     a.err = dev_error_word();
     if (latent_decode_tc_eligible(R, rd)) {
-        latent_decode_tc_workspace(B, Lq, H, max_len, &a.grid);
+        latent_decode_tc_workspace(B, Lq, H, max_len, &a.grid, &a.par);
         note_path(CSA_PATH_LATENT_DECODE_TC);
         return status_of(launch_latent_decode_tc(a, S(stream)));
     }
-    latent_decode_generic_workspace(B, Lq, H, R, max_len, &a.grid);
+    latent_decode_generic_workspace(B, Lq, H, R, max_len, &a.grid, &a.par);
     note_path(CSA_PATH_LATENT_DECODE_GENERIC);
     return status_of(launch_latent_decode_generic(a, S(stream)));
 }

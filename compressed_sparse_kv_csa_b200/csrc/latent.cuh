@@ -78,6 +78,7 @@ struct LatentDecodeArgs {
     float *lse;  // [B, Lq, H] or null
     float *part; // partials: 2 slots per CTA of RB rows, R + 2 floats each
     int grid;    // CTAs of the split
+    int par;     // CTAs side by side on the same keys, one for each row block; 1: a CTA's runs may be of any row block
     int *err;
 };
 
@@ -89,12 +90,16 @@ __device__ __forceinline__ int64_t latent_visible(const LatentDecodeArgs &a, int
     return p < 0 ? 0 : (p < a.max_len ? p : a.max_len);
 }
 
-// The split of a decode call: every (sequence, block of RB query rows) is a run of key tiles, all
-// runs lie one behind another, and CTA i of G takes the tiles [i T / G, (i + 1) T / G) of them.  So
-// the work is even whatever the lengths are, and a CTA cuts at most the two runs at its ends: its
-// run that starts inside goes to slot 2i, the one that starts at its first tile but does not end
-// here to slot 2i + 1; a run that lies in one CTA is finished there.  A sequence that sees nothing
-// has one (empty) tile, so its rows are written too.
+// The split of a decode call: every (sequence, block of RB query rows) is a run of key tiles, and all runs lie one
+// behind another.  With par = 1 CTA i of G takes the tiles [i T / G, (i + 1) T / G) of them.  With par =
+// the row blocks of a sequence, the runs are those of one row block, G / par groups of CTAs share them
+// so, and CTA rb of a group has row block rb: the row blocks walk the same keys at the same time, so that
+// memory is read once for all of them (one after another, a long sequence's keys have left L2 in
+// between: 4 x 1M keys x 64 heads, two row blocks, read 5.4 GB instead of 2.7).  Either way the work is even
+// whatever the lengths are, and a CTA cuts at most the two runs at its ends: its run that starts inside
+// goes to slot 2i, the one that starts at its first tile but does not end here to slot 2i + 1; a run that
+// lies in one CTA is finished there.  A sequence that sees nothing has one (empty) tile, so its rows are
+// written too.
 template <int RB, int KT> struct LatentSplit {
     static __device__ __forceinline__ int64_t tiles(const LatentDecodeArgs &a, int64_t b)
     {
@@ -102,6 +107,15 @@ template <int RB, int KT> struct LatentSplit {
         return t < 1 ? 1 : t;
     }
     static __host__ __device__ __forceinline__ int64_t row_blocks(int Lq, int H) { return ((int64_t)Lq * H + RB - 1) / RB; }
+    // Grid and par for at most `most` CTAs; side by side where that leaves at most a tenth of them idle.
+    static void plan(int64_t B, int Lq, int H, int64_t max_len, int most, int *grid, int *par)
+    {
+        const int64_t nrb = row_blocks(Lq, H), t = (max_len + KT - 1) / KT, tiles = B * (t < 1 ? 1 : t);
+        const bool side = nrb <= most && most / nrb * nrb * 10 >= 9 * (int64_t)most;
+        *par = side ? (int)nrb : 1;
+        const int64_t work = side ? tiles : tiles * nrb, groups = most / *par;
+        *grid = (int)((work < groups ? work : groups) * *par);
+    }
     // Tiles of the sequences [0, b1), one warp.
     static __device__ __forceinline__ int64_t warp_total(const LatentDecodeArgs &a, int64_t b0, int64_t b1, int lane)
     {
@@ -138,19 +152,66 @@ template <int RB, int KT> struct LatentSplit {
     }
 };
 
-// A CTA's walk over its runs.
+// A part of a run.
 struct LatentRun {
     int64_t b, t0, t1; // sequence, first tile and end of the part that lies here
     int rb;            // row block
     bool whole, first; // the run lies here entirely; its first tile lies here
 };
 
+// A CTA's walk over its runs.  One warp finds where it begins (begin()); then every role walks by itself.
+template <int RB, int KT> struct LatentWalk {
+    using Split = LatentSplit<RB, KT>;
+    int64_t at, end, b, before, nrb; // nrb: row blocks within the runs (1 side by side)
+    int rb0;                         // the CTA's row block side by side
+    static __device__ __forceinline__ void begin(const LatentDecodeArgs &a, int lane, int64_t (&out)[3])
+    {
+        const int64_t nrb = a.par > 1 ? 1 : Split::row_blocks(a.Lq, a.H), G = gridDim.x / a.par, i = blockIdx.x / a.par;
+        const int64_t T = Split::warp_total(a, 0, a.B, lane) * nrb;
+        int64_t b, before;
+        Split::warp_find(a, T * i / G, nrb, lane, &b, &before);
+        if (lane == 0) out[0] = b, out[1] = before, out[2] = T;
+    }
+    __device__ __forceinline__ LatentWalk(const LatentDecodeArgs &a, const int64_t (&from)[3])
+    {
+        const int64_t G = gridDim.x / a.par, i = blockIdx.x / a.par, T = from[2];
+        nrb = a.par > 1 ? 1 : Split::row_blocks(a.Lq, a.H);
+        rb0 = (int)(blockIdx.x % a.par);
+        at = T * i / G;
+        end = T * (i + 1) / G;
+        b = from[0];
+        before = from[1];
+    }
+    __device__ __forceinline__ bool next(const LatentDecodeArgs &a, LatentRun &r)
+    {
+        if (at >= end || b >= a.B) return false;
+        const int64_t tiles = Split::tiles(a, b);
+        int64_t in = at - before;
+        r.b = b;
+        r.rb = rb0;
+        if (nrb > 1) {
+            r.rb = (int)(in / tiles);
+            in -= r.rb * tiles;
+        }
+        r.t0 = in;
+        r.t1 = min(tiles, r.t0 + (end - at));
+        r.first = r.t0 == 0;
+        r.whole = r.first && r.t1 == tiles;
+        at += r.t1 - r.t0;
+        if (r.t1 == tiles && (nrb == 1 || r.rb + 1 == nrb)) {
+            before += tiles * nrb;
+            ++b;
+        }
+        return true;
+    }
+};
+
 cudaError_t launch_latent_decode_generic(LatentDecodeArgs a, cudaStream_t st);
-size_t latent_decode_generic_workspace(int64_t B, int Lq, int H, int R, int64_t max_len, int *grid);
+size_t latent_decode_generic_workspace(int64_t B, int Lq, int H, int R, int64_t max_len, int *grid, int *par);
 
 // 512 + 64 channels on the tensor cores (blocks of 32 rows, tiles of 128 keys).
 bool latent_decode_tc_eligible(int R, int rd);
-size_t latent_decode_tc_workspace(int64_t B, int Lq, int H, int64_t max_len, int *grid);
+size_t latent_decode_tc_workspace(int64_t B, int Lq, int H, int64_t max_len, int *grid, int *par);
 cudaError_t launch_latent_decode_tc(const LatentDecodeArgs &a, cudaStream_t st);
 cudaError_t launch_latent_merge_32x128(const LatentDecodeArgs &a, cudaStream_t st);
 

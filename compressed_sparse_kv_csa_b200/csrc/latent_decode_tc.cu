@@ -134,27 +134,7 @@ __device__ __forceinline__ void split16(const float2 (&v)[8], float lo_scale, ui
     }
 }
 
-// The runs of a CTA, one after another; every role walks them by itself.
-struct Walk {
-    int64_t at, end, b, before, nrb;
-    __device__ __forceinline__ bool next(const LatentDecodeArgs &a, LatentRun &r)
-    {
-        if (at >= end || b >= a.B) return false;
-        const int64_t tiles = Split::tiles(a, b);
-        r.b = b;
-        r.rb = (int)((at - before) / tiles);
-        r.t0 = (at - before) - r.rb * tiles;
-        r.t1 = min(tiles, r.t0 + (end - at));
-        r.first = r.t0 == 0;
-        r.whole = r.first && r.t1 == tiles;
-        at += r.t1 - r.t0;
-        if (r.t1 == tiles && r.rb + 1 == nrb) {
-            before += tiles * nrb;
-            ++b;
-        }
-        return true;
-    }
-};
+using Walk = LatentWalk<kRB, kKT>;
 
 struct Ctx {
     uint32_t base, tmem;
@@ -241,29 +221,32 @@ __device__ __forceinline__ bool tma_role(const LatentDecodeArgs &a, const Maps &
             }
             const uint32_t st = c.stage(n), full = c.bar(B_KFULL + n % kStages);
             const uint32_t bar = tail ? c.bar(B_TAIL) : full;
-            if (M.box == kKT) { // one box: lane 0 has its first row
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(bar, row[0] < 0 ? 0u : kKT * 640u);
-                    if (row[0] >= 0) {
-                        tma_load_3d(st, &M.lat, 0, (int32_t)row[0], 0, bar);
-                        tma_load_2d(st + 4 * kSlice, &M.rope, 0, (int32_t)row[0], bar);
+            if (M.box == kKT) {
+                const int32_t first = __shfl_sync(0xffffffffu, row[0], 0);
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(bar, first < 0 ? 0u : kKT * 640u);
+                    if (first >= 0) {
+                        tma_load_3d(st, &M.lat, 0, first, 0, bar);
+                        tma_load_2d(st + 4 * kSlice, &M.rope, 0, first, bar);
                     }
                 }
-            } else { // the lane that has a box's first row loads it
-                uint32_t bytes = 0;
+            } else { // box i begins at key i * box: lane (i * box) % 32 of row[i * box / 32]
+                const bool begins = lane % M.box == 0;
+                uint32_t boxes = 0;
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    bytes += (uint32_t)__popc(__ballot_sync(0xffffffffu, row[k] >= 0 && lane % M.box == 0 && (32 * k) % M.box == 0)) * (uint32_t)M.box * 640u;
-                if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
-                __syncwarp();
+                    boxes += (uint32_t)__popc(__ballot_sync(0xffffffffu, row[k] >= 0 && begins && (32 * k) % M.box == 0));
+                if (elect_one()) mbar_arrive_expect_tx(bar, boxes * (uint32_t)M.box * 640u);
+                for (int j = 0; j < kKT; j += M.box) {
+                    const int k = j >> 5;
+                    const int32_t first = __shfl_sync(0xffffffffu, k == 0 ? row[0] : k == 1 ? row[1] : k == 2 ? row[2] : row[3], j & 31);
+                    if (first >= 0 && elect_one()) {
+                        const uint32_t dst = st + (uint32_t)j * 128u;
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (row[k] >= 0 && lane % M.box == 0 && (32 * k) % M.box == 0) {
-                        const uint32_t dst = st + (uint32_t)(32 * k + lane) * 128u;
-#pragma unroll
-                        for (int s = 0; s < 4; ++s) tma_load_3d(dst + (uint32_t)s * kSlice, &M.lat, 0, (int32_t)row[k], s, bar);
-                        tma_load_2d(dst + 4 * kSlice, &M.rope, 0, (int32_t)row[k], bar);
+                        for (int s = 0; s < 4; ++s) tma_load_3d(dst + (uint32_t)s * kSlice, &M.lat, 0, first, s, bar);
+                        tma_load_2d(dst + 4 * kSlice, &M.rope, 0, first, bar);
                     }
+                }
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k)
@@ -281,7 +264,7 @@ __device__ __forceinline__ bool tma_role(const LatentDecodeArgs &a, const Maps &
                         for (int e = 0; e < 5 * 8; ++e)
                             asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(st + (uint32_t)(e >> 3) * kSlice + (uint32_t)(32 * k + lane) * 128u + 16u * (e & 7)), "r"(zero) : "memory");
                 fence_proxy_async_smem();
-                if (lane == 0) mbar_arrive(full);
+                if (elect_one()) mbar_arrive(full);
             }
             asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full) : "memory"); // for the scales
             mbar_arrive(full);                                                                           // and the plain stores
@@ -759,13 +742,9 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_tc_kernel(LatentDec
     const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
     uint8_t *sp = smem_raw + (base - raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    int64_t *s_at = reinterpret_cast<int64_t *>(sp + OFF_AT);
-    const int64_t nrb = Split::row_blocks(a.Lq, a.H), G = gridDim.x;
+    int64_t(&s_at)[3] = *reinterpret_cast<int64_t(*)[3]>(sp + OFF_AT);
     if (warp == 0) {
-        const int64_t T = Split::warp_total(a, 0, a.B, lane) * nrb;
-        int64_t b, before;
-        Split::warp_find(a, T * blockIdx.x / G, nrb, lane, &b, &before);
-        if (lane == 0) s_at[0] = b, s_at[1] = before, s_at[2] = T;
+        Walk::begin(a, lane, s_at);
     } else if (tid == 32) {
         for (int b = 0; b < NUM_BARS; ++b) {
             uint32_t count = 1;
@@ -781,15 +760,14 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_tc_kernel(LatentDec
     __syncthreads();
     tc_fence_after();
     const Ctx c{base, *reinterpret_cast<volatile uint32_t *>(sp + OFF_TMEM)};
-    const int64_t T = s_at[2];
-    const Walk walk{T * blockIdx.x / G, T * (blockIdx.x + 1) / G, s_at[0], s_at[1], nrb};
+    const Walk walk(a, s_at);
     bool ok = true;
     if (warp < kProdWarp0) ok = softmax_role(a, c, walk, warp, lane);
     else if (warp < kMmaWarp && !maps.box) ok = copy_role(a, c, walk, warp - kProdWarp0, lane);
     else if (warp == kProdWarp0) ok = tma_role(a, maps, c, walk, lane);
-    else if (warp == kMmaWarp && lane == 0) ok = mma_role(a, c, walk);
+    else if (warp == kMmaWarp && elect_one()) ok = mma_role(a, c, walk);
     if (!ok) flag_error(a.err, CSA_DEVERR_TIMEOUT);
-    if (warp == kMmaWarp && lane == 0) { // every MMA completes before TMEM is released
+    if (warp == kMmaWarp && elect_one()) { // every MMA completes before TMEM is released
         mma_commit(c.bar(B_FINAL));
         if (!mbar_wait(c.bar(B_FINAL), 0)) flag_error(a.err, CSA_DEVERR_TIMEOUT);
     }
@@ -804,11 +782,9 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_tc_kernel(LatentDec
 
 bool latent_decode_tc_eligible(int R, int rd) { return R == kR && rd == kRd; }
 
-size_t latent_decode_tc_workspace(int64_t B, int Lq, int H, int64_t max_len, int *grid)
+size_t latent_decode_tc_workspace(int64_t B, int Lq, int H, int64_t max_len, int *grid, int *par)
 {
-    const int64_t tiles = (max_len + kKT - 1) / kKT, work = B * Split::row_blocks(Lq, H) * (tiles < 1 ? 1 : tiles);
-    const int64_t most = device_sms();
-    *grid = (int)(work < most ? work : most);
+    Split::plan(B, Lq, H, max_len, device_sms(), grid, par);
     return (size_t)*grid * 2 * kRB * (kR + 4) * sizeof(float);
 }
 

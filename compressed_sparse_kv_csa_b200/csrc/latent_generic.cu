@@ -51,25 +51,18 @@ constexpr int kMaxNV = 16; // R <= 512
 __global__ void __launch_bounds__(32 * kWarps) latent_decode_generic_kernel(LatentDecodeArgs a)
 {
     extern __shared__ float sm[];
-    __shared__ int64_t s_at[3]; // sequence, tiles before it, tiles of the whole call
+    __shared__ int64_t s_at[3];
     __shared__ int ok[kKT];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int rd = a.rows.rope_dims, R = a.rows.c - rd, c = a.rows.c, ld = c + 1;
     float *kt = sm, *qs = sm + kKT * ld; // [kKT, ld], [kRB, c]
-    const int64_t nrb = Split::row_blocks(a.Lq, a.H), G = gridDim.x;
-    if (warp == 0) {
-        const int64_t T = Split::warp_total(a, 0, a.B, lane) * nrb;
-        int64_t b, before;
-        Split::warp_find(a, T * blockIdx.x / G, nrb, lane, &b, &before);
-        if (lane == 0) s_at[0] = b, s_at[1] = before, s_at[2] = T;
-    }
+    if (warp == 0) LatentWalk<kRB, kKT>::begin(a, lane, s_at);
     __syncthreads();
-    const int64_t T = s_at[2], end = T * (blockIdx.x + 1) / G;
-    int64_t at = T * blockIdx.x / G, b = s_at[0], before = s_at[1];
-    while (at < end && b < a.B) {
-        const int64_t tiles = Split::tiles(a, b);
-        const int rb = (int)((at - before) / tiles);
-        const int64_t t0 = (at - before) % tiles, t1 = min(tiles, t0 + end - at);
+    LatentWalk<kRB, kKT> walk(a, s_at);
+    LatentRun run;
+    while (walk.next(a, run)) {
+        const int64_t b = run.b, t0 = run.t0, t1 = run.t1;
+        const int rb = run.rb;
         // the block's queries
         const int row0 = rb * kRB, n_rows = min(kRB, a.Lq * a.H - row0);
         __syncthreads();
@@ -117,7 +110,7 @@ __global__ void __launch_bounds__(32 * kWarps) latent_decode_generic_kernel(Late
                 tile_step<kMaxNV>(qs + r * c, kt, ld, c, kt, ld, R, a.scale * kLog2e, seen, lane, m[u], l[u], acc[u]);
             }
         }
-        const bool first = t0 == 0, whole = first && t1 == tiles;
+        const bool first = run.first, whole = run.whole;
 #pragma unroll
         for (int u = 0; u < kRowsPerWarp; ++u) {
             const int r = warp * kRowsPerWarp + u;
@@ -137,11 +130,6 @@ __global__ void __launch_bounds__(32 * kWarps) latent_decode_generic_kernel(Late
                     if (lane + 32 * i < R) p[4 + lane + 32 * i] = acc[u][i];
             }
         }
-        at += t1 - t0;
-        if (t1 == tiles && rb + 1 == nrb) {
-            before += tiles * nrb;
-            ++b;
-        }
     }
 }
 
@@ -150,7 +138,7 @@ __global__ void __launch_bounds__(32 * kWarps) latent_decode_generic_kernel(Late
 // m = max m_i, l = sum 2^(m_i - m) l_i, O = sum 2^(m_i - m) O_i; the output is O / l.
 constexpr int kMaxParts = 512;
 
-template <int RB, int KT> __global__ void __launch_bounds__(128) latent_merge_kernel(LatentDecodeArgs a, int64_t G)
+template <int RB, int KT> __global__ void __launch_bounds__(128) latent_merge_kernel(LatentDecodeArgs a)
 {
     __shared__ int64_t s_at[2];
     __shared__ float red[4], weight[kMaxParts];
@@ -159,21 +147,22 @@ template <int RB, int KT> __global__ void __launch_bounds__(128) latent_merge_ke
     const int r = (int)(blockIdx.x % rows), rb = r / RB;
     const int R = a.rows.c - a.rows.rope_dims;
     using Split = LatentSplit<RB, KT>;
-    const int64_t nrb = Split::row_blocks(a.Lq, a.H);
+    const int64_t nrb = a.par > 1 ? 1 : Split::row_blocks(a.Lq, a.H), G = a.grid / a.par;
     if (tid < 64) { // tiles before this sequence (warp 0), from it on (warp 1)
         const int64_t s = tid < 32 ? Split::warp_total(a, 0, b, lane) : Split::warp_total(a, b, a.B, lane);
         if (lane == 0) s_at[tid >> 5] = s * nrb;
     }
     __syncthreads();
-    const int64_t tiles = Split::tiles(a, b), T = s_at[0] + s_at[1], s0 = s_at[0] + rb * tiles, s1 = s0 + tiles - 1;
-    // the CTAs that hold the run's first and last tile: the largest i with floor(i T / G) <= tile
+    const int64_t tiles = Split::tiles(a, b), T = s_at[0] + s_at[1], s0 = s_at[0] + (a.par > 1 ? 0 : rb * tiles), s1 = s0 + tiles - 1;
+    // the CTAs (or groups) that hold the run's first and last tile: the largest i with floor(i T / G) <= tile
     const int64_t i0 = ((s0 + 1) * G - 1) / T, i1 = ((s1 + 1) * G - 1) / T;
     if (i0 == i1) return; // finished by the CTA that holds it
     const int64_t ld = R + 4;
     const int n = (int)(i1 - i0 + 1);
     // part k: slot 2 i + 1 where the run begins, slot 2 i behind; a CTA without tiles has none
-    const float *first = a.part + ((2 * i0 + 1) * RB + (r % RB)) * ld, *rest = a.part + (2 * i0 * RB + (r % RB)) * ld;
-    auto part = [&](int k) { return k == 0 ? first : rest + (int64_t)k * 2 * RB * ld; };
+    const int64_t cta0 = i0 * a.par + (a.par > 1 ? rb : 0), step = 2 * (int64_t)a.par * RB * ld;
+    const float *first = a.part + ((2 * cta0 + 1) * RB + (r % RB)) * ld, *rest = a.part + (2 * cta0 * RB + (r % RB)) * ld;
+    auto part = [&](int k) { return k == 0 ? first : rest + k * step; };
     float m = -INFINITY, ml[kMaxParts / 128][2];
 #pragma unroll
     for (int u = 0; u < kMaxParts / 128; ++u) {
@@ -291,24 +280,21 @@ template <typename T> __global__ void __launch_bounds__(32 * kWarps) latent_pref
 
 } // namespace
 
-// Two CTAs of the split per SM at most (shared memory), as many as there are tiles when that is less.
-size_t latent_decode_generic_workspace(int64_t B, int Lq, int H, int R, int64_t max_len, int *grid)
+size_t latent_decode_generic_workspace(int64_t B, int Lq, int H, int R, int64_t max_len, int *grid, int *par)
 {
-    const int64_t tiles = (max_len + kKT - 1) / kKT, work = B * Split::row_blocks(Lq, H) * (tiles < 1 ? 1 : tiles);
-    const int64_t most = device_sms();
-    *grid = (int)(work < most ? work : most);
+    Split::plan(B, Lq, H, max_len, device_sms(), grid, par);
     return (size_t)*grid * 2 * kRB * (R + 4) * sizeof(float);
 }
 
-template <int RB, int KT> static cudaError_t launch_merge(const LatentDecodeArgs &a, int grid, cudaStream_t st)
+template <int RB, int KT> static cudaError_t launch_merge(const LatentDecodeArgs &a, cudaStream_t st)
 {
-    if (grid < 2) return cudaSuccess; // one CTA cuts no run
-    if (grid > kMaxParts) return cudaErrorInvalidValue;
-    latent_merge_kernel<RB, KT><<<(unsigned)(a.B * a.Lq * a.H), 128, 0, st>>>(a, grid);
+    if (a.grid == a.par) return cudaSuccess; // one CTA, or one group, cuts no run
+    if (a.grid > kMaxParts) return cudaErrorInvalidValue;
+    latent_merge_kernel<RB, KT><<<(unsigned)(a.B * a.Lq * a.H), 128, 0, st>>>(a);
     return cudaGetLastError();
 }
 
-cudaError_t launch_latent_merge_32x128(const LatentDecodeArgs &a, cudaStream_t st) { return launch_merge<32, 128>(a, a.grid, st); }
+cudaError_t launch_latent_merge_32x128(const LatentDecodeArgs &a, cudaStream_t st) { return launch_merge<32, 128>(a, st); }
 
 cudaError_t launch_latent_decode_generic(LatentDecodeArgs a, cudaStream_t st)
 {
@@ -318,7 +304,7 @@ cudaError_t launch_latent_decode_generic(LatentDecodeArgs a, cudaStream_t st)
     latent_decode_generic_kernel<<<(unsigned)a.grid, 32 * kWarps, smem, st>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_merge<kRB, kKT>(a, a.grid, st);
+    return launch_merge<kRB, kKT>(a, st);
 }
 
 template <typename T> static cudaError_t prefill_generic(const LatentPrefillArgs &a, cudaStream_t st)

@@ -402,10 +402,10 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_tc_kernel(LatentPr
     } else {
         regs_dec<kRegsRest>();
         if (warp == kTmaWarp) ok = tma_role(j, maps, base, lane);
-        else if (warp == kMmaWarp && lane == 0) ok = mma_role(j, base, tmem);
+        else if (warp == kMmaWarp && elect_one()) ok = mma_role(j, base, tmem);
     }
     if (!ok) flag_error(a.err, CSA_DEVERR_TIMEOUT);
-    if (warp == kMmaWarp && lane == 0) { // every MMA completes before TMEM is released
+    if (warp == kMmaWarp && elect_one()) { // every MMA completes before TMEM is released
         mma_commit(base + OFF_BAR + 8u * B_FINAL);
         if (!mbar_wait(base + OFF_BAR + 8u * B_FINAL, 0)) flag_error(a.err, CSA_DEVERR_TIMEOUT);
     }

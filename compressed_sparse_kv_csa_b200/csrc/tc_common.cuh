@@ -21,6 +21,15 @@ __device__ __forceinline__ uint32_t smem_u32(const void *p)
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
+// True on one lane of a converged warp.  The compiler keeps the operands of what the elected lane issues in
+// uniform registers, which it does not do behind a comparison of the lane's number.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 __device__ __forceinline__ uint64_t globaltimer()
 {
     uint64_t t;

@@ -253,6 +253,13 @@ def test_decode_splits(C, lens):
     run_decode(C, lens, 8, 1, 512, 64, 64, seed=len(lens))
 
 
+@pytest.mark.parametrize("R", [512, 256])
+def test_decode_many_row_blocks(C, R):
+    """More row blocks than lie side by side (40 of 32 rows), and some that do, over cut runs."""
+    run_decode(C, [700, 10, 300], 128, 10, R, 64, 64)
+    run_decode(C, [2000, 10, 900], 16, 5, R, 64, 64)
+
+
 @pytest.mark.parametrize("Lq", [4, 64])
 def test_decode_several_tokens_and_padding(C, Lq):
     """Tokens in front of position 0 see nothing: zeros and -inf (checked inside)."""
