@@ -164,23 +164,22 @@ template <int RB, int KT> struct LatentWalk {
     using Split = LatentSplit<RB, KT>;
     int64_t at, end, b, before, nrb; // nrb: row blocks within the runs (1 side by side)
     int rb0;                         // the CTA's row block side by side
-    static __device__ __forceinline__ void begin(const LatentDecodeArgs &a, int lane, int64_t (&out)[3])
+    static __device__ __forceinline__ void begin(const LatentDecodeArgs &a, int lane, int64_t (&out)[4])
     {
         const int64_t nrb = a.par > 1 ? 1 : Split::row_blocks(a.Lq, a.H), G = gridDim.x / a.par, i = blockIdx.x / a.par;
-        const int64_t T = Split::warp_total(a, 0, a.B, lane) * nrb;
+        const int64_t T = Split::warp_total(a, 0, a.B, lane) * nrb, at = T * i / G;
         int64_t b, before;
-        Split::warp_find(a, T * i / G, nrb, lane, &b, &before);
-        if (lane == 0) out[0] = b, out[1] = before, out[2] = T;
+        Split::warp_find(a, at, nrb, lane, &b, &before);
+        if (lane == 0) out[0] = b, out[1] = before, out[2] = at, out[3] = T * (i + 1) / G;
     }
-    __device__ __forceinline__ LatentWalk(const LatentDecodeArgs &a, const int64_t (&from)[3])
+    __device__ __forceinline__ LatentWalk(const LatentDecodeArgs &a, const int64_t (&from)[4])
     {
-        const int64_t G = gridDim.x / a.par, i = blockIdx.x / a.par, T = from[2];
         nrb = a.par > 1 ? 1 : Split::row_blocks(a.Lq, a.H);
         rb0 = (int)(blockIdx.x % a.par);
-        at = T * i / G;
-        end = T * (i + 1) / G;
         b = from[0];
         before = from[1];
+        at = from[2];
+        end = from[3];
     }
     __device__ __forceinline__ bool next(const LatentDecodeArgs &a, LatentRun &r)
     {

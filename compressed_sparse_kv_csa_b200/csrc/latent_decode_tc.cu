@@ -49,7 +49,7 @@ constexpr uint32_t OFF_Q = OFF_K + kStages * 5 * kSlice; // 4 slices, 1 of the r
 constexpr uint32_t OFF_SC = OFF_Q + 5 * kQSlice;
 constexpr uint32_t OFF_XCH = OFF_SC + kStages * kKT * 4;     // [2 buffers][4 key quarters][32 rows]
 constexpr uint32_t OFF_BAR = OFF_XCH + 2 * 4 * 32 * 4;
-constexpr uint32_t OFF_AT = OFF_BAR + 160;            // where the CTA's walk begins (3 x int64)
+constexpr uint32_t OFF_AT = OFF_BAR + 160;            // where the CTA's walk begins (4 x int64)
 constexpr uint32_t OFF_TMEM = OFF_AT + 32;
 constexpr uint32_t SMEM_ALLOC = OFF_TMEM + 64 + 1024;
 static_assert(SMEM_ALLOC <= 232448, "shared memory per block");
@@ -742,9 +742,12 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_tc_kernel(LatentDec
     const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
     uint8_t *sp = smem_raw + (base - raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    int64_t(&s_at)[3] = *reinterpret_cast<int64_t(*)[3]>(sp + OFF_AT);
+    int64_t(&s_at)[4] = *reinterpret_cast<int64_t(*)[4]>(sp + OFF_AT);
     if (warp == 0) {
         Walk::begin(a, lane, s_at);
+    } else if (tid == 64 && maps.box) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.lat));
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.rope));
     } else if (tid == 32) {
         for (int b = 0; b < NUM_BARS; ++b) {
             uint32_t count = 1;
@@ -760,6 +763,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_tc_kernel(LatentDec
     __syncthreads();
     tc_fence_after();
     const Ctx c{base, *reinterpret_cast<volatile uint32_t *>(sp + OFF_TMEM)};
+    cudaTriggerProgrammaticLaunchCompletion(); // the merge may come up
     const Walk walk(a, s_at);
     bool ok = true;
     if (warp < kProdWarp0) ok = softmax_role(a, c, walk, warp, lane);

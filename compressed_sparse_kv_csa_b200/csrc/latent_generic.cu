@@ -51,7 +51,8 @@ constexpr int kMaxNV = 16; // R <= 512
 __global__ void __launch_bounds__(32 * kWarps) latent_decode_generic_kernel(LatentDecodeArgs a)
 {
     extern __shared__ float sm[];
-    __shared__ int64_t s_at[3];
+    cudaTriggerProgrammaticLaunchCompletion(); // the merge may come up
+    __shared__ int64_t s_at[4];
     __shared__ int ok[kKT];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int rd = a.rows.rope_dims, R = a.rows.c - rd, c = a.rows.c, ld = c + 1;
@@ -156,6 +157,9 @@ template <int RB, int KT> __global__ void __launch_bounds__(128) latent_merge_ke
     const int64_t tiles = Split::tiles(a, b), T = s_at[0] + s_at[1], s0 = s_at[0] + (a.par > 1 ? 0 : rb * tiles), s1 = s0 + tiles - 1;
     // the CTAs (or groups) that hold the run's first and last tile: the largest i with floor(i T / G) <= tile
     const int64_t i0 = ((s0 + 1) * G - 1) / T, i1 = ((s1 + 1) * G - 1) / T;
+    // launched beside the kernel that writes the parts: every block waits for it, those with nothing to do too, since
+    // what follows in the stream waits for this kernel alone
+    cudaGridDependencySynchronize();
     if (i0 == i1) return; // finished by the CTA that holds it
     const int64_t ld = R + 4;
     const int n = (int)(i1 - i0 + 1);
@@ -290,8 +294,17 @@ template <int RB, int KT> static cudaError_t launch_merge(const LatentDecodeArgs
 {
     if (a.grid == a.par) return cudaSuccess; // one CTA, or one group, cuts no run
     if (a.grid > kMaxParts) return cudaErrorInvalidValue;
-    latent_merge_kernel<RB, KT><<<(unsigned)(a.B * a.Lq * a.H), 128, 0, st>>>(a);
-    return cudaGetLastError();
+    // its blocks come up while the parts are written, and wait for them
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(a.B * a.Lq * a.H));
+    cfg.blockDim = dim3(128);
+    cfg.stream = st;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, latent_merge_kernel<RB, KT>, a);
 }
 
 cudaError_t launch_latent_merge_32x128(const LatentDecodeArgs &a, cudaStream_t st) { return launch_merge<32, 128>(a, st); }
