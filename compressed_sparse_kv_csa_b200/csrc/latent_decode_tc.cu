@@ -40,7 +40,11 @@ namespace {
 using namespace tc;
 
 constexpr int kR = 512, kRd = 64, kRB = 32, kKT = 128, kStages = 2;
-constexpr int kSoftThreads = 256, kProdWarp0 = 8, kMmaWarp = 10, kThreads = 11 * 32;
+constexpr int kSoftThreads = 256, kProdWarp0 = 8, kMmaWarp = 10, kThreads = 384; // whole warpgroups, for the register split
+// Of the registers that the block is launched with (168 a thread, checked on the host), the two softmax warpgroups take 192
+// a thread and the other leaves 120.
+constexpr int kRegs = 168, kRegsSoft = 192, kRegsRest = 120;
+static_assert(256 * kRegsSoft + 128 * kRegsRest <= kThreads * kRegs, "register split");
 // operand tiles of 128-byte rows, 128-byte swizzle: 64 rows of q and v, 128 keys
 constexpr uint32_t kQSlice = 8192, kPTile = 8192, kSlice = 16384;
 constexpr uint32_t OFF_P = 0;                         // v: two buffers
@@ -397,6 +401,10 @@ struct Meet {
     __device__ __forceinline__ bool sync()
     {
         mbar_arrive(bar);
+        return wait();
+    }
+    __device__ __forceinline__ bool wait() // after the arrival
+    {
         const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, phase));
         phase ^= 1;
         return ok;
@@ -532,9 +540,13 @@ __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, const Ct
     Meet all{c.bar(B_ALL), 0}, rows{c.bar(B_ROWS + g), 0}; // the eight warps; those that share the rows
     // one value of the row from each quarter of the keys, in the quarters' order, so that all reduce them alike
     const uint32_t xch = c.base + OFF_XCH + 4u * (uint32_t)row;
-    auto put = [&](uint32_t buf, float v) {
+    auto put_part = [&](uint32_t buf, float v) {
         if (part == 0) asm volatile("st.shared.f32 [%0], %1;" ::"r"(xch + 512u * buf + 128u * (uint32_t)kq), "f"(v) : "memory");
-        return rows.sync();
+        mbar_arrive(rows.bar);
+    };
+    auto put = [&](uint32_t buf, float v) {
+        put_part(buf, v);
+        return rows.wait();
     };
     auto get = [&](uint32_t buf, float (&v)[4]) {
 #pragma unroll
@@ -561,15 +573,11 @@ __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, const Ct
         bool begun = seen <= run.t0 * kKT;  // the row has a reference, or needs none here
         for (int64_t t = run.t0; t < run.t1; ++t, ++n) {
             const uint32_t buf = n & 1;
-            if (!__all_sync(0xffffffffu, mbar_wait(c.bar(B_S + buf), (n >> 1) & 1) && mbar_wait(c.bar(B_KFULL + n % kStages), (n / kStages) & 1)))
-                return false;
-            tc_fence_after();
+            if (!__all_sync(0xffffffffu, mbar_wait(c.bar(B_KFULL + n % kStages), (n / kStages) & 1))) return false;
             float2 z[8], s[8], v[8];
             bool odd = (t + 1) * kKT > seen_least; // some key may not be seen by some row
             {
                 float2 sn[16], sr[16], sk[16];
-                tmem_ld32_pairs(tw + kColSn + 64u * buf + 32u * (uint32_t)sub, sn);
-                tmem_ld32_pairs(tw + kColSr + 64u * buf + 32u * (uint32_t)sub, sr);
                 const uint32_t sc = c.base + OFF_SC + (n % kStages) * kKT * 4 + 128u * (uint32_t)kq;
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
@@ -577,6 +585,15 @@ __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, const Ct
                                  : "=f"(sk[2 * e].x), "=f"(sk[2 * e].y), "=f"(sk[2 * e + 1].x), "=f"(sk[2 * e + 1].y)
                                  : "r"(sc + 16u * e)
                                  : "memory");
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    s[e] = part ? sk[8 + e] : sk[e];
+                    odd |= __float_as_uint(s[e].x) == kNoKey || __float_as_uint(s[e].y) == kNoKey;
+                }
+                if (!__all_sync(0xffffffffu, mbar_wait(c.bar(B_S + buf), (n >> 1) & 1))) return false;
+                tc_fence_after();
+                tmem_ld32_pairs(tw + kColSn + 64u * buf + 32u * (uint32_t)sub, sn);
+                tmem_ld32_pairs(tw + kColSr + 64u * buf + 32u * (uint32_t)sub, sr);
                 tmem_ld_wait();
 #pragma unroll
                 for (int e = 0; e < 16; ++e) sn[e] = fma2(sn[e], sk[e], sr[e]);
@@ -584,9 +601,7 @@ __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, const Ct
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const float2 send = part ? sn[e] : sn[8 + e], keep = part ? sn[8 + e] : sn[e];
-                    s[e] = part ? sk[8 + e] : sk[e];
                     z[e] = add2(keep, make_float2(other_part(send.x), other_part(send.y)));
-                    odd |= __float_as_uint(s[e].x) == kNoKey || __float_as_uint(s[e].y) == kNoKey;
                 }
             }
             uint32_t open = 0xffffu; // bit e: key e is seen
@@ -631,7 +646,10 @@ __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, const Ct
             weigh();
             // a row without a reference, or whose p leave fp32 (scales far below those that it was set by), takes one
             top = begun && !(pt > 1e37f) ? top : INFINITY;
-            if (!put(buf, fmaxf(top, other_part(top)))) return false;
+            put_part(buf, fmaxf(top, other_part(top)));
+            uint32_t hi[4], lo[4];
+            split16(v, 16.f, hi, lo); // while the others arrive; seldom in vain
+            if (!rows.wait()) return false;
             get(buf, other);
             const float row_top = max4(other);
             const bool raise = row_top > kTop, low = row_top < kLow && row_top > 1e-30f;
@@ -673,11 +691,10 @@ __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, const Ct
                     tmem_st_wait();
                 }
                 weigh();
+                split16(v, 16.f, hi, lo);
             }
             l += pt;
             vs += vt;
-            uint32_t hi[4], lo[4];
-            split16(v, 16.f, hi, lo);
             const uint32_t at = c.base + OFF_P + kPTile * buf;
             sts4(at + sw128((uint32_t)(32 * g + r16), (uint32_t)key), hi);
             sts4(at + sw128((uint32_t)(32 * g + 16 + r16), (uint32_t)key), lo);
@@ -766,10 +783,19 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_tc_kernel(LatentDec
     cudaTriggerProgrammaticLaunchCompletion(); // the merge may come up
     const Walk walk(a, s_at);
     bool ok = true;
-    if (warp < kProdWarp0) ok = softmax_role(a, c, walk, warp, lane);
-    else if (warp < kMmaWarp && !maps.box) ok = copy_role(a, c, walk, warp - kProdWarp0, lane);
-    else if (warp == kProdWarp0) ok = tma_role(a, maps, c, walk, lane);
-    else if (warp == kMmaWarp && elect_one()) ok = mma_role(a, c, walk);
+    if (warp < kProdWarp0) {
+        regs_inc<kRegsSoft>();
+        ok = softmax_role(a, c, walk, warp, lane);
+    } else {
+        regs_dec<kRegsRest>();
+        if (warp == kMmaWarp) {
+            if (elect_one()) ok = mma_role(a, c, walk);
+        } else if (!maps.box) {
+            if (warp < kMmaWarp) ok = copy_role(a, c, walk, warp - kProdWarp0, lane);
+        } else if (warp == kProdWarp0) {
+            ok = tma_role(a, maps, c, walk, lane);
+        }
+    }
     if (!ok) flag_error(a.err, CSA_DEVERR_TIMEOUT);
     if (warp == kMmaWarp && elect_one()) { // every MMA completes before TMEM is released
         mma_commit(c.bar(B_FINAL));
@@ -825,6 +851,10 @@ cudaError_t launch_latent_decode_tc(const LatentDecodeArgs &a, cudaStream_t st)
         return cudaErrorNotSupported;
     cudaError_t e = cudaFuncSetAttribute(latent_decode_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_ALLOC);
     if (e != cudaSuccess) return e;
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, latent_decode_tc_kernel);
+    if (e != cudaSuccess) return e;
+    if (fa.numRegs != kRegs) return cudaErrorInvalidConfiguration; // the register split would wait for ever
     latent_decode_tc_kernel<<<(unsigned)a.grid, kThreads, SMEM_ALLOC, st>>>(a, maps);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;

@@ -199,15 +199,20 @@ template <int RB, int KT> __global__ void __launch_bounds__(128) latent_merge_ke
     const float inv = l != 0.f ? 1.f / l : 0.f;
     for (int j = 4 * tid; j < R; j += 512) {
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int k = 0; k < n; ++k) {
-            const float w = weight[k];
-            if (w == 0.f) continue; // nothing was seen there, or nothing was written
-            const float4 v = __ldcs(reinterpret_cast<const float4 *>(part(k) + 4 + j));
-            acc.x = fmaf(w, v.x, acc.x);
-            acc.y = fmaf(w, v.y, acc.y);
-            acc.z = fmaf(w, v.z, acc.z);
-            acc.w = fmaf(w, v.w, acc.w);
+        for (int k0 = 0; k0 < n; k0 += 8) { // 8 loads on their way together
+            float4 v[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) v[u] = __ldcs(reinterpret_cast<const float4 *>(part(min(k0 + u, n - 1)) + 4 + j));
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const float w = k0 + u < n ? weight[k0 + u] : 0.f;
+                if (w != 0.f) { // else nothing was seen there, or nothing was written
+                    acc.x = fmaf(w, v[u].x, acc.x);
+                    acc.y = fmaf(w, v[u].y, acc.y);
+                    acc.z = fmaf(w, v[u].z, acc.z);
+                    acc.w = fmaf(w, v[u].w, acc.w);
+                }
+            }
         }
         st4(a.o, (int64_t)blockIdx.x * R + j, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
     }

@@ -104,9 +104,6 @@ __device__ __forceinline__ uint32_t pk_bf16(float lo, float hi)
     return *reinterpret_cast<uint32_t *>(&h);
 }
 
-template <int N> __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N> __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
-
 // Two fp32 operations in one instruction.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
 {

@@ -21,6 +21,11 @@ __device__ __forceinline__ uint32_t smem_u32(const void *p)
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
+// Registers of a warpgroup (all four warps of it).  What the warpgroups of a block hold together must not exceed what
+// the block was launched with: its threads x the kernel's registers.
+template <int N> __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
 // True on one lane of a converged warp.  The compiler keeps the operands of what the elected lane issues in
 // uniform registers, which it does not do behind a comparison of the lane's number.
 __device__ __forceinline__ bool elect_one()
