@@ -25,8 +25,8 @@
 // 680 more cycles of the chain below; measured 5,100 cycles a tile.)  One exchange a tile, of the rows' largest v,
 // lets the softmax warps decide alike whether a reference moves.
 //
-// Roles: warps 0-7 softmax and output; warp 8 copies the keys by TMA, in boxes of a page or of 128 rows (with
-// pages that no box fits, warps 8 and 9 by cp.async); warp 10 MMA.  Two stages of 80 KB.  Rows that are not to
+// Roles: warps 0-7 softmax and output; warp 8 copies the keys by TMA, in boxes of a page or of 128 rows, and
+// warp 9 brings the tile after into L2 (with pages that no box fits, both copy by cp.async); warp 10 MMA.  Two stages of 80 KB.  Rows that are not to
 // be seen are zeros in shared memory: the probability 0 times whatever they held would not be 0.
 // Bound by HBM for up to 32 query rows a key, by the chain load - S - softmax - O over two stages above.
 #include "latent.cuh"
@@ -149,9 +149,13 @@ struct Ctx {
 struct Maps {
     CUtensorMap lat, rope;
     int box;             // rows of a box; 0: copied by cp.async
-    uint32_t page_tiles; // box = 128: tiles of a page
-    int shift;           // box < 128: log2 of the page's rows
-    uint32_t n_pages;    // pages that the cache has (a last partial one counts)
+    int shift;           // pages of less than a tile: log2 of their rows
+    uint32_t page_tiles; // pages of whole tiles: how many
+    uint32_t n_pages;    // pages that lie in the cache in full
+    // the latent part of a stage: bytes between slices of 128 channels and between groups of 8 rows.  Boxes of pages
+    // put the four slices of 8 rows side by side (one box whatever the page's size, 8 rows on an 8-row boundary);
+    // a contiguous run, which may begin anywhere, and cp.async put the rows of a slice side by side
+    uint32_t slice, group;
 };
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, uint32_t bytes) // 16 bytes, or zeros
@@ -159,123 +163,196 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void *src, uint32_t b
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
-// The scale of key row r of a stage; kNoKey where there is none.
-__device__ __forceinline__ void copy_scale(const LatentDecodeArgs &a, uint32_t dst, int64_t row)
-{
-    if (row < 0) asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst), "r"(kNoKey) : "memory");
-    else asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(a.rows.scale + row) : "memory");
-}
+__device__ __forceinline__ void sts1(uint32_t dst, uint32_t v) { asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst), "r"(v) : "memory"); }
 
-// Keys by TMA (warp 8).  A box is a page, or 128 rows of a larger page or of a contiguous run.
-__device__ __forceinline__ bool tma_role(const LatentDecodeArgs &a, const Maps &M, const Ctx &c, Walk walk, int lane)
+// The boxes of a run's tiles: lane i has box i.  Everything here is on the way between a free stage and its copies,
+// so a tile costs a lane one page number, loaded two tiles ahead and untouched before (behind a busy memory a
+// lookup takes as long as a tile).
+struct Boxes {
+    const LatentDecodeArgs &a;
+    const Maps &M;
+    const int32_t *table;
+    int64_t base, seen, t1;
+    int lane, n; // boxes of a tile
+    __device__ __forceinline__ Boxes(const LatentDecodeArgs &a_, const Maps &M_, int lane_) : a(a_), M(M_), lane(lane_), n(kKT / M_.box) {}
+    __device__ __forceinline__ void begin(const LatentRun &run)
+    {
+        table = a.map.pages + (a.map.pages ? run.b * a.map.max_pages : 0);
+        base = a.map.first(run.b); // without pages: the row of position 0
+        seen = latent_visible(a, run.b, a.Lq - 1);
+        t1 = run.t1;
+    }
+    __device__ __forceinline__ int32_t page(int64_t t) const
+    {
+        int32_t p = -1;
+        if (a.map.pages && lane < n && t < t1) {
+            const uint32_t i = M.box == kKT ? (uint32_t)t / M.page_tiles : ((uint32_t)t * kKT + lane * M.box) >> M.shift;
+            if (i < (uint32_t)a.map.max_pages) p = __ldg(table + i);
+        }
+        return p;
+    }
+    // First row of this lane's box, or -1 when not all of its rows are there to be seen.
+    __device__ __forceinline__ int32_t row(int64_t t, int32_t page) const
+    {
+        int64_t r = base + t * kKT;
+        bool ok = seen >= t * kKT + (lane + 1) * M.box;
+        if (a.map.pages) {
+            r = (int64_t)(uint32_t)page * a.map.page_rows + (M.box == kKT ? (uint32_t)t % M.page_tiles * kKT : 0u);
+            ok = ok && (uint32_t)page < M.n_pages;
+        } else {
+            ok = ok && r >= 0 && r + kKT <= a.rows.n;
+        }
+        return ok ? (int32_t)r : -1;
+    }
+    __device__ __forceinline__ bool whole(int32_t row) const { return !__any_sync(0xffffffffu, lane < n && row < 0); }
+};
+
+// Keys by TMA (warp 8).
+__device__ __forceinline__ bool tma_role(const LatentDecodeArgs &a, const Maps &M, const Ctx &c, Walk walk, volatile uint32_t *issued, int lane)
 {
     LatentRun run;
     uint32_t n = 0, tails = 0; // tiles so far, those with rows that are not to be seen
     bool ok = true;
+    Boxes B(a, M, lane);
+    const bool paged = a.map.pages != nullptr;
     while (ok && walk.next(a, run)) {
-        const int64_t seen = latent_visible(a, run.b, a.Lq - 1);
-        // Page numbers are loaded two tiles ahead of their use, and nothing touches them before: behind a busy memory a
-        // lookup takes as long as a tile.  Every instruction counts here: the copies of a tile wait for this warp.
-        const int64_t base = a.map.first(run.b); // without pages: the row of position 0
-        const int32_t *table = a.map.pages + (a.map.pages ? run.b * a.map.max_pages : 0);
-        const uint32_t max_pages = (uint32_t)a.map.max_pages, rows_n = (uint32_t)a.rows.n;
-        auto fetch = [&](int64_t t, int32_t (&page)[4]) {
+        B.begin(run);
+        auto scales = [&](int64_t t, float (&s)[4]) { // contiguous: a tile ahead, in registers
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                page[k] = -1;
-                const uint32_t i = M.box == kKT ? (uint32_t)t / M.page_tiles : ((uint32_t)t * kKT + 32 * k + lane) >> M.shift;
-                if (a.map.pages && (k == 0 || M.box < kKT) && t < run.t1 && i < max_pages) page[k] = __ldg(table + i);
+                const int64_t r = B.base + t * kKT + 32 * k + lane;
+                s[k] = 0.f;
+                if (!paged && t < run.t1 && r >= 0 && r < a.rows.n) s[k] = __ldg(a.rows.scale + r);
             }
         };
-        int32_t now[4], next[4];
-        fetch(run.t0, now);
-        fetch(run.t0 + 1, next);
+        int32_t now = B.page(run.t0), next = B.page(run.t0 + 1);
+        float sc_next[4];
+        scales(run.t0, sc_next);
         for (int64_t t = run.t0; t < run.t1; ++t, ++n) {
-            int32_t row[4];
-            const int n_seen = (int)min((int64_t)kKT, seen - t * kKT); // keys of this tile
-            if (M.box == kKT) {
-                // one run of rows: r0 .. r0 + 127
-                const int64_t r0 = !a.map.pages ? base + t * kKT
-                                   : (uint32_t)now[0] < M.n_pages ? (int64_t)now[0] * a.map.page_rows + (uint32_t)t % M.page_tiles * kKT : -kKT;
+            const int32_t page = now, row = B.row(t, now);
+            const bool whole = B.whole(row);
+            float sc_now[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int64_t r = r0 + 32 * k + lane;
-                    row[k] = 32 * k + lane < n_seen && (uint64_t)r < rows_n ? (int32_t)r : -1;
-                }
-            } else {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint32_t in_page = ((uint32_t)(32 * k) + lane) & ((1u << M.shift) - 1u);
-                    const uint32_t r = ((uint32_t)now[k] << M.shift) + in_page;
-                    row[k] = 32 * k + lane < n_seen && (uint32_t)now[k] < M.n_pages && r < rows_n ? (int32_t)r : -1;
-                }
-            }
-            const bool tail = __any_sync(0xffffffffu, row[0] < 0 || row[1] < 0 || row[2] < 0 || row[3] < 0);
-            if (tail) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (row[k] < 0 && 32 * k + lane < n_seen) flag_error(a.err, CSA_DEVERR_INDEX);
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) now[k] = next[k];
-            fetch(t + 2, next);
+            for (int k = 0; k < 4; ++k) sc_now[k] = sc_next[k];
+            now = next;
+            next = B.page(t + 2);
+            scales(t + 1, sc_next);
             if (n >= kStages && !__all_sync(0xffffffffu, mbar_wait(c.bar(B_KEMPTY + n % kStages), ((n / kStages) & 1) ^ 1))) {
                 ok = false;
                 break;
             }
-            const uint32_t st = c.stage(n), full = c.bar(B_KFULL + n % kStages);
-            const uint32_t bar = tail ? c.bar(B_TAIL) : full;
-            if (M.box == kKT) {
-                const int32_t first = __shfl_sync(0xffffffffu, row[0], 0);
-                if (elect_one()) {
-                    mbar_arrive_expect_tx(bar, first < 0 ? 0u : kKT * 640u);
-                    if (first >= 0) {
-                        tma_load_3d(st, &M.lat, 0, first, 0, bar);
-                        tma_load_2d(st + 4 * kSlice, &M.rope, 0, first, bar);
+            const uint32_t st = c.stage(n), full = c.bar(B_KFULL + n % kStages), sc = c.base + OFF_SC + (n % kStages) * kKT * 4;
+            if (whole && paged) {
+                if (elect_one()) mbar_arrive_expect_tx(full, kKT * 644u);
+                for (int i = 0; i < B.n; ++i) {
+                    const int32_t r = __shfl_sync(0xffffffffu, row, i);
+                    if (elect_one()) {
+                        tma_load_4d(st + (uint32_t)(i * M.box) * 512u, &M.lat, 0, 0, 0, r >> 3, full);
+                        tma_load_2d(st + 4 * kSlice + (uint32_t)(i * M.box) * 128u, &M.rope, 0, r, full);
+                        bulk_load(sc + (uint32_t)(i * M.box) * 4u, a.rows.scale + r, (uint32_t)M.box * 4u, full);
                     }
                 }
-            } else { // box i begins at key i * box: lane (i * box) % 32 of row[i * box / 32]
-                const bool begins = lane % M.box == 0;
-                uint32_t boxes = 0;
+            } else if (whole) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) sts1(sc + 4u * (uint32_t)(32 * k + lane), __float_as_uint(sc_now[k]));
+                const int32_t r = __shfl_sync(0xffffffffu, row, 0);
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(full, kKT * 640u);
+                    tma_load_3d(st, &M.lat, 0, r, 0, full);
+                    tma_load_2d(st + 4 * kSlice, &M.rope, 0, r, full);
+                }
+            } else {
+                // some rows are not to be seen, or not there: row by row, their places zeroed once no box is on its way
+                int64_t key_row[4];
+                const int64_t n_seen = B.seen - t * kKT;
+                bool refused = false;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int j = 32 * k + lane;
+                    const int32_t p = __shfl_sync(0xffffffffu, page, j / M.box);
+                    key_row[k] = j < n_seen ? a.map.row(p, B.base, (uint32_t)(t * kKT + j)) : -1;
+                    refused |= j < n_seen && key_row[k] < 0;
+                }
+                if (refused) flag_error(a.err, CSA_DEVERR_INDEX);
+                uint32_t bytes = 0;
+                if (!paged && __any_sync(0xffffffffu, key_row[0] >= 0 || key_row[1] >= 0 || key_row[2] >= 0 || key_row[3] >= 0)) {
+                    bytes = kKT * 640u; // the run may begin or end outside the cache: zeros
+                    if (elect_one()) {
+                        tma_load_3d(st, &M.lat, 0, (int32_t)(B.base + t * kKT), 0, c.bar(B_TAIL));
+                        tma_load_2d(st + 4 * kSlice, &M.rope, 0, (int32_t)(B.base + t * kKT), c.bar(B_TAIL));
+                    }
+                }
+                for (int i = 0; paged && i < B.n; ++i) { // boxes whose first row is there; the rest of them may reach past the cache (zeros)
+                    const int j = i * M.box, k = j >> 5;
+                    const int64_t r = __shfl_sync(0xffffffffu, k == 0 ? key_row[0] : k == 1 ? key_row[1] : k == 2 ? key_row[2] : key_row[3], j & 31);
+                    if (r < 0) continue;
+                    bytes += (uint32_t)M.box * 640u;
+                    if (elect_one()) {
+                        tma_load_4d(st + (uint32_t)j * 512u, &M.lat, 0, 0, 0, (int32_t)(r >> 3), c.bar(B_TAIL));
+                        tma_load_2d(st + 4 * kSlice + (uint32_t)j * 128u, &M.rope, 0, (int32_t)r, c.bar(B_TAIL));
+                    }
+                }
+                if (elect_one()) mbar_arrive_expect_tx(c.bar(B_TAIL), bytes);
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    boxes += (uint32_t)__popc(__ballot_sync(0xffffffffu, row[k] >= 0 && begins && (32 * k) % M.box == 0));
-                if (elect_one()) mbar_arrive_expect_tx(bar, boxes * (uint32_t)M.box * 640u);
-                for (int j = 0; j < kKT; j += M.box) {
-                    const int k = j >> 5;
-                    const int32_t first = __shfl_sync(0xffffffffu, k == 0 ? row[0] : k == 1 ? row[1] : k == 2 ? row[2] : row[3], j & 31);
-                    if (first >= 0 && elect_one()) {
-                        const uint32_t dst = st + (uint32_t)j * 128u;
-#pragma unroll
-                        for (int s = 0; s < 4; ++s) tma_load_3d(dst + (uint32_t)s * kSlice, &M.lat, 0, first, s, bar);
-                        tma_load_2d(dst + 4 * kSlice, &M.rope, 0, first, bar);
-                    }
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                copy_scale(a, c.base + OFF_SC + (n % kStages) * kKT * 4 + 4u * (uint32_t)(32 * k + lane), row[k]);
-            if (tail) { // rows that are not to be seen: zeros, written once no box is on its way
-                if (!__all_sync(0xffffffffu, mbar_wait(bar, tails & 1))) {
+                    sts1(sc + 4u * (uint32_t)(32 * k + lane), key_row[k] < 0 ? kNoKey : __float_as_uint(__ldg(a.rows.scale + key_row[k])));
+                if (!__all_sync(0xffffffffu, mbar_wait(c.bar(B_TAIL), tails & 1))) {
                     ok = false;
                     break;
                 }
                 ++tails;
-                const uint32_t zero = 0;
+                const uint32_t zero[4] = {0, 0, 0, 0};
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    if (row[k] < 0)
-                        for (int e = 0; e < 5 * 8; ++e)
-                            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(st + (uint32_t)(e >> 3) * kSlice + (uint32_t)(32 * k + lane) * 128u + 16u * (e & 7)), "r"(zero) : "memory");
+                    if (key_row[k] < 0) {
+                        const uint32_t j = (uint32_t)(32 * k + lane), at = (j >> 3) * M.group + (j & 7u) * 128u;
+                        for (uint32_t e = 0; e < 32; ++e) sts4(st + (e >> 3) * M.slice + at + 16u * (e & 7u), zero);
+                        for (uint32_t e = 0; e < 8; ++e) sts4(st + 4 * kSlice + j * 128u + 16u * e, zero);
+                    }
                 fence_proxy_async_smem();
+                __syncwarp();
                 if (elect_one()) mbar_arrive(full);
             }
-            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full) : "memory"); // for the scales
-            mbar_arrive(full);                                                                           // and the plain stores
+            if (lane == 0) *issued = n + 1;
         }
     }
-    asm volatile("cp.async.wait_all;" ::: "memory"); // nothing is in flight when the block ends
+    if (lane == 0) *issued = 0xffffffffu;
     return ok;
+}
+
+// The next tile into L2 (warp 9): its stage is not free yet when this one's is, and the way from HBM is most of what a
+// load takes.  It follows the tiles that warp 8 has asked for, and nothing waits for it: what it is too late for it
+// leaves out.
+__device__ __forceinline__ void prefetch_role(const LatentDecodeArgs &a, const Maps &M, Walk walk, const volatile uint32_t *issued, int lane)
+{
+    LatentRun run;
+    uint32_t n = 0;
+    Boxes B(a, M, lane);
+    while (walk.next(a, run)) {
+        B.begin(run);
+        int32_t next = B.page(run.t0 + 1);
+        for (int64_t t = run.t0; t < run.t1; ++t, ++n) {
+            const int32_t row = t + 1 < run.t1 ? B.row(t + 1, next) : -1;
+            next = B.page(t + 2);
+            uint32_t at = *issued;
+            const uint64_t t0 = globaltimer();
+            while (at <= n) {
+                __nanosleep(100);
+                if (globaltimer() - t0 > 2000000000ull) return;
+                at = *issued;
+            }
+            if (!__all_sync(0xffffffffu, at == n + 1) || !B.whole(row)) continue;
+            if (lane < B.n) asm volatile("prefetch.global.L2 [%0];" ::"l"(a.rows.scale + row));
+            for (int i = 0; i < B.n; ++i) {
+                const int32_t r = __shfl_sync(0xffffffffu, row, i);
+                if (elect_one()) {
+                    if (a.map.pages) tma_prefetch_4d(&M.lat, 0, 0, 0, r >> 3);
+                    else tma_prefetch_3d(&M.lat, 0, r, 0);
+                    tma_prefetch_2d(&M.rope, 0, r);
+                }
+            }
+        }
+    }
 }
 
 // Keys by cp.async (warps 8-9): warp w copies rows 64 w .. 64 w + 63 of a tile, 8 lanes a row of 128 bytes.
@@ -316,7 +393,11 @@ __device__ __forceinline__ bool copy_role(const LatentDecodeArgs &a, const Ctx &
             }
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                copy_scale(a, c.base + OFF_SC + (n % kStages) * kKT * 4 + 4u * (uint32_t)(64 * warp + 32 * h + lane), cur[h]);
+            {
+                const uint32_t dst = c.base + OFF_SC + (n % kStages) * kKT * 4 + 4u * (uint32_t)(64 * warp + 32 * h + lane);
+                if (cur[h] < 0) sts1(dst, kNoKey);
+                else asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(a.rows.scale + cur[h]) : "memory");
+            }
             asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(c.bar(B_KFULL + n % kStages)) : "memory");
             mbar_arrive(c.bar(B_KFULL + n % kStages)); // and for the plain stores
         }
@@ -339,13 +420,13 @@ __device__ __forceinline__ bool mbar_wait_either(uint32_t a, uint32_t pa, uint32
 // MMA issue (one thread).  S of tile n goes before O of tile n - 1, so that the softmax of one runs beside
 // the MMAs of the other; at a run's first tile O of the run before goes first, since its output has to
 // be read before the new queries are there.
-__device__ __forceinline__ bool mma_role(const LatentDecodeArgs &a, const Ctx &c, Walk walk)
+__device__ __forceinline__ bool mma_role(const LatentDecodeArgs &a, const Maps &M, const Ctx &c, Walk walk)
 {
     LatentRun run;
     uint32_t n = 0, runs = 0;
     bool pending = false, pending_first = false;
-    const Desc q_desc(sdesc_sw128(c.base + OFF_Q, 16, 1024)), k_desc(sdesc_sw128(c.base + OFF_K, 16, 1024));
-    const Desc p_desc(sdesc_sw128(c.base + OFF_P, 16, 1024)), v_desc(sdesc_sw128(c.base + OFF_K, kSlice, 1024));
+    const Desc q_desc(sdesc_sw128(c.base + OFF_Q, 16, 1024)), k_desc(sdesc_sw128(c.base + OFF_K, 16, M.group)), r_desc(sdesc_sw128(c.base + OFF_K, 16, 1024));
+    const Desc p_desc(sdesc_sw128(c.base + OFF_P, 16, 1024)), v_desc(sdesc_sw128(c.base + OFF_K, M.slice, M.group));
     auto output = [&](uint32_t k, bool first) { // O (+)= v code of tile k
         if (!mbar_wait(c.bar(B_P + (k & 1)), (k >> 1) & 1)) return false;
         tc_fence_after();
@@ -354,7 +435,7 @@ __device__ __forceinline__ bool mma_role(const LatentDecodeArgs &a, const Ctx &c
         for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                mma_ws<true>(c.tmem + kColO + 128u * h, dp.at(32u * kk), dv.at(2u * h * kSlice + 4096u * kk), IDESC_O, !first || kk > 0);
+                mma_ws<true>(c.tmem + kColO + 128u * h, dp.at(32u * kk), dv.at(2u * h * M.slice + 4u * kk * M.group), IDESC_O, !first || kk > 0);
         mma_commit(c.bar(B_KEMPTY + k % kStages));
         return true;
     };
@@ -376,16 +457,16 @@ __device__ __forceinline__ bool mma_role(const LatentDecodeArgs &a, const Ctx &c
             if (!mbar_wait(full, full_ph)) return false;
             fence_proxy_async_smem(); // cp.async writes for the generic proxy
             tc_fence_after();
-            const Desc dk = k_desc.at((n % kStages) * 5 * kSlice);
+            const Desc dk = k_desc.at((n % kStages) * 5 * kSlice), dr = r_desc.at((n % kStages) * 5 * kSlice + 4 * kSlice);
             const uint32_t buf = 64u * (n & 1);
 #pragma unroll
             for (int s = 0; s < 4; ++s)
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    mma_ws<true>(c.tmem + kColSn + buf, q_desc.at(s * kQSlice + 32u * kk), dk.at(s * kSlice + 32u * kk), IDESC_SN, (s | kk) != 0);
+                    mma_ws<true>(c.tmem + kColSn + buf, q_desc.at(s * kQSlice + 32u * kk), dk.at(s * M.slice + 32u * kk), IDESC_SN, (s | kk) != 0);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-                mma_ws<false>(c.tmem + kColSr + buf, q_desc.at(4 * kQSlice + 32u * kk), dk.at(4 * kSlice + 32u * kk), IDESC_SR, kk != 0);
+                mma_ws<false>(c.tmem + kColSr + buf, q_desc.at(4 * kQSlice + 32u * kk), dr.at(32u * kk), IDESC_SR, kk != 0);
             mma_commit(c.bar(B_S + (n & 1)));
             if (pending && !output(n - 1, pending_first)) return false;
             pending = true;
@@ -768,12 +849,13 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_tc_kernel(LatentDec
     } else if (tid == 32) {
         for (int b = 0; b < NUM_BARS; ++b) {
             uint32_t count = 1;
-            if (b >= B_KFULL && b < B_KFULL + kStages) count = maps.box ? 65 : 128; // each copying thread's copies, and itself; TMA
+            if (b >= B_KFULL && b < B_KFULL + kStages) count = maps.box ? 1 : 128; // TMA; each copying thread's copies, and itself
             if (b == B_P || b == B_P + 1 || b == B_Q || b == B_ALL) count = kSoftThreads;
             if (b == B_ROWS || b == B_ROWS + 1) count = kSoftThreads / 2;
             mbar_init(base + OFF_BAR + 8u * (uint32_t)b, count);
         }
         mbar_init_fence();
+        *reinterpret_cast<volatile uint32_t *>(sp + OFF_TMEM + 16) = 0;
     }
     if (warp == kMmaWarp) tmem_alloc(base + OFF_TMEM, kTmemCols);
     tc_fence_before();
@@ -782,6 +864,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_tc_kernel(LatentDec
     const Ctx c{base, *reinterpret_cast<volatile uint32_t *>(sp + OFF_TMEM)};
     cudaTriggerProgrammaticLaunchCompletion(); // the merge may come up
     const Walk walk(a, s_at);
+    volatile uint32_t *issued = reinterpret_cast<volatile uint32_t *>(sp + OFF_TMEM + 16); // tiles asked for
     bool ok = true;
     if (warp < kProdWarp0) {
         regs_inc<kRegsSoft>();
@@ -789,11 +872,13 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_tc_kernel(LatentDec
     } else {
         regs_dec<kRegsRest>();
         if (warp == kMmaWarp) {
-            if (elect_one()) ok = mma_role(a, c, walk);
+            if (elect_one()) ok = mma_role(a, maps, c, walk);
         } else if (!maps.box) {
             if (warp < kMmaWarp) ok = copy_role(a, c, walk, warp - kProdWarp0, lane);
         } else if (warp == kProdWarp0) {
-            ok = tma_role(a, maps, c, walk, lane);
+            ok = tma_role(a, maps, c, walk, issued, lane);
+        } else if (warp == kProdWarp0 + 1) {
+            prefetch_role(a, maps, walk, issued, lane);
         }
     }
     if (!ok) flag_error(a.err, CSA_DEVERR_TIMEOUT);
@@ -818,37 +903,52 @@ size_t latent_decode_tc_workspace(int64_t B, int Lq, int H, int64_t max_len, int
     return (size_t)*grid * 2 * kRB * (kR + 4) * sizeof(float);
 }
 
-// A row-major byte matrix [rows, slices * 128] seen as [slices][rows][128], read in boxes of box_rows rows of
-// box_slices slices with the 128-byte swizzle; rows outside read as zeros.
-static bool encode_slices(CUtensorMap *m, const void *base, int64_t rows, uint32_t slices, uint32_t box_rows, uint32_t box_slices)
+// Boxes with the 128-byte swizzle; what lies outside reads as zeros.
+static bool encode_u8(CUtensorMap *m, const void *base, int rank, const cuuint64_t *dims, const cuuint64_t *strides, const cuuint32_t *box)
 {
     PFN_cuTensorMapEncodeTiled_v12000 enc = tma::encoder();
-    if (!enc) return false;
-    const cuuint64_t dims[3] = {128, (cuuint64_t)rows, slices}, strides[2] = {(cuuint64_t)slices * 128, 128};
-    const cuuint32_t box[3] = {128, box_rows, box_slices}, estr[3] = {1, 1, 1};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, slices > 1 ? 3 : 2, const_cast<void *>(base), dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return enc && enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, (cuuint32_t)rank, const_cast<void *>(base), dims, strides, box, estr,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 cudaError_t launch_latent_decode_tc(const LatentDecodeArgs &a, cudaStream_t st)
 {
-    // a box is 128 rows of a contiguous run or of pages of whole tiles, or a page of 8, 16, 32 or 64 rows (a swizzle
-    // atom is 8 rows); other pages are copied row by row: 3,700 cycles of issue a tile where a box takes one
+    // a box is 128 rows of a contiguous run or of pages of whole tiles, or a page of 8, 16, 32 or 64 rows (in groups of 8,
+    // as the swizzle has them); other pages are copied row by row: 3,700 cycles of issue a tile where a box takes one
     Maps maps{};
     const int pr = a.map.page_rows;
+    const uint64_t n = (uint64_t)a.rows.n;
     maps.page_tiles = 1;
-    maps.box = !a.map.pages || pr % kKT == 0 ? kKT : (pr == 8 || pr == 16 || pr == 32 || pr == 64) ? pr : 0;
-    if (a.rows.n < 1 || a.rows.n >= ((int64_t)1 << 31)) maps.box = 0; // TMA coordinates are int32
-    if (maps.box && a.map.pages) {
-        maps.n_pages = (uint32_t)((a.rows.n + pr - 1) / pr);
-        if (maps.box == kKT) maps.page_tiles = (uint32_t)(pr / kKT);
-        else
-            while ((1 << maps.shift) < pr) ++maps.shift;
+    maps.slice = kSlice;
+    maps.group = 1024;
+    if (n >= 1 && n < (1ull << 31)) { // TMA coordinates are int32
+        if (!a.map.pages) maps.box = kKT;
+        else if (n % 8 == 0 && (reinterpret_cast<uintptr_t>(a.rows.scale) & 15u) == 0) // whole groups; scales as bulk copies
+            maps.box = pr % kKT == 0 ? kKT : (pr == 8 || pr == 16 || pr == 32 || pr == 64) ? pr : 0;
     }
-    if (maps.box && (!encode_slices(&maps.lat, a.rows.fp8, a.rows.n, kR / 128, (uint32_t)maps.box, maps.box == kKT ? kR / 128 : 1) ||
-                     !encode_slices(&maps.rope, a.rows.rope, a.rows.n, 1, (uint32_t)maps.box, 1)))
-        return cudaErrorNotSupported;
+    if (maps.box) {
+        const uint32_t rows = (uint32_t)maps.box;
+        bool ok;
+        if (a.map.pages) {
+            maps.n_pages = (uint32_t)(n / pr);
+            if (maps.box == kKT) maps.page_tiles = (uint32_t)(pr / kKT);
+            while ((1 << maps.shift) < pr) ++maps.shift;
+            maps.slice = 1024;
+            maps.group = 4096;
+            const cuuint64_t dims[4] = {128, 8, kR / 128, n / 8}, strides[3] = {kR, 128, 8 * kR};
+            const cuuint32_t box[4] = {128, 8, kR / 128, rows / 8};
+            ok = encode_u8(&maps.lat, a.rows.fp8, 4, dims, strides, box);
+        } else {
+            const cuuint64_t dims[3] = {128, n, kR / 128}, strides[2] = {kR, 128};
+            const cuuint32_t box[3] = {128, rows, kR / 128};
+            ok = encode_u8(&maps.lat, a.rows.fp8, 3, dims, strides, box);
+        }
+        const cuuint64_t dims[2] = {2 * kRd, n}, strides[1] = {2 * kRd};
+        const cuuint32_t box[2] = {2 * kRd, rows};
+        if (!ok || !encode_u8(&maps.rope, a.rows.rope, 2, dims, strides, box)) return cudaErrorNotSupported;
+    }
     cudaError_t e = cudaFuncSetAttribute(latent_decode_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_ALLOC);
     if (e != cudaSuccess) return e;
     cudaFuncAttributes fa;

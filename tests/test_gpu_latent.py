@@ -330,6 +330,42 @@ def test_decode_refused_pages_are_skipped(C, R):
     L.check_attention(o, lse, ref, R + 64, 64, V_STEP)
 
 
+def test_decode_runs_that_begin_or_end_outside_the_cache(C):
+    """Contiguous rows of which the first or the last lie outside are left out of the sums, and reported."""
+    rows = cache(C, 300, 512, 64)
+    q = torch.randn((3, 1, 8, 576), generator=rng(2)).to(BF16)
+    pos, off = ints(150, 200, 20), ints(-5, 211, 100000)
+    lse = torch.empty((3, 1, 8), device="cuda")
+    o = C.latent_attn_decode(q.cuda(), rows, pos, 0.05, 256, off=off, lse=lse)
+    assert C.csa_device_error() == C.CSA_DEVERR_INDEX
+    lat, rope = L.dequant(rows.fp8, rows.rope, rows.scale)
+    ref = L.decode(q, lat, rope, lambda b, s: int(off[b]) + s, pos.tolist(), 0.05, 256, rows.scale)
+    L.check_attention(o, lse, ref, 576, 256, V_STEP)
+
+
+@pytest.mark.parametrize("page", [8, 32, 256, 384])
+def test_decode_page_sizes(C, page):
+    """The other sizes that boxes are made of, in a cache of whole groups of 8 rows, and one that is not."""
+    run_decode(C, [1000, 385, 7], 16, 1, 512, 64, page)
+
+    run_decode(C, [100, 385, 7], 16, 1, 512, 64, page, rows=lambda n: cache(C, n + 5, 512, 64, 3))
+
+
+def test_decode_last_page_ends_behind_the_cache(C):
+    """A page of which only some rows are in the cache: the others are left out, and reported."""
+    for n in (40 * 8, 40 * 8 - 3):
+        rows = cache(C, n, 512, 64, 5)
+        pages = torch.tensor([[2, 0], [1, 2]], dtype=I32, device="cuda")  # pages of 128 rows; the third has 64 or 61
+        q = torch.randn((2, 1, 8, 576), generator=rng(2)).to(BF16)
+        pos = ints(255, 255)
+        lse = torch.empty((2, 1, 8), device="cuda")
+        o = C.latent_attn_decode(q.cuda(), rows, pos, 0.05, 256, pages=pages, page_rows=128, lse=lse)
+        assert C.csa_device_error() == C.CSA_DEVERR_INDEX
+        lat, rope = L.dequant(rows.fp8, rows.rope, rows.scale)
+        ref = L.decode(q, lat, rope, lambda b, s: L.row_of(pages.cpu(), 128, None, b, s), pos.tolist(), 0.05, 256, rows.scale)
+        L.check_attention(o, lse, ref, 576, 256, V_STEP)
+
+
 def test_decode_positions_out_of_any_range(C):
     rows = cache(C, 64, 512, 64)
     q = torch.randn((3, 2, 8, 576), generator=rng(2)).to(BF16)
