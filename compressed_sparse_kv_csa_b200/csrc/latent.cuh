@@ -99,8 +99,11 @@ __device__ __forceinline__ int64_t latent_visible(const LatentDecodeArgs &a, int
 // whatever the lengths are, and a CTA cuts at most the two runs at its ends: its run that starts inside
 // goes to slot 2i, the one that starts at its first tile but does not end here to slot 2i + 1; a run that
 // lies in one CTA is finished there.  A sequence that sees nothing has one (empty) tile, so its rows are
-// written too.
-template <int RB, int KT> struct LatentSplit {
+// written too.  What a run costs beside its tiles -- queries in, output out, the first tile's references -- counts as
+// COST tiles in front of its own (64 sequences of 1k to 16k keys: the CTAs with the short ones took 80 us where
+// the median took 54).
+template <int RB, int KT, int COST> struct LatentSplit {
+    static constexpr int kCost = COST;
     static __device__ __forceinline__ int64_t tiles(const LatentDecodeArgs &a, int64_t b)
     {
         const int64_t t = (latent_visible(a, b, a.Lq - 1) + KT - 1) / KT;
@@ -110,29 +113,29 @@ template <int RB, int KT> struct LatentSplit {
     // Grid and par for at most `most` CTAs; side by side where that leaves at most a tenth of them idle.
     static void plan(int64_t B, int Lq, int H, int64_t max_len, int most, int *grid, int *par)
     {
-        const int64_t nrb = row_blocks(Lq, H), t = (max_len + KT - 1) / KT, tiles = B * (t < 1 ? 1 : t);
+        const int64_t nrb = row_blocks(Lq, H), t = (max_len + KT - 1) / KT, tiles = B * (t < 1 ? 1 : t); // a CTA for each tile at most
         const bool side = nrb <= most && most / nrb * nrb * 10 >= 9 * (int64_t)most;
         *par = side ? (int)nrb : 1;
         const int64_t work = side ? tiles : tiles * nrb, groups = most / *par;
         *grid = (int)((work < groups ? work : groups) * *par);
     }
-    // Tiles of the sequences [0, b1), one warp.
+    static __device__ __forceinline__ int64_t length(const LatentDecodeArgs &a, int64_t b) { return tiles(a, b) + COST; }
+    // Lengths of the runs of the sequences [b0, b1), one warp.
     static __device__ __forceinline__ int64_t warp_total(const LatentDecodeArgs &a, int64_t b0, int64_t b1, int lane)
     {
         int64_t s = 0;
-        for (int64_t b = b0 + lane; b < b1; b += 32) s += tiles(a, b);
+        for (int64_t b = b0 + lane; b < b1; b += 32) s += length(a, b);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
         return s;
     }
-    // The sequence that holds tile `at` (in units of one row block's tiles scaled by nrb) and the
-    // tiles before it; one warp, every lane returns the same.
+    // The sequence whose nrb runs hold place `at`, and the length before them; one warp, every lane returns the same.
     static __device__ __forceinline__ void warp_find(const LatentDecodeArgs &a, int64_t at, int64_t nrb, int lane,
                                                      int64_t *b_out, int64_t *before)
     {
         int64_t base = 0;
         for (int64_t b0 = 0; b0 < a.B; b0 += 32) {
-            int64_t v = b0 + lane < a.B ? tiles(a, b0 + lane) * nrb : 0, inc = v;
+            int64_t v = b0 + lane < a.B ? length(a, b0 + lane) * nrb : 0, inc = v;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int64_t u = __shfl_up_sync(0xffffffffu, inc, o);
@@ -160,8 +163,7 @@ struct LatentRun {
 };
 
 // A CTA's walk over its runs.  One warp finds where it begins (begin()); then every role walks by itself.
-template <int RB, int KT> struct LatentWalk {
-    using Split = LatentSplit<RB, KT>;
+template <class Split> struct LatentWalk {
     int64_t at, end, b, before, nrb; // nrb: row blocks within the runs (1 side by side)
     int rb0;                         // the CTA's row block side by side
     static __device__ __forceinline__ void begin(const LatentDecodeArgs &a, int lane, int64_t (&out)[4])
@@ -183,25 +185,28 @@ template <int RB, int KT> struct LatentWalk {
     }
     __device__ __forceinline__ bool next(const LatentDecodeArgs &a, LatentRun &r)
     {
-        if (at >= end || b >= a.B) return false;
-        const int64_t tiles = Split::tiles(a, b);
-        int64_t in = at - before;
-        r.b = b;
-        r.rb = rb0;
-        if (nrb > 1) {
-            r.rb = (int)(in / tiles);
-            in -= r.rb * tiles;
+        while (at < end && b < a.B) {
+            const int64_t tiles = Split::tiles(a, b), length = tiles + Split::kCost;
+            int64_t in = at - before;
+            r.b = b;
+            r.rb = rb0;
+            if (nrb > 1) {
+                r.rb = (int)(in / length);
+                in -= r.rb * length;
+            }
+            const int64_t out = min(length, in + (end - at));
+            r.t0 = max((int64_t)0, in - Split::kCost);
+            r.t1 = max((int64_t)0, out - Split::kCost);
+            r.first = r.t0 == 0;
+            r.whole = r.first && r.t1 == tiles;
+            at += out - in;
+            if (out == length && (nrb == 1 || r.rb + 1 == nrb)) {
+                before += length * nrb;
+                ++b;
+            }
+            if (r.t0 < r.t1) return true; // else only of what counts in front of the tiles
         }
-        r.t0 = in;
-        r.t1 = min(tiles, r.t0 + (end - at));
-        r.first = r.t0 == 0;
-        r.whole = r.first && r.t1 == tiles;
-        at += r.t1 - r.t0;
-        if (r.t1 == tiles && (nrb == 1 || r.rb + 1 == nrb)) {
-            before += tiles * nrb;
-            ++b;
-        }
-        return true;
+        return false;
     }
 };
 

@@ -68,7 +68,7 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr uint32_t kNoKey = 0xffffffffu; // in place of a row's scale: the key is not to be seen
 constexpr float kTop = 448.f, kLow = 1.f / 16.f, kSmallestScale = 7.8886090522101181e-31f; // 2^-100
 
-using Split = LatentSplit<kRB, kKT>;
+using Split = LatentSplit<kRB, kKT, 2>;
 
 // A descriptor as two words, so that a step along an operand is one 32-bit addition (the issuing thread's
 // instructions between two MMAs bound the chain as much as the MMAs do).
@@ -138,7 +138,7 @@ __device__ __forceinline__ void split16(const float2 (&v)[8], float lo_scale, ui
     }
 }
 
-using Walk = LatentWalk<kRB, kKT>;
+using Walk = LatentWalk<Split>;
 
 struct Ctx {
     uint32_t base, tmem;
@@ -492,8 +492,7 @@ struct Meet {
     }
 };
 
-// A warp's 4 rows of a run's queries, on their way from memory: they are asked for before the output of the run
-// before is written.
+// A warp's 4 rows of a run's queries, on their way from memory.
 struct Queries {
     uint4 u[4][2];
     uint32_t w[4];
@@ -639,13 +638,17 @@ __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, const Ct
     LatentRun run, next_run;
     Queries queries;
     uint32_t n = 0;
+    float cq = 0.f, cq_next = 0.f;
     bool more = walk.next(a, next_run);
-    if (more) queries.fetch(a, next_run, warp, lane);
+    if (more) {
+        queries.fetch(a, next_run, warp, lane);
+        if (!store_queries(a, c, queries, warp, lane, all, &cq_next)) return false;
+        mbar_arrive(c.bar(B_Q));
+    }
     while (more) {
         run = next_run;
-        float cq, other[4];
-        if (!store_queries(a, c, queries, warp, lane, all, &cq)) return false;
-        mbar_arrive(c.bar(B_Q));
+        cq = cq_next;
+        float other[4];
         const int rr = run.rb * kRB + row, n_rows = a.Lq * a.H;
         const bool valid = rr < n_rows;
         const int64_t seen = valid ? latent_visible(a, run.b, rr / a.H) : 0;
@@ -724,55 +727,67 @@ __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, const Ct
                 pt = ps.x + ps.y;
                 vt = ws.x + ws.y;
             };
-            weigh();
-            // a row without a reference, or whose p leave fp32 (scales far below those that it was set by), takes one
-            top = begun && !(pt > 1e37f) ? top : INFINITY;
-            put_part(buf, fmaxf(top, other_part(top)));
-            uint32_t hi[4], lo[4];
-            split16(v, 16.f, hi, lo); // while the others arrive; seldom in vain
-            if (!rows.wait()) return false;
-            get(buf, other);
-            const float row_top = max4(other);
-            const bool raise = row_top > kTop, low = row_top < kLow && row_top > 1e-30f;
-            if (__any_sync(0xffffffffu, raise || low)) { // (the warps of the rows see the same values)
-                float zt = -INFINITY; // the row's largest z + log2 s of this tile
+            auto largest = [&]() { // the row's largest z + log2 s of this tile, in this thread
+                float zt = -INFINITY;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     if (open >> (2 * e) & 1u) zt = fmaxf(zt, fmaf(z[e].x, cq, __log2f(fmaxf(s[e].x, kSmallestScale))));
                     if (open >> (2 * e) & 2u) zt = fmaxf(zt, fmaf(z[e].y, cq, __log2f(fmaxf(s[e].y, kSmallestScale))));
                 }
-                if (!put(buf ^ 1, fmaxf(zt, other_part(zt)))) return false;
-                get(buf ^ 1, other);
-                zt = max4(other);
-                if (!put(buf, vs + other_part(vs))) return false;
+                return fmaxf(zt, other_part(zt));
+            };
+            uint32_t hi[4], lo[4];
+            if (t == run.t0) { // the reference that the run begins with
+                if (!put(buf, largest())) return false;
                 get(buf, other);
-                const float left = (float)(run.t1 - t) * kKT;
-                const bool move = raise || (low && left * row_top > sum4(other) * (1.f / 256.f));
-                float f = 1.f;
-                if (move && zt > -INFINITY) {
-                    const float next = rintf(zt) - 3.f; // a whole number: O and the sums move by an exact power of two
-                    f = begun ? ex2(ref - next) : 0.f;
-                    ref = next;
-                    begun = true;
-                    l *= f;
-                    vs *= f;
-                }
-                if (t > run.t0 && __any_sync(0xffffffffu, f != 1.f)) { // O of the tiles before this one
-                    if (!__all_sync(0xffffffffu, mbar_wait(c.bar(B_KEMPTY + (n - 1) % kStages), ((n - 1) / kStages) & 1))) return false;
-                    tc_fence_after();
-#pragma unroll 1
-                    for (int k = 0; k < 4; ++k) {
-                        uint32_t o[32];
-                        tmem_ld32(tO + 32u * k, o);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                        tmem_st32(tO + 32u * k, o);
-                    }
-                    tmem_st_wait();
-                }
+                const float zt = max4(other);
+                if (zt > -INFINITY) ref = rintf(zt) - 3.f, begun = true;
                 weigh();
                 split16(v, 16.f, hi, lo);
+            } else {
+                weigh();
+                // a row without a reference, or whose p leave fp32 (scales far below those that it was set by), takes one
+                top = begun && !(pt > 1e37f) ? top : INFINITY;
+                put_part(buf, fmaxf(top, other_part(top)));
+                split16(v, 16.f, hi, lo); // while the others arrive; seldom in vain
+                if (!rows.wait()) return false;
+                get(buf, other);
+                const float row_top = max4(other);
+                const bool raise = row_top > kTop, low = row_top < kLow && row_top > 1e-30f;
+                if (__any_sync(0xffffffffu, raise || low)) { // (the warps of the rows see the same values)
+                    if (!put(buf ^ 1, largest())) return false;
+                    get(buf ^ 1, other);
+                    const float zt = max4(other);
+                    if (!put(buf, vs + other_part(vs))) return false;
+                    get(buf, other);
+                    const float left = (float)(run.t1 - t) * kKT;
+                    const bool move = raise || (low && left * row_top > sum4(other) * (1.f / 256.f));
+                    float f = 1.f;
+                    if (move && zt > -INFINITY) {
+                        const float next = rintf(zt) - 3.f; // a whole number: O and the sums move by an exact power of two
+                        f = begun ? ex2(ref - next) : 0.f;
+                        ref = next;
+                        begun = true;
+                        l *= f;
+                        vs *= f;
+                    }
+                    if (__any_sync(0xffffffffu, f != 1.f)) { // O of the tiles before this one
+                        if (!__all_sync(0xffffffffu, mbar_wait(c.bar(B_KEMPTY + (n - 1) % kStages), ((n - 1) / kStages) & 1))) return false;
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int k = 0; k < 4; ++k) {
+                            uint32_t o[32];
+                            tmem_ld32(tO + 32u * k, o);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tmem_st32(tO + 32u * k, o);
+                        }
+                        tmem_st_wait();
+                    }
+                    weigh();
+                    split16(v, 16.f, hi, lo);
+                }
             }
             l += pt;
             vs += vt;
@@ -783,8 +798,14 @@ __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, const Ct
             tc_fence_before();
             mbar_arrive(c.bar(B_P + buf));
         }
+        // every S of this run is there, so the next one's queries may go in, and its first S beside this one's output
         more = walk.next(a, next_run);
-        if (more) queries.fetch(a, next_run, warp, lane);
+        if (more) {
+            queries.fetch(a, next_run, warp, lane);
+            if (!all.sync()) return false; // the last exchange has been read
+            if (!store_queries(a, c, queries, warp, lane, all, &cq_next)) return false;
+            mbar_arrive(c.bar(B_Q));
+        }
         // the run's last O, and the row's sum over the eight warps
         if (!__all_sync(0xffffffffu, mbar_wait(c.bar(B_KEMPTY + (n - 1) % kStages), ((n - 1) / kStages) & 1))) return false;
         tc_fence_after();

@@ -17,7 +17,8 @@ constexpr int kRB = kWarps * kRowsPerWarp; // query rows of a block
 constexpr int kKT = 32;                    // keys of a tile
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-using Split = LatentSplit<kRB, kKT>;
+using Split = LatentSplit<kRB, kKT, 1>;
+using TcSplit = LatentSplit<32, 128, 2>; // of the tensor-core kernel
 
 // One tile of up to 32 keys for one query row: q [dk] and kt [32, ldk] in shared memory, score of
 // key `lane` masked by `seen`, values vt[j * ldv + ch], ch < dv.
@@ -57,9 +58,9 @@ __global__ void __launch_bounds__(32 * kWarps) latent_decode_generic_kernel(Late
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int rd = a.rows.rope_dims, R = a.rows.c - rd, c = a.rows.c, ld = c + 1;
     float *kt = sm, *qs = sm + kKT * ld; // [kKT, ld], [kRB, c]
-    if (warp == 0) LatentWalk<kRB, kKT>::begin(a, lane, s_at);
+    if (warp == 0) LatentWalk<Split>::begin(a, lane, s_at);
     __syncthreads();
-    LatentWalk<kRB, kKT> walk(a, s_at);
+    LatentWalk<Split> walk(a, s_at);
     LatentRun run;
     while (walk.next(a, run)) {
         const int64_t b = run.b, t0 = run.t0, t1 = run.t1;
@@ -139,7 +140,7 @@ __global__ void __launch_bounds__(32 * kWarps) latent_decode_generic_kernel(Late
 // m = max m_i, l = sum 2^(m_i - m) l_i, O = sum 2^(m_i - m) O_i; the output is O / l.
 constexpr int kMaxParts = 512;
 
-template <int RB, int KT> __global__ void __launch_bounds__(128) latent_merge_kernel(LatentDecodeArgs a)
+template <class Split, int RB> __global__ void __launch_bounds__(128) latent_merge_kernel(LatentDecodeArgs a)
 {
     __shared__ int64_t s_at[2];
     __shared__ float red[4], weight[kMaxParts];
@@ -147,15 +148,15 @@ template <int RB, int KT> __global__ void __launch_bounds__(128) latent_merge_ke
     const int64_t rows = (int64_t)a.Lq * a.H, b = blockIdx.x / rows;
     const int r = (int)(blockIdx.x % rows), rb = r / RB;
     const int R = a.rows.c - a.rows.rope_dims;
-    using Split = LatentSplit<RB, KT>;
     const int64_t nrb = a.par > 1 ? 1 : Split::row_blocks(a.Lq, a.H), G = a.grid / a.par;
-    if (tid < 64) { // tiles before this sequence (warp 0), from it on (warp 1)
+    if (tid < 64) { // the length before this sequence (warp 0), from it on (warp 1)
         const int64_t s = tid < 32 ? Split::warp_total(a, 0, b, lane) : Split::warp_total(a, b, a.B, lane);
         if (lane == 0) s_at[tid >> 5] = s * nrb;
     }
     __syncthreads();
-    const int64_t tiles = Split::tiles(a, b), T = s_at[0] + s_at[1], s0 = s_at[0] + (a.par > 1 ? 0 : rb * tiles), s1 = s0 + tiles - 1;
-    // the CTAs (or groups) that hold the run's first and last tile: the largest i with floor(i T / G) <= tile
+    const int64_t length = Split::length(a, b), T = s_at[0] + s_at[1], begin = s_at[0] + (a.par > 1 ? 0 : rb * length);
+    const int64_t s0 = begin + Split::kCost, s1 = begin + length - 1; // the places of its first and last tile
+    // the CTAs (or groups) that hold the run's first and last tile: the largest i with floor(i T / G) <= place
     const int64_t i0 = ((s0 + 1) * G - 1) / T, i1 = ((s1 + 1) * G - 1) / T;
     // launched beside the kernel that writes the parts: every block waits for it, those with nothing to do too, since
     // what follows in the stream waits for this kernel alone
@@ -295,7 +296,7 @@ size_t latent_decode_generic_workspace(int64_t B, int Lq, int H, int R, int64_t 
     return (size_t)*grid * 2 * kRB * (R + 4) * sizeof(float);
 }
 
-template <int RB, int KT> static cudaError_t launch_merge(const LatentDecodeArgs &a, cudaStream_t st)
+template <class Split, int RB> static cudaError_t launch_merge(const LatentDecodeArgs &a, cudaStream_t st)
 {
     if (a.grid == a.par) return cudaSuccess; // one CTA, or one group, cuts no run
     if (a.grid > kMaxParts) return cudaErrorInvalidValue;
@@ -309,10 +310,10 @@ template <int RB, int KT> static cudaError_t launch_merge(const LatentDecodeArgs
     at.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, latent_merge_kernel<RB, KT>, a);
+    return cudaLaunchKernelEx(&cfg, latent_merge_kernel<Split, RB>, a);
 }
 
-cudaError_t launch_latent_merge_32x128(const LatentDecodeArgs &a, cudaStream_t st) { return launch_merge<32, 128>(a, st); }
+cudaError_t launch_latent_merge_32x128(const LatentDecodeArgs &a, cudaStream_t st) { return launch_merge<TcSplit, 32>(a, st); }
 
 cudaError_t launch_latent_decode_generic(LatentDecodeArgs a, cudaStream_t st)
 {
@@ -322,7 +323,7 @@ cudaError_t launch_latent_decode_generic(LatentDecodeArgs a, cudaStream_t st)
     latent_decode_generic_kernel<<<(unsigned)a.grid, 32 * kWarps, smem, st>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_merge<kRB, kKT>(a, st);
+    return launch_merge<Split, kRB>(a, st);
 }
 
 template <typename T> static cudaError_t prefill_generic(const LatentPrefillArgs &a, cudaStream_t st)
