@@ -27,7 +27,7 @@
 //
 // Roles: warps 0-7 softmax and output; warp 8 copies the keys by TMA, in boxes of a page or of 128 rows, and
 // warp 9 brings the tile after into L2 (with pages that no box fits, both copy by cp.async); warp 10 MMA.  Two stages of 80 KB.  Rows that are not to
-// be seen are zeros in shared memory: the probability 0 times whatever they held would not be 0.
+// be seen are zeros in shared memory, or not read: the probability 0 times whatever they held would not be 0.
 // Bound by HBM for up to 32 query rows a key, by the chain load - S - softmax - O over two stages above.
 #include "latent.cuh"
 #include "tc_common.cuh"
@@ -165,6 +165,14 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void *src, uint32_t b
 
 __device__ __forceinline__ void sts1(uint32_t dst, uint32_t v) { asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst), "r"(v) : "memory"); }
 
+// Steps of 32 keys that O (+)= v code takes of tile t: up to the last key that is to be seen.  Rows behind it are not read
+// (a score that they gave is not used, whatever it is); of those before, the ones that are not there are zeros.
+__device__ __forceinline__ int output_steps(int64_t seen, int64_t t)
+{
+    const int64_t n = seen - t * kKT;
+    return n >= kKT ? kKT / 32 : n <= 32 ? 1 : (int)(n + 31) / 32;
+}
+
 // The boxes of a run's tiles: lane i has box i.  Everything here is on the way between a free stage and its copies,
 // so a tile costs a lane one page number, loaded two tiles ahead and untouched before (behind a busy memory a
 // lookup takes as long as a tile).
@@ -237,6 +245,21 @@ __device__ __forceinline__ bool tma_role(const LatentDecodeArgs &a, const Maps &
             now = next;
             next = B.page(t + 2);
             scales(t + 1, sc_next);
+            int64_t tail_row[4];
+            uint32_t tail_scale[4];
+            if (!whole) { // row by row
+                const int64_t n_seen = B.seen - t * kKT;
+                bool refused = false;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int j = 32 * k + lane;
+                    const int32_t p = __shfl_sync(0xffffffffu, page, j / M.box);
+                    tail_row[k] = j < n_seen ? a.map.row(p, B.base, (uint32_t)(t * kKT + j)) : -1;
+                    tail_scale[k] = tail_row[k] < 0 ? kNoKey : __float_as_uint(__ldg(a.rows.scale + tail_row[k]));
+                    refused |= j < n_seen && tail_row[k] < 0;
+                }
+                if (refused) flag_error(a.err, CSA_DEVERR_INDEX);
+            }
             if (n >= kStages && !__all_sync(0xffffffffu, mbar_wait(c.bar(B_KEMPTY + n % kStages), ((n / kStages) & 1) ^ 1))) {
                 ok = false;
                 break;
@@ -262,18 +285,8 @@ __device__ __forceinline__ bool tma_role(const LatentDecodeArgs &a, const Maps &
                     tma_load_2d(st + 4 * kSlice, &M.rope, 0, r, full);
                 }
             } else {
-                // some rows are not to be seen, or not there: row by row, their places zeroed once no box is on its way
-                int64_t key_row[4];
-                const int64_t n_seen = B.seen - t * kKT;
-                bool refused = false;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int j = 32 * k + lane;
-                    const int32_t p = __shfl_sync(0xffffffffu, page, j / M.box);
-                    key_row[k] = j < n_seen ? a.map.row(p, B.base, (uint32_t)(t * kKT + j)) : -1;
-                    refused |= j < n_seen && key_row[k] < 0;
-                }
-                if (refused) flag_error(a.err, CSA_DEVERR_INDEX);
+                // some rows are not to be seen, or not there: their places are zeroed once no box is on its way
+                const int64_t(&key_row)[4] = tail_row;
                 uint32_t bytes = 0;
                 if (!paged && __any_sync(0xffffffffu, key_row[0] >= 0 || key_row[1] >= 0 || key_row[2] >= 0 || key_row[3] >= 0)) {
                     bytes = kKT * 640u; // the run may begin or end outside the cache: zeros
@@ -294,21 +307,23 @@ __device__ __forceinline__ bool tma_role(const LatentDecodeArgs &a, const Maps &
                 }
                 if (elect_one()) mbar_arrive_expect_tx(c.bar(B_TAIL), bytes);
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    sts1(sc + 4u * (uint32_t)(32 * k + lane), key_row[k] < 0 ? kNoKey : __float_as_uint(__ldg(a.rows.scale + key_row[k])));
+                for (int k = 0; k < 4; ++k) sts1(sc + 4u * (uint32_t)(32 * k + lane), tail_scale[k]);
                 if (!__all_sync(0xffffffffu, mbar_wait(c.bar(B_TAIL), tails & 1))) {
                     ok = false;
                     break;
                 }
                 ++tails;
                 const uint32_t zero[4] = {0, 0, 0, 0};
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (key_row[k] < 0) {
-                        const uint32_t j = (uint32_t)(32 * k + lane), at = (j >> 3) * M.group + (j & 7u) * 128u;
-                        for (uint32_t e = 0; e < 32; ++e) sts4(st + (e >> 3) * M.slice + at + 16u * (e & 7u), zero);
-                        for (uint32_t e = 0; e < 8; ++e) sts4(st + 4 * kSlice + j * 128u + 16u * e, zero);
+                const int steps = output_steps(B.seen, t);
+#pragma unroll 1
+                for (int k = 0; k < steps; ++k) {
+                    uint32_t bad = __ballot_sync(0xffffffffu, (k == 0 ? key_row[0] : k == 1 ? key_row[1] : k == 2 ? key_row[2] : key_row[3]) < 0);
+                    while (bad) { // a row at a time: 32 chunks of 16 bytes
+                        const uint32_t j = (uint32_t)(32 * k + __ffs(bad) - 1), e = (uint32_t)lane;
+                        bad &= bad - 1;
+                        sts4(st + (e >> 3) * M.slice + (j >> 3) * M.group + (j & 7u) * 128u + 16u * (e & 7u), zero);
                     }
+                }
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (elect_one()) mbar_arrive(full);
@@ -425,9 +440,10 @@ __device__ __forceinline__ bool mma_role(const LatentDecodeArgs &a, const Maps &
     LatentRun run;
     uint32_t n = 0, runs = 0;
     bool pending = false, pending_first = false;
+    int pending_steps = 0;
     const Desc q_desc(sdesc_sw128(c.base + OFF_Q, 16, 1024)), k_desc(sdesc_sw128(c.base + OFF_K, 16, M.group)), r_desc(sdesc_sw128(c.base + OFF_K, 16, 1024));
     const Desc p_desc(sdesc_sw128(c.base + OFF_P, 16, 1024)), v_desc(sdesc_sw128(c.base + OFF_K, M.slice, M.group));
-    auto output = [&](uint32_t k, bool first) { // O (+)= v code of tile k
+    auto output = [&](uint32_t k, bool first, int steps) { // O (+)= v code of tile k
         if (!mbar_wait(c.bar(B_P + (k & 1)), (k >> 1) & 1)) return false;
         tc_fence_after();
         const Desc dp = p_desc.at(kPTile * (k & 1)), dv = v_desc.at((k % kStages) * 5 * kSlice);
@@ -435,15 +451,16 @@ __device__ __forceinline__ bool mma_role(const LatentDecodeArgs &a, const Maps &
         for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                mma_ws<true>(c.tmem + kColO + 128u * h, dp.at(32u * kk), dv.at(2u * h * M.slice + 4u * kk * M.group), IDESC_O, !first || kk > 0);
+                if (kk < steps) mma_ws<true>(c.tmem + kColO + 128u * h, dp.at(32u * kk), dv.at(2u * h * M.slice + 4u * kk * M.group), IDESC_O, !first || kk > 0);
         mma_commit(c.bar(B_KEMPTY + k % kStages));
         return true;
     };
     while (walk.next(a, run)) {
+        const int64_t seen = latent_visible(a, run.b, a.Lq - 1);
         for (int64_t t = run.t0; t < run.t1; ++t, ++n) {
             const bool first = t == run.t0;
             if (first) {
-                if (pending && !output(n - 1, pending_first)) return false;
+                if (pending && !output(n - 1, pending_first, pending_steps)) return false;
                 pending = false;
                 if (!mbar_wait(c.bar(B_Q), runs & 1)) return false;
                 ++runs;
@@ -451,7 +468,7 @@ __device__ __forceinline__ bool mma_role(const LatentDecodeArgs &a, const Maps &
             const uint32_t full = c.bar(B_KFULL + n % kStages), full_ph = (n / kStages) & 1;
             if (pending && !mbar_test_wait(full, full_ph) && mbar_wait_either(full, full_ph, c.bar(B_P + ((n - 1) & 1)), ((n - 1) >> 1) & 1)) {
                 // the keys are late: O of the tile before goes first, so that its stage is free the sooner
-                if (!output(n - 1, pending_first)) return false;
+                if (!output(n - 1, pending_first, pending_steps)) return false;
                 pending = false;
             }
             if (!mbar_wait(full, full_ph)) return false;
@@ -468,12 +485,13 @@ __device__ __forceinline__ bool mma_role(const LatentDecodeArgs &a, const Maps &
             for (int kk = 0; kk < 4; ++kk)
                 mma_ws<false>(c.tmem + kColSr + buf, q_desc.at(4 * kQSlice + 32u * kk), dr.at(32u * kk), IDESC_SR, kk != 0);
             mma_commit(c.bar(B_S + (n & 1)));
-            if (pending && !output(n - 1, pending_first)) return false;
+            if (pending && !output(n - 1, pending_first, pending_steps)) return false;
             pending = true;
             pending_first = first;
+            pending_steps = output_steps(seen, t);
         }
     }
-    return !pending || output(n - 1, pending_first);
+    return !pending || output(n - 1, pending_first, pending_steps);
 }
 
 // A barrier between softmax warps, with the bound of every other wait.
@@ -515,34 +533,31 @@ struct Queries {
     }
 };
 
-// Into shared memory, as hi and lo; *factor takes a score of this lane's row to the log2 domain.
-__device__ __forceinline__ bool store_queries(const LatentDecodeArgs &a, const Ctx &c, const Queries &in, int warp, int lane, Meet &all,
+// Into shared memory, as hi and lo; *factor takes a score of this lane's row to the log2 domain.  (Rows one after
+// another: code that runs once a run comes from far away, and its length is what it costs.)
+__device__ __forceinline__ bool store_queries(const LatentDecodeArgs &a, const Ctx &c, Queries &in, int warp, int lane, Meet &all,
                                               float *factor)
 {
-    const uint4(&u)[4][2] = in.u;
-    const uint32_t(&w)[4] = in.w;
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < 4; ++i) {
         const int r = 4 * warp + i;
         float2 x[8];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const uint32_t y[4] = {u[i][h].x, u[i][h].y, u[i][h].z, u[i][h].w};
+            const uint32_t y[4] = {in.u[0][h].x, in.u[0][h].y, in.u[0][h].z, in.u[0][h].w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) x[4 * h + e] = make_float2(__uint_as_float(y[e] << 16), __uint_as_float(y[e] & 0xffff0000u));
         }
         float am = 0.f;
-        bool finite = true;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float y = fmaxf(fabsf(x[e].x), fabsf(x[e].y));
-            am = fmaxf(am, y);
-            finite = finite && fabsf(x[e].x) < INFINITY && fabsf(x[e].y) < INFINITY;
-        }
-        const float rx = __uint_as_float(w[i] << 16), ry = __uint_as_float(w[i] & 0xffff0000u);
+        for (int e = 0; e < 8; ++e) am = fmaxf(am, fmaxf(fabsf(x[e].x), fabsf(x[e].y)));
+        float nan = 0.f; // NaN where an entry is not finite
+#pragma unroll
+        for (int e = 0; e < 8; ++e) nan = fmaf(x[e].x, 0.f, fmaf(x[e].y, 0.f, nan));
+        const float rx = __uint_as_float(in.w[0] << 16), ry = __uint_as_float(in.w[0] & 0xffff0000u);
         am = warp_max(am);
         const float ar = warp_max(fmaxf(fabsf(rx), fabsf(ry)));
-        finite = __all_sync(0xffffffffu, finite);
+        const bool finite = __all_sync(0xffffffffu, nan == 0.f);
         // the largest latent entry to [128, 256), as far as the rotated entries stay far inside bf16's range
         const int en = (int)(__float_as_uint(am) >> 23) - 127, er = (int)(__float_as_uint(ar) >> 23) - 127;
         int k = am > 0.f && finite ? min(7 - en, 126) : 0;
@@ -552,16 +567,17 @@ __device__ __forceinline__ bool store_queries(const LatentDecodeArgs &a, const C
         for (int e = 0; e < 8; ++e) x[e].x *= up, x[e].y *= up;
         uint32_t hi[4], lo[4];
         split16(x, 1.f, hi, lo);
-        const uint32_t row = 32u * (uint32_t)(r >> 4) + (uint32_t)(r & 15);
         // lane holds channels 16 lane .. 16 lane + 15: byte 16 (lane & 7) of slice lane / 8
-        sts4(c.base + OFF_Q + (uint32_t)(lane >> 3) * kQSlice + sw128(row, 16u * (uint32_t)(lane & 7)), hi);
-        sts4(c.base + OFF_Q + (uint32_t)(lane >> 3) * kQSlice + sw128(row + 16, 16u * (uint32_t)(lane & 7)), lo);
-        const uint32_t rr = uint32_t(f32_to_bf16_bits(rx * up)) | (uint32_t(f32_to_bf16_bits(ry * up)) << 16);
-        asm volatile("st.shared.u32 [%0], %1;" ::"r"(c.base + OFF_Q + 4 * kQSlice + sw128(row, 4u * (uint32_t)lane)), "r"(rr) : "memory");
-        asm volatile("st.shared.u32 [%0], %1;" ::"r"(c.base + OFF_Q + 4 * kQSlice + sw128(row + 16, 4u * (uint32_t)lane)), "r"(0) : "memory");
+        const uint32_t row = 32u * (uint32_t)(r >> 4) + (uint32_t)(r & 15), q = c.base + OFF_Q, at = q + (uint32_t)(lane >> 3) * kQSlice;
+        sts4(at + sw128(row, 16u * (uint32_t)(lane & 7)), hi);
+        sts4(at + sw128(row + 16, 16u * (uint32_t)(lane & 7)), lo);
+        sts1(q + 4 * kQSlice + sw128(row, 4u * (uint32_t)lane), uint32_t(f32_to_bf16_bits(rx * up)) | (uint32_t(f32_to_bf16_bits(ry * up)) << 16));
+        sts1(q + 4 * kQSlice + sw128(row + 16, 4u * (uint32_t)lane), 0);
         // a row that is not finite makes NaN of its scores
         const float f = finite ? a.scale * kLog2e * exp2i(-k) : NAN;
-        if (lane == 0) asm volatile("st.shared.f32 [%0], %1;" ::"r"(c.base + OFF_XCH + 4u * (uint32_t)r), "f"(f) : "memory");
+        if (lane == 0) sts1(c.base + OFF_XCH + 4u * (uint32_t)r, __float_as_uint(f));
+#pragma unroll
+        for (int n = 0; n < 3; ++n) in.u[n][0] = in.u[n + 1][0], in.u[n][1] = in.u[n + 1][1], in.w[n] = in.w[n + 1];
     }
     fence_proxy_async_smem();
     if (!all.sync()) return false;
@@ -638,22 +654,81 @@ __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, const Ct
     LatentRun run, next_run;
     Queries queries;
     uint32_t n = 0;
-    float cq = 0.f, cq_next = 0.f;
-    bool more = walk.next(a, next_run);
-    if (more) {
-        queries.fetch(a, next_run, warp, lane);
-        if (!store_queries(a, c, queries, warp, lane, all, &cq_next)) return false;
-        mbar_arrive(c.bar(B_Q));
-    }
-    while (more) {
+    float cq = 0.f, ref = 0.f, l = 0.f; // factor; reference and sum of p over this thread's keys
+    // the run's last O, and the row's sum over the eight threads that share it
+    auto output = [&](uint32_t n) {
+        float other[4];
+        const int rr = run.rb * kRB + row, n_rows = a.Lq * a.H;
+        const bool valid = rr < n_rows;
+        // the run's last O, and the row's sum over the eight warps
+        if (!__all_sync(0xffffffffu, mbar_wait(c.bar(B_KEMPTY + n % kStages), (n / kStages) & 1))) return false;
+        tc_fence_after();
+        if (!rows.sync() || !put(0, l + other_part(l))) return false;
+        get(0, other);
+        l = sum4(other);
+        const int64_t out_row = run.b * n_rows + rr;
+        const float inv = l != 0.f ? 1.f / l : 0.f;
+        float *rec = a.part + ((2 * (int64_t)blockIdx.x + run.first) * kRB + row) * (kR + 4);
+#pragma unroll 1
+        for (int k = 0; k < 4; ++k) {
+            uint32_t o[32];
+            tmem_ld32(tO + 32u * k, o);
+            tmem_ld_wait();
+            float x[16]; // hi + lo / 16 of channels 256 sub + 128 half + 32 k + 16 part + e
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const float a0 = __uint_as_float(o[e]), a1 = __uint_as_float(o[16 + e]), got = other_part(part ? a0 : a1);
+                x[e] = part ? fmaf(a1, 1.f / 16.f, got) : fmaf(got, 1.f / 16.f, a0);
+            }
+            const int ch = 256 * sub + 128 * half + 32 * k + 16 * part;
+            if (valid && run.whole) {
+                uint32_t w[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    w[e] = uint32_t(f32_to_bf16_bits(x[2 * e] * inv)) | (uint32_t(f32_to_bf16_bits(x[2 * e + 1] * inv)) << 16);
+                uint4 *d = reinterpret_cast<uint4 *>(a.o + out_row * kR + ch);
+                d[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                d[1] = make_uint4(w[4], w[5], w[6], w[7]);
+            } else if (valid) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    *reinterpret_cast<float4 *>(rec + 4 + ch + 4 * e) = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+            }
+        }
+        if (valid && kq == 0 && part == 0) {
+            if (run.whole) {
+                if (a.lse) a.lse[out_row] = l != 0.f ? (ref + log2f(l)) * kLn2 : -INFINITY;
+            } else {
+                rec[0] = l != 0.f ? ref : -INFINITY;
+                rec[1] = l;
+            }
+        }
+        tc_fence_before();
+        return rows.sync(); // the sums are read before the place is used again
+    };
+    bool have = false;
+    for (;;) {
+        // every S of the run behind is there, so the next one's queries may go in, and its first S beside the output
+        const bool more = walk.next(a, next_run);
+        float cq_next = 0.f;
+        if (more) {
+            queries.fetch(a, next_run, warp, lane);
+            if (!all.sync()) return false; // the last exchange has been read
+            if (!store_queries(a, c, queries, warp, lane, all, &cq_next)) return false;
+            mbar_arrive(c.bar(B_Q));
+        }
+        if (have && !output(n - 1)) return false;
+        if (!more) break;
+        have = true;
         run = next_run;
         cq = cq_next;
+        ref = l = 0.f;
         float other[4];
         const int rr = run.rb * kRB + row, n_rows = a.Lq * a.H;
         const bool valid = rr < n_rows;
         const int64_t seen = valid ? latent_visible(a, run.b, rr / a.H) : 0;
         const int64_t seen_least = latent_visible(a, run.b, run.rb * kRB / a.H); // by every row of the block
-        float ref = 0.f, l = 0.f, vs = 0.f; // reference, sum of p and of v over this thread's keys
+        float vs = 0.f;                    // sum of v over this thread's keys
         bool begun = seen <= run.t0 * kKT;  // the row has a reference, or needs none here
         for (int64_t t = run.t0; t < run.t1; ++t, ++n) {
             const uint32_t buf = n & 1;
@@ -736,15 +811,11 @@ __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, const Ct
                 }
                 return fmaxf(zt, other_part(zt));
             };
+            // weigh with the reference as it is, and again if that turns out to move; a run's first tile sets it first
             uint32_t hi[4], lo[4];
-            if (t == run.t0) { // the reference that the run begins with
-                if (!put(buf, largest())) return false;
-                get(buf, other);
-                const float zt = max4(other);
-                if (zt > -INFINITY) ref = rintf(zt) - 3.f, begun = true;
-                weigh();
-                split16(v, 16.f, hi, lo);
-            } else {
+            bool set = true, raise = true;
+            float row_top = 0.f;
+            if (t > run.t0) {
                 weigh();
                 // a row without a reference, or whose p leave fp32 (scales far below those that it was set by), takes one
                 top = begun && !(pt > 1e37f) ? top : INFINITY;
@@ -752,42 +823,47 @@ __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, const Ct
                 split16(v, 16.f, hi, lo); // while the others arrive; seldom in vain
                 if (!rows.wait()) return false;
                 get(buf, other);
-                const float row_top = max4(other);
-                const bool raise = row_top > kTop, low = row_top < kLow && row_top > 1e-30f;
-                if (__any_sync(0xffffffffu, raise || low)) { // (the warps of the rows see the same values)
-                    if (!put(buf ^ 1, largest())) return false;
-                    get(buf ^ 1, other);
-                    const float zt = max4(other);
+                row_top = max4(other);
+                raise = row_top > kTop;
+                set = __any_sync(0xffffffffu, raise || (row_top < kLow && row_top > 1e-30f)); // (alike in the warps of the rows)
+            }
+            if (set) {
+                const uint32_t place = t == run.t0 ? buf : buf ^ 1;
+                if (!put(place, largest())) return false;
+                get(place, other);
+                const float zt = max4(other);
+                bool move = raise;
+                if (t > run.t0) { // low: what is still to come against what is summed
                     if (!put(buf, vs + other_part(vs))) return false;
                     get(buf, other);
                     const float left = (float)(run.t1 - t) * kKT;
-                    const bool move = raise || (low && left * row_top > sum4(other) * (1.f / 256.f));
-                    float f = 1.f;
-                    if (move && zt > -INFINITY) {
-                        const float next = rintf(zt) - 3.f; // a whole number: O and the sums move by an exact power of two
-                        f = begun ? ex2(ref - next) : 0.f;
-                        ref = next;
-                        begun = true;
-                        l *= f;
-                        vs *= f;
-                    }
-                    if (__any_sync(0xffffffffu, f != 1.f)) { // O of the tiles before this one
-                        if (!__all_sync(0xffffffffu, mbar_wait(c.bar(B_KEMPTY + (n - 1) % kStages), ((n - 1) / kStages) & 1))) return false;
-                        tc_fence_after();
-#pragma unroll 1
-                        for (int k = 0; k < 4; ++k) {
-                            uint32_t o[32];
-                            tmem_ld32(tO + 32u * k, o);
-                            tmem_ld_wait();
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                            tmem_st32(tO + 32u * k, o);
-                        }
-                        tmem_st_wait();
-                    }
-                    weigh();
-                    split16(v, 16.f, hi, lo);
+                    move = raise || (row_top < kLow && row_top > 1e-30f && left * row_top > sum4(other) * (1.f / 256.f));
                 }
+                float f = 1.f;
+                if (move && zt > -INFINITY) {
+                    const float next = rintf(zt) - 3.f; // a whole number: O and the sums move by an exact power of two
+                    f = begun ? ex2(ref - next) : 0.f;
+                    ref = next;
+                    begun = true;
+                    l *= f;
+                    vs *= f;
+                }
+                if (t > run.t0 && __any_sync(0xffffffffu, f != 1.f)) { // O of the tiles before this one
+                    if (!__all_sync(0xffffffffu, mbar_wait(c.bar(B_KEMPTY + (n - 1) % kStages), ((n - 1) / kStages) & 1))) return false;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t o[32];
+                        tmem_ld32(tO + 32u * k, o);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                        tmem_st32(tO + 32u * k, o);
+                    }
+                    tmem_st_wait();
+                }
+                weigh();
+                split16(v, 16.f, hi, lo);
             }
             l += pt;
             vs += vt;
@@ -798,59 +874,6 @@ __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, const Ct
             tc_fence_before();
             mbar_arrive(c.bar(B_P + buf));
         }
-        // every S of this run is there, so the next one's queries may go in, and its first S beside this one's output
-        more = walk.next(a, next_run);
-        if (more) {
-            queries.fetch(a, next_run, warp, lane);
-            if (!all.sync()) return false; // the last exchange has been read
-            if (!store_queries(a, c, queries, warp, lane, all, &cq_next)) return false;
-            mbar_arrive(c.bar(B_Q));
-        }
-        // the run's last O, and the row's sum over the eight warps
-        if (!__all_sync(0xffffffffu, mbar_wait(c.bar(B_KEMPTY + (n - 1) % kStages), ((n - 1) / kStages) & 1))) return false;
-        tc_fence_after();
-        if (!rows.sync() || !put(0, l + other_part(l))) return false;
-        get(0, other);
-        l = sum4(other);
-        const int64_t out_row = run.b * n_rows + rr;
-        const float inv = l != 0.f ? 1.f / l : 0.f;
-        float *rec = a.part + ((2 * (int64_t)blockIdx.x + run.first) * kRB + row) * (kR + 4);
-#pragma unroll 1
-        for (int k = 0; k < 4; ++k) {
-            uint32_t o[32];
-            tmem_ld32(tO + 32u * k, o);
-            tmem_ld_wait();
-            float x[16]; // hi + lo / 16 of channels 256 sub + 128 half + 32 k + 16 part + e
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const float a0 = __uint_as_float(o[e]), a1 = __uint_as_float(o[16 + e]), got = other_part(part ? a0 : a1);
-                x[e] = part ? fmaf(a1, 1.f / 16.f, got) : fmaf(got, 1.f / 16.f, a0);
-            }
-            const int ch = 256 * sub + 128 * half + 32 * k + 16 * part;
-            if (valid && run.whole) {
-                uint32_t w[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    w[e] = uint32_t(f32_to_bf16_bits(x[2 * e] * inv)) | (uint32_t(f32_to_bf16_bits(x[2 * e + 1] * inv)) << 16);
-                uint4 *d = reinterpret_cast<uint4 *>(a.o + out_row * kR + ch);
-                d[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                d[1] = make_uint4(w[4], w[5], w[6], w[7]);
-            } else if (valid) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    *reinterpret_cast<float4 *>(rec + 4 + ch + 4 * e) = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
-            }
-        }
-        if (valid && kq == 0 && part == 0) {
-            if (run.whole) {
-                if (a.lse) a.lse[out_row] = l != 0.f ? (ref + log2f(l)) * kLn2 : -INFINITY;
-            } else {
-                rec[0] = l != 0.f ? ref : -INFINITY;
-                rec[1] = l;
-            }
-        }
-        tc_fence_before();
-        if (!all.sync()) return false; // everything shared is read before it is used again
     }
     return true;
 }
