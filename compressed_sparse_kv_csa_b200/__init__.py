@@ -446,58 +446,64 @@ def csa_decode_glue(o, P, Rm=None, q_next=None, qI: Fp4Rows | None = None, strea
 # latent attention (one latent row per token; see include/csa.h for the formulas and limits)
 # ----------------------------------------------------------------------------------------
 
-def _operand(name: str, t, dtypes, shape, device=None, optional: bool = False):
-    """Refuse an operand that the C call would misread: it is handed over as a bare pointer, so its
-    dtype, shape and packing are checked here.  None in `shape` = any extent."""
+def _refuse(name: str, t, dtype, shape, dev):
     if t is None:
-        if optional:
-            return
         raise ValueError(f"{name} is missing")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name}: unsupported dtype {t.dtype}")
-    if t.dim() != len(shape) or any(e is not None and t.shape[i] != e for i, e in enumerate(shape)):
-        raise ValueError(f"{name}: shape {tuple(t.shape)} does not match {shape}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, not {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, not {shape}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    raise ValueError(f"{name} is on {t.device}, not on the GPU of the other operands")
 
 
-def _kv_operand(name: str, rows: KvRows, device):
-    n, dev = rows.n, device
-    _operand(name + ".fp8", rows.fp8, (torch.uint8,), (n, None), dev)
-    _operand(name + ".rope", rows.rope, (torch.bfloat16,), (n, None), dev)
-    _operand(name + ".scale", rows.scale, (torch.float32,), (n,), dev)
+def _in(name: str, t, dtype, shape, dev):
+    """The address of an operand that has to be there.  It is handed over bare, so whatever the C call would
+    misread is refused here: its dtype, shape, packing and device."""
+    if t is None or t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
+        _refuse(name, t, dtype, shape, dev)
+    return t.data_ptr()
 
 
-def _row_map(pages, page_rows, off, device):
+def _opt(name: str, t, dtype, shape, dev):
+    return None if t is None else _in(name, t, dtype, shape, dev)
+
+
+def _rows(name: str, rows: KvRows, dev):
+    """The C view of a latent cache, its planes checked."""
+    n, lat, rd = rows.fp8.shape[0], rows.fp8.shape[1], rows.rope.shape[1]
+    return _KvRows(_in(name + ".fp8", rows.fp8, torch.uint8, (n, lat), dev), _in(name + ".rope", rows.rope, torch.bfloat16, (n, rd), dev),
+                   _in(name + ".scale", rows.scale, torch.float32, (n,), dev), n, lat + rd, rd)
+
+
+def _row_map(pages, page_rows, off, dev):
     """The page table or offsets of a latent cache, checked: (B, pages, max_pages, page_rows, off)."""
     if (pages is None) == (off is None):
         raise ValueError("give either pages or off")
-    if pages is not None:
-        _operand("pages", pages, (torch.int32,), (None, None), device)
-        return pages.shape[0], _ptr(pages), pages.shape[1], int(page_rows), None
-    _operand("off", off, (torch.int64,), (None,), device)
-    return off.shape[0], None, 0, 0, _ptr(off)
+    if off is not None:
+        return off.shape[0], None, 0, 0, _in("off", off, torch.int64, (off.shape[0],), dev)
+    B, m = pages.shape
+    return B, _in("pages", pages, torch.int32, (B, m), dev), m, int(page_rows), None
 
 
-class _current:
-    """Makes the operands' device current for a call (the library launches on the current one)."""
+def _launch(fn: str, dev: int, stream, args):
+    """Call the entry point with the operands' device current and the stream last."""
+    if dev < 0:
+        raise ValueError("the operands have to be on a GPU")
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _launch(fn, dev, stream, args)
+    st = torch.cuda.current_stream(dev).cuda_stream if stream is None else getattr(stream, "cuda_stream", stream)
+    _check(fn, getattr(_lib, fn)(*args, int(st)))
 
-    def __init__(self, device):
-        self.guard = None
-        if device.type != "cuda":
-            raise ValueError(f"the operands are on {device}: they have to be on a GPU")
-        if device.index is not None and device.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(device)
 
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *e):
-        if self.guard is not None:
-            self.guard.__exit__(*e)
+def _float_dtype(name: str, t):
+    if t.dtype is torch.bfloat16:
+        return CSA_BF16
+    if t.dtype is torch.float32:
+        return CSA_F32
+    raise TypeError(f"{name}: unsupported dtype {t.dtype}")
 
 
 def latent_append(x, pos, out: KvRows, g=None, eps: float = 1e-6, base: float = 0.0, seq=None, pages=None,
@@ -505,18 +511,13 @@ def latent_append(x, pos, out: KvRows, g=None, eps: float = 1e-6, base: float = 
     """Write the rows x [n, R + rd] (fp32/bf16) into the latent cache ``out`` at position pos[i] of
     sequence seq[i] (None: of sequence i): RMSNorm of the latent part (when g is given), rotation of
     the rest by pos (when base is not 0), quantise on write."""
-    dev = x.device
-    _operand("x", x, (torch.float32, torch.bfloat16), (None, out.c))
-    n = x.shape[0]
-    _operand("pos", pos, (torch.int64,), (n,), dev)
-    _operand("seq", seq, (torch.int32,), (n,), dev, optional=True)
-    _operand("g", g, (torch.float32,), (out.c - out.rope_dims,), dev, optional=True)
-    _kv_operand("out", out, dev)
+    dev, n, dt = x.get_device(), x.shape[0], _float_dtype("x", x)
+    rows = _rows("out", out, dev)
+    xp = _in("x", x, x.dtype, (n, rows.c), dev)
+    gp = _opt("g", g, torch.float32, (rows.c - rows.rope_dims,), dev)
+    pp, sp = _in("pos", pos, torch.int64, (n,), dev), _opt("seq", seq, torch.int32, (n,), dev)
     B, p, mp, pr, of = _row_map(pages, page_rows, off, dev)
-    with _current(dev):
-        st = _lib.latent_append(_ptr(x), _dtype_code(x), n, _ptr(g), float(eps), float(base), _ptr(pos), _ptr(seq), B, p, mp,
-                                pr, of, ctypes.byref(out._c()), _stream(stream))
-    _check("latent_append", st)
+    _launch("latent_append", dev, stream, (xp, dt, n, gp, eps, base, pp, sp, B, p, mp, pr, of, ctypes.byref(rows)))
     return out
 
 
@@ -525,25 +526,20 @@ def latent_gather(rows: KvRows, cu, n: int | None = None, start=None, pages=None
     """Positions start[b] .. start[b] + cu[b+1] - cu[b] - 1 of every sequence, dequantised and packed at
     rows cu[b] ..; returns (lat [n, R], rope [n, rd]).  With lat and rope None both are allocated with n
     rows of ``dtype``; with one of them given only that one is written."""
-    dev = rows.fp8.device
-    _kv_operand("rows", rows, dev)
+    dev = rows.fp8.get_device()
+    r = _rows("rows", rows, dev)
     B, p, mp, pr, of = _row_map(pages, page_rows, off, dev)
-    _operand("cu", cu, (torch.int64,), (B + 1,), dev)
-    _operand("start", start, (torch.int64,), (B,), dev, optional=True)
-    R, rd = rows.c - rows.rope_dims, rows.rope_dims
+    cp, sp = _in("cu", cu, torch.int64, (B + 1,), dev), _opt("start", start, torch.int64, (B,), dev)
+    R, rd = r.c - r.rope_dims, r.rope_dims
     if lat is None and rope is None:
         if n is None:
             raise ValueError("n (output rows) is needed without lat and rope")
-        lat = torch.empty((n, R), dtype=dtype, device=dev)
-        rope = torch.empty((n, rd), dtype=dtype, device=dev)
-    n = (lat if lat is not None else rope).shape[0]
-    dt = (lat if lat is not None else rope).dtype
-    _operand("lat", lat, (torch.float32, torch.bfloat16), (n, R), dev, optional=True)
-    _operand("rope", rope, (dt,), (n, rd), dev, optional=True)
-    with _current(dev):
-        st = _lib.latent_gather(ctypes.byref(rows._c()), _ptr(cu), _ptr(start), B, p, mp, pr, of, n, _ptr(lat), _ptr(rope),
-                                CSA_F32 if dt == torch.float32 else CSA_BF16, _stream(stream))
-    _check("latent_gather", st)
+        lat = torch.empty((n, R), dtype=dtype, device=cu.device)
+        rope = torch.empty((n, rd), dtype=dtype, device=cu.device)
+    one = lat if lat is not None else rope
+    n, dt = one.shape[0], _float_dtype("the output", one)
+    lp, rp = _opt("lat", lat, one.dtype, (n, R), dev), _opt("rope", rope, one.dtype, (n, rd), dev)
+    _launch("latent_gather", dev, stream, (ctypes.byref(r), cp, sp, B, p, mp, pr, of, n, lp, rp, dt))
     return lat, rope
 
 
@@ -555,26 +551,27 @@ def latent_attn_decode(q, rows: KvRows, pos, scale: float, max_len: int, pages=N
                        lse=None, workspace=None, stream=None):
     """Absorbed latent attention of Lq new tokens per sequence, q [B, Lq, H, R + rd] bf16, over the latent
     cache; token j sits at pos[b] + j and sees every position up to its own.  Returns o [B, Lq, H, R]."""
-    dev = q.device
-    _operand("q", q, (torch.bfloat16,), (None, None, None, rows.c))
+    dev = q.get_device()
+    r = _rows("rows", rows, dev)
     B, Lq, H, _ = q.shape
-    R = rows.c - rows.rope_dims
-    _kv_operand("rows", rows, dev)
-    _operand("pos", pos, (torch.int64,), (B,), dev)
+    R = r.c - r.rope_dims
+    qp, pp = _in("q", q, torch.bfloat16, (B, Lq, H, r.c), dev), _in("pos", pos, torch.int64, (B,), dev)
     nb, p, mp, pr, of = _row_map(pages, page_rows, off, dev)
     if nb != B:
         raise ValueError(f"{B} sequences, but a row map of {nb}")
     if o is None:
-        o = torch.empty((B, Lq, H, R), dtype=torch.bfloat16, device=dev)
-    _operand("o", o, (torch.bfloat16,), (B, Lq, H, R), dev)
-    _operand("lse", lse, (torch.float32,), (B, Lq, H), dev, optional=True)
-    with _current(dev):
-        if workspace is None:
-            workspace = torch.empty((latent_attn_decode_workspace_size(B, Lq, H, R, max_len),), dtype=torch.uint8, device=dev)
-        _operand("workspace", workspace, (torch.uint8,), (None,), dev)
-        st = _lib.latent_attn_decode(_ptr(q), ctypes.byref(rows._c()), _ptr(pos), p, mp, pr, of, float(scale), B, Lq, H,
-                                     int(max_len), _ptr(o), _ptr(lse), _ptr(workspace), workspace.numel(), _stream(stream))
-    _check("latent_attn_decode", st)
+        o = torch.empty((B, Lq, H, R), dtype=torch.bfloat16, device=q.device)
+    op, lp = _in("o", o, torch.bfloat16, (B, Lq, H, R), dev), _opt("lse", lse, torch.float32, (B, Lq, H), dev)
+    if workspace is None:
+        if dev >= 0 and dev != torch.cuda.current_device():
+            with torch.cuda.device(dev):
+                need = latent_attn_decode_workspace_size(B, Lq, H, R, max_len)
+        else:
+            need = latent_attn_decode_workspace_size(B, Lq, H, R, max_len)
+        workspace = torch.empty((need,), dtype=torch.uint8, device=q.device)
+    ws = workspace.numel()
+    wp = _in("workspace", workspace, torch.uint8, (ws,), dev)
+    _launch("latent_attn_decode", dev, stream, (qp, ctypes.byref(r), pp, p, mp, pr, of, scale, B, Lq, H, max_len, op, lp, wp, ws))
     return o
 
 
@@ -582,27 +579,20 @@ def latent_attn_prefill(q, kv, k_rope, cu_q, cu_k, max_q: int, scale: float, cau
                         stream=None):
     """Expanded latent attention over packed sequences: q [Tq, H, dn + dr], kv [Tk, H, dn + dv] (a head's
     unrotated key, then its value), k_rope [Tk, dr] shared by the heads.  Returns o [Tq, H, dv]."""
-    dev, dt = q.device, q.dtype
-    _operand("q", q, (torch.float32, torch.bfloat16), (None, None, None))
-    Tq, H, dk = q.shape
-    _operand("kv", kv, (dt,), (None, H, None), dev)
-    Tk = kv.shape[0]
-    _operand("k_rope", k_rope, (dt,), (Tk, None), dev)
-    dr = k_rope.shape[1]
+    dev, t, dt = q.get_device(), q.dtype, _float_dtype("q", q)
+    (Tq, H, dk), (Tk, _, dkv), dr, B = q.shape, kv.shape, k_rope.shape[1], cu_q.shape[0] - 1
     dn = dk - dr
-    dv = kv.shape[2] - dn
-    _operand("cu_q", cu_q, (torch.int64,), (None,), dev)
-    B = cu_q.shape[0] - 1
-    _operand("cu_k", cu_k, (torch.int64,), (B + 1,), dev)
+    dv = dkv - dn
+    qp, kp = _in("q", q, t, (Tq, H, dk), dev), _in("kv", kv, t, (Tk, H, dkv), dev)
+    rp = _in("k_rope", k_rope, t, (Tk, dr), dev)
+    cq, ck = _in("cu_q", cu_q, torch.int64, (B + 1,), dev), _in("cu_k", cu_k, torch.int64, (B + 1,), dev)
     if o is None:
-        o = torch.empty((Tq, H, dv), dtype=dt, device=dev) if dv > 0 else None
-    _operand("o", o, (dt,), (Tq, H, dv), dev)
-    _operand("lse", lse, (torch.float32,), (Tq, H), dev, optional=True)
-    with _current(dev):
-        st = _lib.latent_attn_prefill(_ptr(q), _ptr(kv), _ptr(k_rope), _ptr(cu_q), _ptr(cu_k), B, Tq, Tk, H, dn, dr, dv,
-                                      int(max_q), float(scale), 1 if causal else 0, _dtype_code(q), _ptr(o), _ptr(lse),
-                                      _stream(stream))
-    _check("latent_attn_prefill", st)
+        if dv < 1:
+            raise ValueError(f"kv has {dkv} channels a head, of which {dn} are the key's")
+        o = torch.empty((Tq, H, dv), dtype=t, device=q.device)
+    op, lp = _in("o", o, t, (Tq, H, dv), dev), _opt("lse", lse, torch.float32, (Tq, H), dev)
+    _launch("latent_attn_prefill", dev, stream,
+            (qp, kp, rp, cq, ck, B, Tq, Tk, H, dn, dr, dv, max_q, scale, 1 if causal else 0, dt, op, lp))
     return o
 
 

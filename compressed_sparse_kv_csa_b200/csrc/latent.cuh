@@ -5,6 +5,8 @@
 // the expanded keys and values.
 #pragma once
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace csa {
@@ -209,6 +211,26 @@ template <class Split> struct LatentWalk {
         return false;
     }
 };
+
+// Shared memory and, for a kernel that splits its registers between warpgroups (regs > 0), the registers that
+// it was compiled to (another number would let the split wait for ever): set and checked once for each device.
+template <class Kernel> inline cudaError_t prepare_kernel(Kernel kernel, size_t smem, int regs, std::atomic<bool> (&done)[64])
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 64 && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    if (regs > 0) {
+        cudaFuncAttributes fa;
+        e = cudaFuncGetAttributes(&fa, kernel);
+        if (e != cudaSuccess) return e;
+        if (fa.numRegs != regs) return cudaErrorInvalidConfiguration;
+    }
+    if (dev < 64) done[dev].store(true, std::memory_order_release);
+    return cudaSuccess;
+}
 
 cudaError_t launch_latent_decode_generic(LatentDecodeArgs a, cudaStream_t st);
 size_t latent_decode_generic_workspace(int64_t B, int Lq, int H, int R, int64_t max_len, int *grid, int *par);

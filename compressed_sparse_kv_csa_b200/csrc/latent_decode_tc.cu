@@ -993,12 +993,9 @@ cudaError_t launch_latent_decode_tc(const LatentDecodeArgs &a, cudaStream_t st)
         const cuuint32_t box[2] = {2 * kRd, rows};
         if (!ok || !encode_u8(&maps.rope, a.rows.rope, 2, dims, strides, box)) return cudaErrorNotSupported;
     }
-    cudaError_t e = cudaFuncSetAttribute(latent_decode_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_ALLOC);
+    static std::atomic<bool> done[64];
+    cudaError_t e = prepare_kernel(latent_decode_tc_kernel, SMEM_ALLOC, kRegs, done);
     if (e != cudaSuccess) return e;
-    cudaFuncAttributes fa;
-    e = cudaFuncGetAttributes(&fa, latent_decode_tc_kernel);
-    if (e != cudaSuccess) return e;
-    if (fa.numRegs != kRegs) return cudaErrorInvalidConfiguration; // the register split would wait for ever
     latent_decode_tc_kernel<<<(unsigned)a.grid, kThreads, SMEM_ALLOC, st>>>(a, maps);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;

@@ -439,12 +439,9 @@ cudaError_t launch_latent_prefill_tc(const LatentPrefillArgs &a, cudaStream_t st
     if (!encode_heads(&maps.q, a.q, a.Tq, a.H, kDn + kDr) || !encode_heads(&maps.kv, a.kv, a.Tk, a.H, kDn + kDv) ||
         !tma::encode_bf16_rows(&maps.kr, a.k_rope, (uint64_t)a.Tk, kDr, kT))
         return cudaErrorNotSupported;
-    cudaError_t e = cudaFuncSetAttribute(latent_prefill_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_ALLOC);
+    static std::atomic<bool> done[64];
+    cudaError_t e = prepare_kernel(latent_prefill_tc_kernel, SMEM_ALLOC, kRegs, done);
     if (e != cudaSuccess) return e;
-    cudaFuncAttributes fa;
-    e = cudaFuncGetAttributes(&fa, latent_prefill_tc_kernel);
-    if (e != cudaSuccess) return e;
-    if (fa.numRegs != kRegs) return cudaErrorInvalidConfiguration; // the register split would wait for ever
     const int64_t blocks = a.B * a.H * ((a.max_q + 2 * kT - 1) / (2 * kT));
     if (blocks >= ((int64_t)1 << 31)) return cudaErrorInvalidValue;
     latent_prefill_tc_kernel<<<(unsigned)blocks, kThreads, SMEM_ALLOC, st>>>(a, maps);

@@ -118,6 +118,8 @@ def test_binding_refuses_operands_it_would_misread(C):
     with pytest.raises(ValueError):
         C.latent_gather(rows, torch.zeros((2,), dtype=torch.int64), n=4, **go)
     cu = torch.zeros((3,), dtype=torch.int64)
+    with pytest.raises(ValueError):
+        C.latent_attn_prefill(torch.zeros((4, 2, 64)), torch.zeros((4, 2, 0)), torch.zeros((4, 64)), cu, cu, 4, 1.0)
     with pytest.raises(TypeError):
         C.latent_attn_prefill(torch.zeros((4, 2, 192)), torch.zeros((4, 2, 256), dtype=torch.bfloat16), torch.zeros((4, 64)), cu, cu, 4, 1.0)
     with pytest.raises(ValueError):
