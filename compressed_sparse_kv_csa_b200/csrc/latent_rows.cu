@@ -12,104 +12,181 @@ namespace csa {
 
 namespace {
 
-constexpr int kMaxVec = 4; // append: 8-channel vectors per lane, R <= 32 * 8 * 4 = 1024
 constexpr double kTwoPi = 6.283185307179586476925287;
 
-__device__ __forceinline__ void ld8(const float *p, float (&v)[8])
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
 {
-    const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
 }
-__device__ __forceinline__ void ld8(const uint16_t *p, float (&v)[8])
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) // (the products are not fused into what follows)
 {
-    const uint4 u = *reinterpret_cast<const uint4 *>(p);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+    float2 d;
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
 }
 
-// The rotation of pair i at position p is by p * base^(-2i/rd).  The angle of a far position needs
-// more than 24 bits before its whole turns are taken off, so it is formed and reduced in 64 bits; the
-// sine and cosine of what is left are taken in 32.  The frequency of a lane's pair is computed once
-// for all rows of the warp.
-template <typename Tin> __global__ void __launch_bounds__(256) latent_append_kernel(LatentAppendArgs a)
+// 8 channels as they are stored.
+template <typename T> struct Raw8;
+template <> struct Raw8<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float *p)
+    {
+        a = __ldcs(reinterpret_cast<const float4 *>(p));
+        b = __ldcs(reinterpret_cast<const float4 *>(p + 4));
+    }
+    __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ void get(float2 (&v)[4]) const
+    {
+        v[0] = make_float2(a.x, a.y), v[1] = make_float2(a.z, a.w), v[2] = make_float2(b.x, b.y), v[3] = make_float2(b.z, b.w);
+    }
+};
+template <> struct Raw8<uint16_t> {
+    uint4 u;
+    __device__ __forceinline__ void load(const uint16_t *p) { u = __ldcs(reinterpret_cast<const uint4 *>(p)); }
+    __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void get(float2 (&v)[4]) const
+    {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+    }
+};
+
+__device__ __forceinline__ float2 pair_of(const float *p) { return __ldcs(reinterpret_cast<const float2 *>(p)); }
+__device__ __forceinline__ float2 pair_of(const uint16_t *p)
+{
+    const uint32_t w = __ldcs(reinterpret_cast<const uint32_t *>(p));
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+
+// 8 values over the row's scale as E4M3 codes, each the code of the IEEE quotient v / sc, as the library's other
+// quantisers take it.  One reciprocal serves the row: with inv = 1 / sc rounded to nearest, q = v inv, r = v - q sc (exact
+// in a fused multiply-add) and q + r inv is the correctly rounded quotient (Markstein, "Computation of elementary
+// functions on the IBM RISC System/6000 processor", 1990) as long as nothing leaves the normal range: scales outside
+// 2^-90 .. 2^90 are divided one by one.
+__device__ __forceinline__ uint2 encode8(const float2 (&v)[4], float sc, float inv, bool plain)
+{
+    uint32_t w[2] = {0, 0};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        float2 q;
+        if (plain) {
+            const float2 i2 = make_float2(inv, inv);
+            q = mul2(v[e], i2);
+            q = fma2(fma2(q, make_float2(-sc, -sc), v[e]), i2, q);
+        } else {
+            q = make_float2(__fdiv_rn(v[e].x, sc), __fdiv_rn(v[e].y, sc));
+        }
+        w[e >> 1] |= (uint32_t)__nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3) << (16 * (e & 1));
+    }
+    // -0 is stored as +0
+    return make_uint2(w[0] & ~(__vcmpeq4(w[0], 0x80808080u) & 0x80808080u), w[1] & ~(__vcmpeq4(w[1], 0x80808080u) & 0x80808080u));
+}
+
+// A warp takes `per` rows one after another: their places are looked up side by side, a lane each, and a row's loads
+// are under way while the row before is worked on.  Lane l holds channels 8 l + 256 k .. + 7, k < NV.
+//
+// The rotation of pair i at position p is by p * base^(-2i/rd).  The angle of a far position needs more than 24
+// bits before its whole turns are taken off, so it is formed in turns and reduced in 64 bits; the sine and
+// cosine of what is left are taken in 32.  The frequency of a lane's pair is computed once for all rows.
+template <typename Tin, int NV> __global__ void __launch_bounds__(256) latent_append_kernel(LatentAppendArgs a, double log_base, int per)
 {
     const int lane = threadIdx.x & 31;
-    const int64_t warps = (int64_t)gridDim.x * 8;
-    const int rd = a.out.rope_dims, R = a.out.c - rd;
-    const double lb = a.base > 0 ? log(a.base) : 0.0;
-    double freq = 0.0; // of pair `lane`; further pairs (rd > 64) are formed below
-    if (a.base > 0 && 2 * lane < rd) freq = exp(-(2.0 * lane / rd) * lb);
-    for (int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); i < a.n; i += warps) {
-        const int64_t p = a.pos[i];
-        if (p < 0) continue;
-        const int64_t b = a.seq ? a.seq[i] : i;
-        const int64_t row = b >= 0 && b < a.B ? a.map.row(b, p) : -1;
-        if (row < 0) {
-            if (lane == 0) flag_error(a.err, CSA_DEVERR_INDEX);
-            continue;
-        }
-        const Tin *x = static_cast<const Tin *>(a.x) + i * a.out.c;
-        float v[kMaxVec][8];
-        float ss = 0.f;
+    const int64_t i0 = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * per;
+    const int cnt = (int)min((int64_t)per, a.n - i0), rd = a.out.rope_dims, R = a.out.c - rd;
+    if (cnt <= 0) return;
+    const Tin *x = static_cast<const Tin *>(a.x) + i0 * a.out.c;
+    Raw8<Tin> next[NV];
+    float2 next_pair = make_float2(0.f, 0.f);
+    auto load = [&](int r) {
+        const Tin *xr = x + (int64_t)r * a.out.c;
 #pragma unroll
-        for (int k = 0; k < kMaxVec; ++k) {
+        for (int k = 0; k < NV; ++k) {
+            const int j = 8 * (lane + 32 * k);
+            if (j < R) next[k].load(xr + j);
+            else next[k].zero();
+        }
+        if (2 * lane < rd) next_pair = pair_of(xr + R + 2 * lane);
+    };
+    load(0);
+    int64_t my_pos = -1, my_row = -1;
+    if (lane < cnt) {
+        my_pos = a.pos[i0 + lane];
+        const int64_t b = a.seq ? a.seq[i0 + lane] : i0 + lane;
+        if (my_pos >= 0) {
+            if (b >= 0 && b < a.B) {
+                // (a position below 2^31 is divided in 32 bits)
+                my_row = my_pos >> 31 ? a.map.row(b, my_pos) : a.map.row(a.map.page(b, (uint32_t)my_pos), a.map.first(b), (uint32_t)my_pos);
+            }
+            if (my_row < 0) flag_error(a.err, CSA_DEVERR_INDEX);
+        }
+    }
+    auto turns_of = [&](int k) { return exp(-(2.0 * k / rd) * log_base) / kTwoPi; }; // of pair k, per position
+    double turns = 0.0;
+    if (a.base > 0 && 2 * lane < rd) turns = turns_of(lane);
+    float2 g[NV][4];
+    if (a.g) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
             const int j = 8 * (lane + 32 * k);
             if (j < R) {
-                ld8(x + j, v[k]);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) ss = fmaf(v[k][e], v[k][e], ss);
+                const float4 u = __ldg(reinterpret_cast<const float4 *>(a.g + j)), w = __ldg(reinterpret_cast<const float4 *>(a.g + j + 4));
+                g[k][0] = make_float2(u.x, u.y), g[k][1] = make_float2(u.z, u.w), g[k][2] = make_float2(w.x, w.y), g[k][3] = make_float2(w.z, w.w);
             }
         }
-        // the rotated part, its loads beside those above
+    }
+    for (int r = 0; r < cnt; ++r) {
+        float2 v[NV][4], pair = next_pair;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) next[k].get(v[k]);
+        if (r + 1 < cnt) load(r + 1);
+        const int64_t row = __shfl_sync(0xffffffffu, my_row, r), p = __shfl_sync(0xffffffffu, my_pos, r);
+        if (row < 0) continue; // skipped, or refused
         for (int k = lane; 2 * k < rd; k += 32) {
-            float u = ld1<Tin>(x, R + 2 * k), w = ld1<Tin>(x, R + 2 * k + 1);
+            if (k >= 32) pair = pair_of(x + (int64_t)r * a.out.c + R + 2 * k);
             if (a.base > 0) {
-                const double f = k == lane ? freq : exp(-(2.0 * k / rd) * lb);
-                const double ang = (double)p * f;
+                const double t = (double)p * (k == lane ? turns : turns_of(k));
                 float sn, cs;
-                sincosf((float)(ang - kTwoPi * rint(ang / kTwoPi)), &sn, &cs);
-                const float t = fmaf(u, cs, -w * sn);
-                w = fmaf(u, sn, w * cs);
-                u = t;
+                sincospif(2.f * (float)(t - rint(t)), &sn, &cs);
+                pair = make_float2(fmaf(pair.x, cs, -pair.y * sn), fmaf(pair.x, sn, pair.y * cs));
             }
             *reinterpret_cast<uint32_t *>(a.out.rope + row * rd + 2 * k) =
-                uint32_t(f32_to_bf16_bits(u)) | (uint32_t(f32_to_bf16_bits(w)) << 16);
+                uint32_t(f32_to_bf16_bits(pair.x)) | (uint32_t(f32_to_bf16_bits(pair.y)) << 16);
         }
         if (a.g) {
-            const float f = 1.f / sqrtf(warp_sum(ss) / (float)R + a.eps);
+            float2 ss = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int k = 0; k < kMaxVec; ++k) {
-                const int j = 8 * (lane + 32 * k);
-                if (j < R) {
-                    float g[8];
-                    ld8(a.g + j, g);
+            for (int k = 0; k < NV; ++k)
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) v[k][e] = v[k][e] * f * g[e];
-                }
-            }
+                for (int e = 0; e < 4; ++e) ss = fma2(v[k][e], v[k][e], ss);
+            const float f = 1.f / sqrtf(warp_sum(ss.x + ss.y) / (float)R + a.eps);
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (8 * (lane + 32 * k) < R) v[k][e] = mul2(mul2(v[k][e], make_float2(f, f)), g[k][e]);
         }
         float m = 0.f;
 #pragma unroll
-        for (int k = 0; k < kMaxVec; ++k)
-            if (8 * (lane + 32 * k) < R) {
+        for (int k = 0; k < NV; ++k)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(v[k][e]));
-            }
+            for (int e = 0; e < 4; ++e) m = fmaxf(m, fmaxf(fabsf(v[k][e].x), fabsf(v[k][e].y)));
         float sc = __fdiv_rn(warp_max(m), 448.f);
         if (!(sc > 0.f)) sc = 1.f;
+        const float inv = 1.f / sc;
+        const bool plain = sc > 8.0779357e-28f && sc < 1.2379400e27f; // 2^-90 .. 2^90
 #pragma unroll
-        for (int k = 0; k < kMaxVec; ++k) {
+        for (int k = 0; k < NV; ++k) {
             const int j = 8 * (lane + 32 * k);
-            if (j < R) {
-                uint32_t w[2] = {0, 0};
-#pragma unroll
-                for (int e = 0; e < 8; ++e) w[e >> 2] |= uint32_t(e4m3_encode(__fdiv_rn(v[k][e], sc))) << (8 * (e & 3));
-                *reinterpret_cast<uint2 *>(a.out.fp8 + row * R + j) = make_uint2(w[0], w[1]);
-            }
+            if (j < R) *reinterpret_cast<uint2 *>(a.out.fp8 + row * R + j) = encode8(v[k], sc, inv, plain);
         }
         if (lane == 0) a.out.scale[row] = sc;
     }
@@ -180,7 +257,11 @@ template <typename Tout> __global__ void __launch_bounds__(256) latent_gather_ke
             const uint32_t w[4] = {u[r].x, u[r].y, u[r].z, u[r].w};
             float v[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] = e4m3_decode(uint8_t(w[e >> 2] >> (8 * (e & 3)))) * s[r];
+            for (int e = 0; e < 8; ++e) {
+                const float2 x = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[e >> 1] >> (16 * (e & 1))), __NV_E4M3)));
+                v[2 * e] = x.x * s[r];
+                v[2 * e + 1] = x.y * s[r];
+            }
             st16(static_cast<Tout *>(a.lat) + (n0 + r) * R + j, v);
         }
     }
@@ -192,7 +273,12 @@ template <typename Tout> __global__ void __launch_bounds__(256) latent_gather_ke
             if (e >= kGatherRows * per || row < -1) continue;
             const int j = 8 * (e % per);
             float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            if (row >= 0) ld8(a.rows.rope + row * rd + j, v);
+            if (row >= 0) {
+                const uint4 q = __ldg(reinterpret_cast<const uint4 *>(a.rows.rope + row * rd + j));
+                const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[2 * i] = __uint_as_float(w[i] << 16), v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            }
             Tout *dst = static_cast<Tout *>(a.rope) + (n0 + r) * rd + j;
             st4(dst, 0, make_float4(v[0], v[1], v[2], v[3]));
             st4(dst, 4, make_float4(v[4], v[5], v[6], v[7]));
@@ -202,12 +288,23 @@ template <typename Tout> __global__ void __launch_bounds__(256) latent_gather_ke
 
 } // namespace
 
+template <typename Tin> static void append(const LatentAppendArgs &a, cudaStream_t st)
+{
+    // a row a warp until every SM has 32 warps, then up to 8
+    const int64_t warps = 32 * (int64_t)device_sms(), p = a.n / warps;
+    const int per = p < 1 ? 1 : p > 8 ? 8 : (int)p;
+    const unsigned grid = (unsigned)((a.n + 8 * per - 1) / (8 * per));
+    const double lb = a.base > 0 ? log(a.base) : 0.0;
+    const int R = a.out.c - a.out.rope_dims;
+    if (R <= 256) latent_append_kernel<Tin, 1><<<grid, 256, 0, st>>>(a, lb, per);
+    else if (R <= 512) latent_append_kernel<Tin, 2><<<grid, 256, 0, st>>>(a, lb, per);
+    else latent_append_kernel<Tin, 4><<<grid, 256, 0, st>>>(a, lb, per);
+}
+
 cudaError_t launch_latent_append(const LatentAppendArgs &a, int in_dtype, cudaStream_t st)
 {
-    const int64_t blocks = (a.n + 7) / 8, most = 16 * (int64_t)device_sms();
-    const unsigned grid = (unsigned)(blocks < most ? blocks : most);
-    if (in_dtype == CSA_F32) latent_append_kernel<float><<<grid, 256, 0, st>>>(a);
-    else latent_append_kernel<uint16_t><<<grid, 256, 0, st>>>(a);
+    if (in_dtype == CSA_F32) append<float>(a, st);
+    else append<uint16_t>(a, st);
     return cudaGetLastError();
 }
 

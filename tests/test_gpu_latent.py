@@ -134,6 +134,38 @@ def test_append_equals_the_quantiser_and_one_row_at_a_time(C):
         assert torch.equal(t.fp8, ref.fp8) and torch.equal(t.rope, ref.rope) and torch.equal(t.scale, ref.scale)
 
 
+@pytest.mark.parametrize("size", [1e-38, 1e-30, 1e-8, 1.0, 3e30, 1e38])
+@pytest.mark.parametrize("R", [512, 1024, 32])
+def test_append_codes_are_those_of_the_division(C, size, R):
+    """Rows whose entries lie on and beside the middles between codes, at scales down to where a reciprocal leaves
+    fp32's range: bit for bit csa_quantize_kv's, which divides."""
+    g = rng(11)
+    n = 300
+    x = torch.randn((n, R + 64), generator=g)
+    mid = (torch.randint(0, 448 * 16, (n // 2, R), generator=g).float() + 0.5) / 16  # middles, over a scale of 1
+    x[:n // 2, :R] = mid * torch.where(torch.rand((n // 2, R), generator=g) < 0.5, -1.0, 1.0)
+    x[:n // 2, 3] = 448.0
+    x = (x * size).cuda()
+    ref, out = C.KvRows.empty(n, R + 64, 64, "cuda"), C.KvRows.empty(n, R + 64, 64, "cuda")
+    C.csa_quantize_kv(x, ref)
+    C.latent_append(x, torch.zeros((n,), dtype=I64, device="cuda"), out, off=torch.arange(n, device="cuda"))
+    assert torch.equal(out.scale, ref.scale) and torch.equal(out.fp8, ref.fp8) and torch.equal(out.rope, ref.rope)
+
+
+def test_append_many_rows(C):
+    """More rows than warps: the same as a few at a time."""
+    n = 50001
+    x = torch.randn((n, 576), generator=rng(12)).to(BF16).cuda()
+    pos, off = torch.arange(n, device="cuda"), torch.zeros((1,), dtype=I64, device="cuda")
+    seq = torch.zeros((n,), dtype=I32, device="cuda")
+    gain = (1 + 0.1 * torch.randn((512,), generator=rng(13))).cuda()
+    a, b = C.KvRows.empty(n, 576, 64, "cuda"), C.KvRows.empty(n, 576, 64, "cuda")
+    C.latent_append(x, pos, a, g=gain, base=10000.0, seq=seq, off=off)
+    for i in range(0, n, 4000):
+        C.latent_append(x[i:i + 4000], pos[i:i + 4000], b, g=gain, base=10000.0, seq=seq[i:i + 4000], off=off)
+    assert torch.equal(a.fp8, b.fp8) and torch.equal(a.rope, b.rope) and torch.equal(a.scale, b.scale)
+
+
 def test_append_refused_rows(C):
     """A page outside the cache, a position behind the table and a sequence that is not there are refused,
     the other rows written."""
