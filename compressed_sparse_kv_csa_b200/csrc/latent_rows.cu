@@ -87,36 +87,42 @@ __device__ __forceinline__ uint2 encode8(const float2 (&v)[4], float sc, float i
         }
         w[e >> 1] |= (uint32_t)__nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3) << (16 * (e & 1));
     }
-    // -0 is stored as +0
-    return make_uint2(w[0] & ~(__vcmpeq4(w[0], 0x80808080u) & 0x80808080u), w[1] & ~(__vcmpeq4(w[1], 0x80808080u) & 0x80808080u));
+    // -0 is stored as +0: a sign stays where the other seven bits are not all zero
+    auto plus0 = [](uint32_t c) { return c & ((((c & 0x7f7f7f7fu) + 0x7f7f7f7fu) & 0x80808080u) | 0x7f7f7f7fu); };
+    return make_uint2(plus0(w[0]), plus0(w[1]));
 }
 
-// A warp takes `per` rows one after another: their places are looked up side by side, a lane each, and a row's loads
-// are under way while the row before is worked on.  Lane l holds channels 8 l + 256 k .. + 7, k < NV.
+constexpr int kBatch = 4; // rows that a warp works on at once
+
+// Sums (or maxima) over the warp of four values, one a row: lane l returns that of row 2 (l / 16) + (l / 8) % 2.  Six
+// shuffles for the four.
+template <class Op> __device__ __forceinline__ float reduce4(const float (&v)[kBatch], int lane, Op op)
+{
+    const bool hi = lane & 16, odd = lane & 8;
+    const float a = op(hi ? v[2] : v[0], __shfl_xor_sync(0xffffffffu, hi ? v[0] : v[2], 16));
+    const float b = op(hi ? v[3] : v[1], __shfl_xor_sync(0xffffffffu, hi ? v[1] : v[3], 16));
+    float c = op(odd ? b : a, __shfl_xor_sync(0xffffffffu, odd ? a : b, 8));
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) c = op(c, __shfl_xor_sync(0xffffffffu, c, o));
+    return c;
+}
+__device__ __forceinline__ float of_row(float v, int r) { return __shfl_sync(0xffffffffu, v, 16 * (r >> 1) + 8 * (r & 1)); }
+
+// A warp takes `per` rows, four at once: their loads are in flight together, their places are looked up side by side (a
+// lane each), and what a row needs once -- a root, three divisions -- is computed by different lanes for the four.
+// Lane l holds channels 8 l + 256 k .. + 7, k < NV.  64k rows of 512 + 64 bf16 channels: 442 instructions a row and
+// 63 us one row at a time.
 //
-// The rotation of pair i at position p is by p * base^(-2i/rd).  The angle of a far position needs more than 24
-// bits before its whole turns are taken off, so it is formed in turns and reduced in 64 bits; the sine and
-// cosine of what is left are taken in 32.  The frequency of a lane's pair is computed once for all rows.
-template <typename Tin, int NV> __global__ void __launch_bounds__(256) latent_append_kernel(LatentAppendArgs a, double log_base, int per)
+// The rotation of pair i at position p is by p * base^(-2i/rd).  The frequency of a lane's pair is computed once for all
+// rows, in 64-bit floating point, as a fraction of a turn of 64 bits; a 64-bit product with the position drops
+// the whole turns by itself, and the sine and cosine of what is left are taken in 32 bits.
+template <typename Tin, int NV> __global__ void __launch_bounds__(256, NV > 2 ? 1 : 2) latent_append_kernel(LatentAppendArgs a, double log_base, int per)
 {
     const int lane = threadIdx.x & 31;
     const int64_t i0 = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * per;
     const int cnt = (int)min((int64_t)per, a.n - i0), rd = a.out.rope_dims, R = a.out.c - rd;
     if (cnt <= 0) return;
     const Tin *x = static_cast<const Tin *>(a.x) + i0 * a.out.c;
-    Raw8<Tin> next[NV];
-    float2 next_pair = make_float2(0.f, 0.f);
-    auto load = [&](int r) {
-        const Tin *xr = x + (int64_t)r * a.out.c;
-#pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int j = 8 * (lane + 32 * k);
-            if (j < R) next[k].load(xr + j);
-            else next[k].zero();
-        }
-        if (2 * lane < rd) next_pair = pair_of(xr + R + 2 * lane);
-    };
-    load(0);
     int64_t my_pos = -1, my_row = -1;
     if (lane < cnt) {
         my_pos = a.pos[i0 + lane];
@@ -129,66 +135,96 @@ template <typename Tin, int NV> __global__ void __launch_bounds__(256) latent_ap
             if (my_row < 0) flag_error(a.err, CSA_DEVERR_INDEX);
         }
     }
-    auto turns_of = [&](int k) { return exp(-(2.0 * k / rd) * log_base) / kTwoPi; }; // of pair k, per position
-    double turns = 0.0;
+    auto turns_of = [&](int k) { return (uint64_t)(exp(-(2.0 * k / rd) * log_base) / kTwoPi * 18446744073709551616.0); }; // pair k, a position
+    uint64_t turns = 0;
     if (a.base > 0 && 2 * lane < rd) turns = turns_of(lane);
-    float2 g[NV][4];
-    if (a.g) {
+    for (int r0 = 0; r0 < cnt; r0 += kBatch) {
+        Raw8<Tin> raw[kBatch][NV];
+        float2 pair[kBatch];
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int j = 8 * (lane + 32 * k);
-            if (j < R) {
-                const float4 u = __ldg(reinterpret_cast<const float4 *>(a.g + j)), w = __ldg(reinterpret_cast<const float4 *>(a.g + j + 4));
-                g[k][0] = make_float2(u.x, u.y), g[k][1] = make_float2(u.z, u.w), g[k][2] = make_float2(w.x, w.y), g[k][3] = make_float2(w.z, w.w);
+        for (int r = 0; r < kBatch; ++r) {
+            const Tin *xr = x + (int64_t)(r0 + r) * a.out.c;
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                const int j = 8 * (lane + 32 * k);
+                if (r0 + r < cnt && j < R) raw[r][k].load(xr + j);
+                else raw[r][k].zero();
+            }
+            if (r0 + r < cnt && 2 * lane < rd) pair[r] = pair_of(xr + R + 2 * lane);
+        }
+        int64_t row[kBatch]; // negative: skipped, refused or not there
+#pragma unroll
+        for (int r = 0; r < kBatch; ++r) row[r] = r0 + r < cnt ? __shfl_sync(0xffffffffu, my_row, (r0 + r) & 31) : -1;
+#pragma unroll
+        for (int r = 0; r < kBatch; ++r) {
+            const uint64_t p = (uint64_t)__shfl_sync(0xffffffffu, my_pos, (r0 + r) & 31);
+            if (row[r] < 0) continue;
+            for (int k = lane; 2 * k < rd; k += 32) {
+                if (k >= 32) pair[r] = pair_of(x + (int64_t)(r0 + r) * a.out.c + R + 2 * k);
+                if (a.base > 0) {
+                    const uint64_t t = p * (k == lane ? turns : turns_of(k));
+                    float sn, cs;
+                    sincospif((float)(int32_t)(t >> 32) * 4.656612873077393e-10f, &sn, &cs); // half turns, -1 .. 1
+                    pair[r] = make_float2(fmaf(pair[r].x, cs, -pair[r].y * sn), fmaf(pair[r].x, sn, pair[r].y * cs));
+                }
+                *reinterpret_cast<uint32_t *>(a.out.rope + row[r] * rd + 2 * k) =
+                    uint32_t(f32_to_bf16_bits(pair[r].x)) | (uint32_t(f32_to_bf16_bits(pair[r].y)) << 16);
             }
         }
-    }
-    for (int r = 0; r < cnt; ++r) {
-        float2 v[NV][4], pair = next_pair;
+        float2 v[kBatch][NV][4];
 #pragma unroll
-        for (int k = 0; k < NV; ++k) next[k].get(v[k]);
-        if (r + 1 < cnt) load(r + 1);
-        const int64_t row = __shfl_sync(0xffffffffu, my_row, r), p = __shfl_sync(0xffffffffu, my_pos, r);
-        if (row < 0) continue; // skipped, or refused
-        for (int k = lane; 2 * k < rd; k += 32) {
-            if (k >= 32) pair = pair_of(x + (int64_t)r * a.out.c + R + 2 * k);
-            if (a.base > 0) {
-                const double t = (double)p * (k == lane ? turns : turns_of(k));
-                float sn, cs;
-                sincospif(2.f * (float)(t - rint(t)), &sn, &cs);
-                pair = make_float2(fmaf(pair.x, cs, -pair.y * sn), fmaf(pair.x, sn, pair.y * cs));
-            }
-            *reinterpret_cast<uint32_t *>(a.out.rope + row * rd + 2 * k) =
-                uint32_t(f32_to_bf16_bits(pair.x)) | (uint32_t(f32_to_bf16_bits(pair.y)) << 16);
-        }
+        for (int r = 0; r < kBatch; ++r)
+#pragma unroll
+            for (int k = 0; k < NV; ++k) raw[r][k].get(v[r][k]);
+        float s[kBatch];
         if (a.g) {
-            float2 ss = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int r = 0; r < kBatch; ++r) {
+                float2 ss = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int k = 0; k < NV; ++k)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) ss = fma2(v[r][k][e], v[r][k][e], ss);
+                s[r] = ss.x + ss.y;
+            }
+            const float f = 1.f / sqrtf(reduce4(s, lane, [](float x, float y) { return x + y; }) / (float)R + a.eps);
+#pragma unroll
+            for (int r = 0; r < kBatch; ++r) s[r] = of_row(f, r);
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                const int j = 8 * (lane + 32 * k);
+                if (j >= R) continue;
+                const float4 u = __ldg(reinterpret_cast<const float4 *>(a.g + j)), w = __ldg(reinterpret_cast<const float4 *>(a.g + j + 4));
+                const float2 g[4] = {make_float2(u.x, u.y), make_float2(u.z, u.w), make_float2(w.x, w.y), make_float2(w.z, w.w)};
+#pragma unroll
+                for (int r = 0; r < kBatch; ++r)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[r][k][e] = mul2(mul2(v[r][k][e], make_float2(s[r], s[r])), g[e]);
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < kBatch; ++r) {
+            s[r] = 0.f;
 #pragma unroll
             for (int k = 0; k < NV; ++k)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) ss = fma2(v[k][e], v[k][e], ss);
-            const float f = 1.f / sqrtf(warp_sum(ss.x + ss.y) / (float)R + a.eps);
-#pragma unroll
-            for (int k = 0; k < NV; ++k)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (8 * (lane + 32 * k) < R) v[k][e] = mul2(mul2(v[k][e], make_float2(f, f)), g[k][e]);
+                for (int e = 0; e < 4; ++e) s[r] = fmaxf(s[r], fmaxf(fabsf(v[r][k][e].x), fabsf(v[r][k][e].y)));
         }
-        float m = 0.f;
+        float my_sc = __fdiv_rn(reduce4(s, lane, [](float x, float y) { return fmaxf(x, y); }), 448.f);
+        if (!(my_sc > 0.f)) my_sc = 1.f;
+        const float my_inv = 1.f / my_sc;
+        const bool plain = __all_sync(0xffffffffu, my_sc > 8.0779357e-28f && my_sc < 1.2379400e27f); // 2^-90 .. 2^90
 #pragma unroll
-        for (int k = 0; k < NV; ++k)
+        for (int r = 0; r < kBatch; ++r) {
+            const float sc = of_row(my_sc, r), inv = of_row(my_inv, r);
+            if (row[r] < 0) continue;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) m = fmaxf(m, fmaxf(fabsf(v[k][e].x), fabsf(v[k][e].y)));
-        float sc = __fdiv_rn(warp_max(m), 448.f);
-        if (!(sc > 0.f)) sc = 1.f;
-        const float inv = 1.f / sc;
-        const bool plain = sc > 8.0779357e-28f && sc < 1.2379400e27f; // 2^-90 .. 2^90
-#pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int j = 8 * (lane + 32 * k);
-            if (j < R) *reinterpret_cast<uint2 *>(a.out.fp8 + row * R + j) = encode8(v[k], sc, inv, plain);
+            for (int k = 0; k < NV; ++k) {
+                const int j = 8 * (lane + 32 * k);
+                if (j < R) *reinterpret_cast<uint2 *>(a.out.fp8 + row[r] * R + j) = encode8(v[r][k], sc, inv, plain);
+            }
+            if (lane == 0) a.out.scale[row[r]] = sc;
         }
-        if (lane == 0) a.out.scale[row] = sc;
     }
 }
 
@@ -290,9 +326,9 @@ template <typename Tout> __global__ void __launch_bounds__(256) latent_gather_ke
 
 template <typename Tin> static void append(const LatentAppendArgs &a, cudaStream_t st)
 {
-    // a row a warp until every SM has 32 warps, then up to 8
-    const int64_t warps = 32 * (int64_t)device_sms(), p = a.n / warps;
-    const int per = p < 1 ? 1 : p > 8 ? 8 : (int)p;
+    // as many rows a warp as make one wave of 16 warps an SM, at most 32 (a lane looks up each)
+    const int64_t warps = 16 * (int64_t)device_sms(), p = (a.n + warps - 1) / warps;
+    const int per = p < kBatch ? (int)p : p > 32 ? 32 : (int)(p + kBatch - 1) / kBatch * kBatch;
     const unsigned grid = (unsigned)((a.n + 8 * per - 1) / (8 * per));
     const double lb = a.base > 0 ? log(a.base) : 0.0;
     const int R = a.out.c - a.out.rope_dims;

@@ -420,7 +420,7 @@ int csa_decode_glue(const void *o, const void *P, const void *Rm, int64_t R, int
  * outside [0, B) is refused.  Per row, in fp32:
  *   u = x[0:R];  u = u / sqrt(mean(u^2) + eps) * g                       when g != NULL (g [R] fp32)
  *   v = x[R:c];  the pairs (2k, 2k+1) of v rotated counter-clockwise by   when base != 0
- *       pos[i] * base^(-2k/rd)                                            (angles in fp64)
+ *       pos[i] * base^(-2k/rd)                                            (angles to 2^-25 of a turn at 2^31)
  *   s = amax(|u|) / 448 (1 when that is not positive), fp8 = e4m3(u / s), rope = bf16(v)
  * as csa_quantize_kv quantises.  The (sequence, position) pairs of one call have to be distinct: of
  * rows written to the same place at once, an unspecified mixture remains.
