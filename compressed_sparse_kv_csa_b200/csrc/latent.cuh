@@ -235,11 +235,11 @@ template <class Kernel> inline cudaError_t prepare_kernel(Kernel kernel, size_t 
 cudaError_t launch_latent_decode_generic(LatentDecodeArgs a, cudaStream_t st);
 size_t latent_decode_generic_workspace(int64_t B, int Lq, int H, int R, int64_t max_len, int *grid, int *par);
 
-// 512 + 64 channels on the tensor cores (blocks of 32 rows, tiles of 128 keys).
+// 512 + 64 channels on the tensor cores (blocks of 32 rows with tiles of 128 keys, or of 64 with 64).
 bool latent_decode_tc_eligible(int R, int rd);
 size_t latent_decode_tc_workspace(int64_t B, int Lq, int H, int64_t max_len, int *grid, int *par);
 cudaError_t launch_latent_decode_tc(const LatentDecodeArgs &a, cudaStream_t st);
-cudaError_t launch_latent_merge_32x128(const LatentDecodeArgs &a, cudaStream_t st);
+cudaError_t launch_latent_merge_tc(const LatentDecodeArgs &a, int rows, cudaStream_t st);
 
 struct LatentPrefillArgs {
     const void *q, *kv, *k_rope; // [Tq, H, dn + dr], [Tk, H, dn + dv], [Tk, dr]

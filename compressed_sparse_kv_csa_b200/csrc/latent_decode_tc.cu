@@ -39,36 +39,15 @@ namespace {
 
 using namespace tc;
 
-constexpr int kR = 512, kRd = 64, kRB = 32, kKT = 128, kStages = 2;
+constexpr int kR = 512, kRd = 64;
 constexpr int kSoftThreads = 256, kProdWarp0 = 8, kMmaWarp = 10, kThreads = 384; // whole warpgroups, for the register split
 // Of the registers that the block is launched with (168 a thread, checked on the host), the two softmax warpgroups take 192
 // a thread and the other leaves 120.
 constexpr int kRegs = 168, kRegsSoft = 192, kRegsRest = 120;
 static_assert(256 * kRegsSoft + 128 * kRegsRest <= kThreads * kRegs, "register split");
-// operand tiles of 128-byte rows, 128-byte swizzle: 64 rows of q and v, 128 keys
-constexpr uint32_t kQSlice = 8192, kPTile = 8192, kSlice = 16384;
-constexpr uint32_t OFF_P = 0;                         // v: two buffers
-constexpr uint32_t OFF_K = 2 * kPTile;                // kStages x 5 slices: 4 of 128 latent channels, 1 of the rotated ones
-constexpr uint32_t OFF_Q = OFF_K + kStages * 5 * kSlice; // 4 slices, 1 of the rotated channels
-constexpr uint32_t OFF_SC = OFF_Q + 5 * kQSlice;
-constexpr uint32_t OFF_XCH = OFF_SC + kStages * kKT * 4;     // [2 buffers][4 key quarters][32 rows]
-constexpr uint32_t OFF_BAR = OFF_XCH + 2 * 4 * 32 * 4;
-constexpr uint32_t OFF_AT = OFF_BAR + 160;            // where the CTA's walk begins (4 x int64)
-constexpr uint32_t OFF_TMEM = OFF_AT + 32;
-constexpr uint32_t SMEM_ALLOC = OFF_TMEM + 64 + 1024;
-static_assert(SMEM_ALLOC <= 232448, "shared memory per block");
-enum { B_KFULL = 0, B_KEMPTY = B_KFULL + kStages, B_S = B_KEMPTY + kStages, B_P = B_S + 2, B_Q = B_P + 2, B_ALL, B_ROWS, B_TAIL = B_ROWS + 2, B_FINAL, NUM_BARS };
-static_assert(8 * NUM_BARS <= 160, "barrier space");
-// TMEM columns: O (two N = 256 accumulators, 128 columns each), S_n and S_r (two buffers of 64 each)
-constexpr uint32_t kColO = 0, kColSn = 256, kColSr = 384, kTmemCols = 512;
-constexpr uint32_t IDESC_SN = (1u << 4) | ((uint32_t)(kKT >> 3) << 17) | (4u << 24); // M = 64, E4M3 x E4M3
-constexpr uint32_t IDESC_SR = idesc_bf16_f32(64, kKT, false, false);
-constexpr uint32_t IDESC_O = (1u << 4) | (1u << 16) | ((uint32_t)(256 >> 3) << 17) | (4u << 24); // M = 64, B MN-major
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr uint32_t kNoKey = 0xffffffffu; // in place of a row's scale: the key is not to be seen
 constexpr float kTop = 448.f, kLow = 1.f / 16.f, kSmallestScale = 7.8886090522101181e-31f; // 2^-100
-
-using Split = LatentSplit<kRB, kKT, 2>;
 
 // A descriptor as two words, so that a step along an operand is one 32-bit addition (the issuing thread's
 // instructions between two MMAs bound the chain as much as the MMAs do).
@@ -121,8 +100,9 @@ __device__ __forceinline__ float2 e4m3x2_value(uint32_t c)
     return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)c, __NV_E4M3)));
 }
 
-// 16 values as hi and lo * lo_scale, 16 E4M3 codes each.
-__device__ __forceinline__ void split16(const float2 (&v)[8], float lo_scale, uint32_t (&hi)[4], uint32_t (&lo)[4])
+// 16 values as two terms, 16 codes each: hi in E4M3, and what is left either 16 times as large in E4M3 or as it is in
+// E5M2 (which has the range for it).
+template <bool E5M2> __device__ __forceinline__ void split16(const float2 (&v)[8], float lo_scale, uint32_t (&hi)[4], uint32_t (&lo)[4])
 {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -133,18 +113,12 @@ __device__ __forceinline__ void split16(const float2 (&v)[8], float lo_scale, ui
             const uint32_t c = e4m3x2(a.x, a.y);
             const float2 x = e4m3x2_value(c);
             hi[i] |= c << (16 * h);
-            lo[i] |= e4m3x2((a.x - x.x) * lo_scale, (a.y - x.y) * lo_scale) << (16 * h);
+            lo[i] |= (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2((a.x - x.x) * lo_scale, (a.y - x.y) * lo_scale), __NV_SATFINITE,
+                                                        E5M2 ? __NV_E5M2 : __NV_E4M3)
+                     << (16 * h);
         }
     }
 }
-
-using Walk = LatentWalk<Split>;
-
-struct Ctx {
-    uint32_t base, tmem;
-    __device__ __forceinline__ uint32_t bar(int b) const { return base + OFF_BAR + 8u * (uint32_t)b; }
-    __device__ __forceinline__ uint32_t stage(uint32_t n) const { return base + OFF_K + (n % kStages) * 5u * kSlice; }
-};
 
 struct Maps {
     CUtensorMap lat, rope;
@@ -165,9 +139,123 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void *src, uint32_t b
 
 __device__ __forceinline__ void sts1(uint32_t dst, uint32_t v) { asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst), "r"(v) : "memory"); }
 
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ void tmem_ld32_pairs(uint32_t taddr, float2 (&r)[16])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+                 : "=f"(r[0].x), "=f"(r[0].y), "=f"(r[1].x), "=f"(r[1].y), "=f"(r[2].x), "=f"(r[2].y), "=f"(r[3].x), "=f"(r[3].y),
+                   "=f"(r[4].x), "=f"(r[4].y), "=f"(r[5].x), "=f"(r[5].y), "=f"(r[6].x), "=f"(r[6].y), "=f"(r[7].x), "=f"(r[7].y),
+                   "=f"(r[8].x), "=f"(r[8].y), "=f"(r[9].x), "=f"(r[9].y), "=f"(r[10].x), "=f"(r[10].y), "=f"(r[11].x), "=f"(r[11].y),
+                   "=f"(r[12].x), "=f"(r[12].y), "=f"(r[13].x), "=f"(r[13].y), "=f"(r[14].x), "=f"(r[14].y), "=f"(r[15].x), "=f"(r[15].y)
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld16_pairs(uint32_t taddr, float2 (&r)[8])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : "=f"(r[0].x), "=f"(r[0].y), "=f"(r[1].x), "=f"(r[1].y), "=f"(r[2].x), "=f"(r[2].y), "=f"(r[3].x), "=f"(r[3].y),
+                   "=f"(r[4].x), "=f"(r[4].y), "=f"(r[5].x), "=f"(r[5].y), "=f"(r[6].x), "=f"(r[6].y), "=f"(r[7].x), "=f"(r[7].y)
+                 : "r"(taddr));
+}
+
+__device__ __forceinline__ void lds4(uint32_t addr, float2 &a, float2 &b)
+{
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(a.x), "=f"(a.y), "=f"(b.x), "=f"(b.y) : "r"(addr) : "memory");
+}
+
+// Waits until either barrier's phase is complete; true when the second's is and the first's is not.
+__device__ __forceinline__ bool mbar_wait_either(uint32_t a, uint32_t pa, uint32_t b, uint32_t pb)
+{
+    const uint64_t t0 = globaltimer();
+    for (uint32_t it = 1;; ++it) {
+        if (mbar_test_wait(a, pa)) return false;
+        if (mbar_test_wait(b, pb)) return true;
+        if ((it & 255u) == 0 && globaltimer() - t0 > 2000000000ull) return false; // the caller's own wait reports it
+    }
+}
+
+// A barrier between softmax warps, with the bound of every other wait.
+struct Meet {
+    uint32_t bar, phase;
+    __device__ __forceinline__ bool sync()
+    {
+        mbar_arrive(bar);
+        return wait();
+    }
+    __device__ __forceinline__ bool wait() // after the arrival
+    {
+        const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, phase));
+        phase ^= 1;
+        return ok;
+    }
+};
+
+// The kernel for blocks of RB query rows.
+template <int RB> struct Decode {
+
+static constexpr int kRB = RB, kKT = RB == 32 ? 128 : 64, kStages = RB == 32 ? 2 : 3;
+static constexpr bool kStacked = RB == 32; // hi and lo as rows of one operand
+// operand tiles of 128-byte rows, 128-byte swizzle: 64 rows of q and v, kKT keys
+static constexpr uint32_t kQSlice = 8192, kPTile = 8192, kSlice = kKT * 128, kStage = 5 * kSlice;
+static constexpr int kQSlices = kStacked ? 5 : 9;            // of q: 4 (hi and lo, or hi, then lo), and the rotated channels
+static constexpr uint32_t OFF_P = 0;                         // v: two buffers
+static constexpr uint32_t OFF_K = 2 * kPTile;                // stages of 5 slices: 4 of 128 latent channels, 1 of the rotated ones
+static constexpr uint32_t OFF_Q = OFF_K + kStages * kStage;
+static constexpr uint32_t OFF_SC = OFF_Q + kQSlices * kQSlice;
+static constexpr uint32_t OFF_XCH = OFF_SC + kStages * kKT * 4; // [2 buffers][4 key quarters][rows]
+static constexpr uint32_t OFF_BAR = OFF_XCH + 2 * 4 * kRB * 4;
+static constexpr uint32_t OFF_AT = OFF_BAR + 160; // where the CTA's walk begins (4 x int64)
+static constexpr uint32_t OFF_TMEM = OFF_AT + 32;
+static constexpr uint32_t SMEM_ALLOC = OFF_TMEM + 64 + 1024;
+static_assert(SMEM_ALLOC <= 232448, "shared memory per block");
+enum { B_KFULL = 0, B_KEMPTY = B_KFULL + kStages, B_S = B_KEMPTY + kStages, B_P = B_S + 2, B_Q = B_P + 2, B_ALL, B_ROWS, B_TAIL = B_ROWS + 2, B_FINAL, NUM_BARS };
+static_assert(8 * NUM_BARS <= 160, "barrier space");
+// TMEM columns: O (two N = 256 accumulators, 128 columns each), S_n and S_r (two buffers each)
+static constexpr uint32_t kSCols = kKT / 2, kColO = 0, kColSn = 256, kColSr = 256 + 2 * kSCols, kTmemCols = 512;
+static constexpr uint32_t IDESC_SN = (1u << 4) | ((uint32_t)(kKT >> 3) << 17) | (4u << 24); // M = 64, E4M3 x E4M3
+static constexpr uint32_t IDESC_SR = idesc_bf16_f32(64, kKT, false, false);
+static constexpr uint32_t IDESC_O = (1u << 4) | (1u << 16) | ((uint32_t)(256 >> 3) << 17) | (4u << 24); // M = 64, B MN-major
+static constexpr uint32_t IDESC_O_LO = IDESC_O | (kStacked ? 0u : 1u << 7);                             // lo in E5M2
+
+using Split = LatentSplit<kRB, kKT, 4>;
+using Walk = LatentWalk<Split>;
+
+struct Ctx {
+    uint32_t base, tmem;
+    __device__ __forceinline__ uint32_t bar(int b) const { return base + OFF_BAR + 8u * (uint32_t)b; }
+    __device__ __forceinline__ uint32_t stage(uint32_t n) const { return base + OFF_K + (n % kStages) * kStage; }
+};
+
 // Steps of 32 keys that O (+)= v code takes of tile t: up to the last key that is to be seen.  Rows behind it are not read
 // (a score that they gave is not used, whatever it is); of those before, the ones that are not there are zeros.
-__device__ __forceinline__ int output_steps(int64_t seen, int64_t t)
+static __device__ __forceinline__ int output_steps(int64_t seen, int64_t t)
 {
     const int64_t n = seen - t * kKT;
     return n >= kKT ? kKT / 32 : n <= 32 ? 1 : (int)(n + 31) / 32;
@@ -215,8 +303,23 @@ struct Boxes {
     __device__ __forceinline__ bool whole(int32_t row) const { return !__any_sync(0xffffffffu, lane < n && row < 0); }
 };
 
+static __device__ __forceinline__ bool any_row(const int64_t (&r)[kKT / 32])
+{
+    bool any = false;
+#pragma unroll
+    for (int k = 0; k < kKT / 32; ++k) any |= r[k] >= 0;
+    return any;
+}
+static __device__ __forceinline__ int64_t pick(const int64_t (&r)[kKT / 32], int k) // without an address
+{
+    int64_t v = r[0];
+#pragma unroll
+    for (int i = 1; i < kKT / 32; ++i) v = k == i ? r[i] : v;
+    return v;
+}
+
 // Keys by TMA (warp 8).
-__device__ __forceinline__ bool tma_role(const LatentDecodeArgs &a, const Maps &M, const Ctx &c, Walk walk, volatile uint32_t *issued, int lane)
+static __device__ __forceinline__ bool tma_role(const LatentDecodeArgs &a, const Maps &M, const Ctx &c, Walk walk, volatile uint32_t *issued, int lane)
 {
     LatentRun run;
     uint32_t n = 0, tails = 0; // tiles so far, those with rows that are not to be seen
@@ -225,33 +328,33 @@ __device__ __forceinline__ bool tma_role(const LatentDecodeArgs &a, const Maps &
     const bool paged = a.map.pages != nullptr;
     while (ok && walk.next(a, run)) {
         B.begin(run);
-        auto scales = [&](int64_t t, float (&s)[4]) { // contiguous: a tile ahead, in registers
+        auto scales = [&](int64_t t, float (&s)[kKT / 32]) { // contiguous: a tile ahead, in registers
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < kKT / 32; ++k) {
                 const int64_t r = B.base + t * kKT + 32 * k + lane;
                 s[k] = 0.f;
                 if (!paged && t < run.t1 && r >= 0 && r < a.rows.n) s[k] = __ldg(a.rows.scale + r);
             }
         };
         int32_t now = B.page(run.t0), next = B.page(run.t0 + 1);
-        float sc_next[4];
+        float sc_next[kKT / 32];
         scales(run.t0, sc_next);
         for (int64_t t = run.t0; t < run.t1; ++t, ++n) {
             const int32_t page = now, row = B.row(t, now);
             const bool whole = B.whole(row);
-            float sc_now[4];
+            float sc_now[kKT / 32];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) sc_now[k] = sc_next[k];
+            for (int k = 0; k < kKT / 32; ++k) sc_now[k] = sc_next[k];
             now = next;
             next = B.page(t + 2);
             scales(t + 1, sc_next);
-            int64_t tail_row[4];
-            uint32_t tail_scale[4];
+            int64_t tail_row[kKT / 32];
+            uint32_t tail_scale[kKT / 32];
             if (!whole) { // row by row
                 const int64_t n_seen = B.seen - t * kKT;
                 bool refused = false;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
+                for (int k = 0; k < kKT / 32; ++k) {
                     const int j = 32 * k + lane;
                     const int32_t p = __shfl_sync(0xffffffffu, page, j / M.box);
                     tail_row[k] = j < n_seen ? a.map.row(p, B.base, (uint32_t)(t * kKT + j)) : -1;
@@ -266,7 +369,7 @@ __device__ __forceinline__ bool tma_role(const LatentDecodeArgs &a, const Maps &
             }
             const uint32_t st = c.stage(n), full = c.bar(B_KFULL + n % kStages), sc = c.base + OFF_SC + (n % kStages) * kKT * 4;
             if (whole && paged) {
-                if (elect_one()) mbar_arrive_expect_tx(full, kKT * 644u);
+                if (elect_one()) mbar_arrive_expect_tx(full, (uint32_t)kKT * 644u);
                 for (int i = 0; i < B.n; ++i) {
                     const int32_t r = __shfl_sync(0xffffffffu, row, i);
                     if (elect_one()) {
@@ -277,19 +380,19 @@ __device__ __forceinline__ bool tma_role(const LatentDecodeArgs &a, const Maps &
                 }
             } else if (whole) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) sts1(sc + 4u * (uint32_t)(32 * k + lane), __float_as_uint(sc_now[k]));
+                for (int k = 0; k < kKT / 32; ++k) sts1(sc + 4u * (uint32_t)(32 * k + lane), __float_as_uint(sc_now[k]));
                 const int32_t r = __shfl_sync(0xffffffffu, row, 0);
                 if (elect_one()) {
-                    mbar_arrive_expect_tx(full, kKT * 640u);
+                    mbar_arrive_expect_tx(full, (uint32_t)kKT * 640u);
                     tma_load_3d(st, &M.lat, 0, r, 0, full);
                     tma_load_2d(st + 4 * kSlice, &M.rope, 0, r, full);
                 }
             } else {
                 // some rows are not to be seen, or not there: their places are zeroed once no box is on its way
-                const int64_t(&key_row)[4] = tail_row;
+                const int64_t(&key_row)[kKT / 32] = tail_row;
                 uint32_t bytes = 0;
-                if (!paged && __any_sync(0xffffffffu, key_row[0] >= 0 || key_row[1] >= 0 || key_row[2] >= 0 || key_row[3] >= 0)) {
-                    bytes = kKT * 640u; // the run may begin or end outside the cache: zeros
+                if (!paged && __any_sync(0xffffffffu, any_row(key_row))) {
+                    bytes = (uint32_t)kKT * 640u; // the run may begin or end outside the cache: zeros
                     if (elect_one()) {
                         tma_load_3d(st, &M.lat, 0, (int32_t)(B.base + t * kKT), 0, c.bar(B_TAIL));
                         tma_load_2d(st + 4 * kSlice, &M.rope, 0, (int32_t)(B.base + t * kKT), c.bar(B_TAIL));
@@ -297,7 +400,7 @@ __device__ __forceinline__ bool tma_role(const LatentDecodeArgs &a, const Maps &
                 }
                 for (int i = 0; paged && i < B.n; ++i) { // boxes whose first row is there; the rest of them may reach past the cache (zeros)
                     const int j = i * M.box, k = j >> 5;
-                    const int64_t r = __shfl_sync(0xffffffffu, k == 0 ? key_row[0] : k == 1 ? key_row[1] : k == 2 ? key_row[2] : key_row[3], j & 31);
+                    const int64_t r = __shfl_sync(0xffffffffu, pick(key_row, k), j & 31);
                     if (r < 0) continue;
                     bytes += (uint32_t)M.box * 640u;
                     if (elect_one()) {
@@ -307,7 +410,7 @@ __device__ __forceinline__ bool tma_role(const LatentDecodeArgs &a, const Maps &
                 }
                 if (elect_one()) mbar_arrive_expect_tx(c.bar(B_TAIL), bytes);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) sts1(sc + 4u * (uint32_t)(32 * k + lane), tail_scale[k]);
+                for (int k = 0; k < kKT / 32; ++k) sts1(sc + 4u * (uint32_t)(32 * k + lane), tail_scale[k]);
                 if (!__all_sync(0xffffffffu, mbar_wait(c.bar(B_TAIL), tails & 1))) {
                     ok = false;
                     break;
@@ -317,7 +420,7 @@ __device__ __forceinline__ bool tma_role(const LatentDecodeArgs &a, const Maps &
                 const int steps = output_steps(B.seen, t);
 #pragma unroll 1
                 for (int k = 0; k < steps; ++k) {
-                    uint32_t bad = __ballot_sync(0xffffffffu, (k == 0 ? key_row[0] : k == 1 ? key_row[1] : k == 2 ? key_row[2] : key_row[3]) < 0);
+                    uint32_t bad = __ballot_sync(0xffffffffu, (pick(key_row, k)) < 0);
                     while (bad) { // a row at a time: 32 chunks of 16 bytes
                         const uint32_t j = (uint32_t)(32 * k + __ffs(bad) - 1), e = (uint32_t)lane;
                         bad &= bad - 1;
@@ -338,7 +441,7 @@ __device__ __forceinline__ bool tma_role(const LatentDecodeArgs &a, const Maps &
 // The next tile into L2 (warp 9): its stage is not free yet when this one's is, and the way from HBM is most of what a
 // load takes.  It follows the tiles that warp 8 has asked for, and nothing waits for it: what it is too late for it
 // leaves out.
-__device__ __forceinline__ void prefetch_role(const LatentDecodeArgs &a, const Maps &M, Walk walk, const volatile uint32_t *issued, int lane)
+static __device__ __forceinline__ void prefetch_role(const LatentDecodeArgs &a, const Maps &M, Walk walk, const volatile uint32_t *issued, int lane)
 {
     LatentRun run;
     uint32_t n = 0;
@@ -370,9 +473,10 @@ __device__ __forceinline__ void prefetch_role(const LatentDecodeArgs &a, const M
     }
 }
 
-// Keys by cp.async (warps 8-9): warp w copies rows 64 w .. 64 w + 63 of a tile, 8 lanes a row of 128 bytes.
-__device__ __forceinline__ bool copy_role(const LatentDecodeArgs &a, const Ctx &c, Walk walk, int warp, int lane)
+// Keys by cp.async (warps 8-9): each warp copies half the rows of a tile, 8 lanes a row of 128 bytes.
+static __device__ __forceinline__ bool copy_role(const LatentDecodeArgs &a, const Ctx &c, Walk walk, int warp, int lane)
 {
+    constexpr int kHalf = kKT / 2;
     LatentRun run;
     uint32_t n = 0;
     bool ok = true;
@@ -380,24 +484,29 @@ __device__ __forceinline__ bool copy_role(const LatentDecodeArgs &a, const Ctx &
         const int64_t seen = latent_visible(a, run.b, a.Lq - 1);
         const int64_t first = a.map.first(run.b);
         auto resolve = [&](int64_t t, int h) { // row of the key that this lane looks up
-            const int64_t s = t * kKT + 64 * warp + 32 * h + lane;
+            const int64_t s = t * kKT + kHalf * warp + 32 * h + lane;
             if (s >= seen) return (int64_t)-1;
             const int64_t row = a.map.row(a.map.page(run.b, (uint32_t)s), first, (uint32_t)s);
             if (row < 0) flag_error(a.err, CSA_DEVERR_INDEX);
             return row;
         };
-        int64_t mine[2] = {resolve(run.t0, 0), resolve(run.t0, 1)};
+        int64_t mine[kHalf / 32];
+        for (int h = 0; h < kHalf / 32; ++h) mine[h] = resolve(run.t0, h);
         for (int64_t t = run.t0; t < run.t1; ++t, ++n) {
-            const int64_t cur[2] = {mine[0], mine[1]};
-            if (t + 1 < run.t1) mine[0] = resolve(t + 1, 0), mine[1] = resolve(t + 1, 1);
+            int64_t cur[kHalf / 32];
+#pragma unroll
+            for (int h = 0; h < kHalf / 32; ++h) {
+                cur[h] = mine[h];
+                if (t + 1 < run.t1) mine[h] = resolve(t + 1, h);
+            }
             if (n >= kStages && !__all_sync(0xffffffffu, mbar_wait(c.bar(B_KEMPTY + n % kStages), ((n / kStages) & 1) ^ 1))) {
                 ok = false;
                 break;
             }
             const uint32_t st = c.stage(n);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int r = 64 * warp + 4 * i + (lane >> 3);
+            for (int i = 0; i < kHalf / 4; ++i) {
+                const int r = kHalf * warp + 4 * i + (lane >> 3);
                 const int64_t row = __shfl_sync(0xffffffffu, cur[i >> 3], 4 * (i & 7) + (lane >> 3));
                 const int64_t src = row < 0 ? 0 : row;
                 const uint32_t bytes = row < 0 ? 0u : 16u, dst = st + sw128((uint32_t)r, 16u * (uint32_t)(lane & 7));
@@ -407,9 +516,8 @@ __device__ __forceinline__ bool copy_role(const LatentDecodeArgs &a, const Ctx &
                 copy16(dst + 4 * kSlice, a.rows.rope + src * kRd + 8 * (lane & 7), bytes);
             }
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-            {
-                const uint32_t dst = c.base + OFF_SC + (n % kStages) * kKT * 4 + 4u * (uint32_t)(64 * warp + 32 * h + lane);
+            for (int h = 0; h < kHalf / 32; ++h) {
+                const uint32_t dst = c.base + OFF_SC + (n % kStages) * kKT * 4 + 4u * (uint32_t)(kHalf * warp + 32 * h + lane);
                 if (cur[h] < 0) sts1(dst, kNoKey);
                 else asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(a.rows.scale + cur[h]) : "memory");
             }
@@ -421,21 +529,10 @@ __device__ __forceinline__ bool copy_role(const LatentDecodeArgs &a, const Ctx &
     return ok;
 }
 
-// Waits until either barrier's phase is complete; true when the second's is and the first's is not.
-__device__ __forceinline__ bool mbar_wait_either(uint32_t a, uint32_t pa, uint32_t b, uint32_t pb)
-{
-    const uint64_t t0 = globaltimer();
-    for (uint32_t it = 1;; ++it) {
-        if (mbar_test_wait(a, pa)) return false;
-        if (mbar_test_wait(b, pb)) return true;
-        if ((it & 255u) == 0 && globaltimer() - t0 > 2000000000ull) return false; // the caller's own wait reports it
-    }
-}
-
 // MMA issue (one thread).  S of tile n goes before O of tile n - 1, so that the softmax of one runs beside
 // the MMAs of the other; at a run's first tile O of the run before goes first, since its output has to
 // be read before the new queries are there.
-__device__ __forceinline__ bool mma_role(const LatentDecodeArgs &a, const Maps &M, const Ctx &c, Walk walk)
+static __device__ __forceinline__ bool mma_role(const LatentDecodeArgs &a, const Maps &M, const Ctx &c, Walk walk)
 {
     LatentRun run;
     uint32_t n = 0, runs = 0;
@@ -446,12 +543,16 @@ __device__ __forceinline__ bool mma_role(const LatentDecodeArgs &a, const Maps &
     auto output = [&](uint32_t k, bool first, int steps) { // O (+)= v code of tile k
         if (!mbar_wait(c.bar(B_P + (k & 1)), (k >> 1) & 1)) return false;
         tc_fence_after();
-        const Desc dp = p_desc.at(kPTile * (k & 1)), dv = v_desc.at((k % kStages) * 5 * kSlice);
+        const Desc dp = p_desc.at(kPTile * (k & 1)), dv = v_desc.at((k % kStages) * kStage);
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
+        for (int kk = 0; kk < kKT / 32; ++kk)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                if (kk < steps) mma_ws<true>(c.tmem + kColO + 128u * h, dp.at(32u * kk), dv.at(2u * h * M.slice + 4u * kk * M.group), IDESC_O, !first || kk > 0);
+                if (kk < steps) {
+                    const Desc b = dv.at(2u * h * M.slice + 4u * kk * M.group);
+                    mma_ws<true>(c.tmem + kColO + 128u * h, dp.at(32u * kk), b, IDESC_O, !first || kk > 0);
+                    if constexpr (!kStacked) mma_ws<true>(c.tmem + kColO + 128u * h, dp.at(64u + 32u * kk), b, IDESC_O_LO, 1);
+                }
         mma_commit(c.bar(B_KEMPTY + k % kStages));
         return true;
     };
@@ -474,16 +575,16 @@ __device__ __forceinline__ bool mma_role(const LatentDecodeArgs &a, const Maps &
             if (!mbar_wait(full, full_ph)) return false;
             fence_proxy_async_smem(); // cp.async writes for the generic proxy
             tc_fence_after();
-            const Desc dk = k_desc.at((n % kStages) * 5 * kSlice), dr = r_desc.at((n % kStages) * 5 * kSlice + 4 * kSlice);
-            const uint32_t buf = 64u * (n & 1);
+            const Desc dk = k_desc.at((n % kStages) * kStage), dr = r_desc.at((n % kStages) * kStage + 4 * kSlice);
+            const uint32_t buf = kSCols * (n & 1);
 #pragma unroll
-            for (int s = 0; s < 4; ++s)
+            for (int s = 0; s < kQSlices - 1; ++s)
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    mma_ws<true>(c.tmem + kColSn + buf, q_desc.at(s * kQSlice + 32u * kk), dk.at(s * M.slice + 32u * kk), IDESC_SN, (s | kk) != 0);
+                    mma_ws<true>(c.tmem + kColSn + buf, q_desc.at(s * kQSlice + 32u * kk), dk.at((s & 3) * M.slice + 32u * kk), IDESC_SN, (s | kk) != 0);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-                mma_ws<false>(c.tmem + kColSr + buf, q_desc.at(4 * kQSlice + 32u * kk), dr.at(32u * kk), IDESC_SR, kk != 0);
+                mma_ws<false>(c.tmem + kColSr + buf, q_desc.at((kQSlices - 1) * kQSlice + 32u * kk), dr.at(32u * kk), IDESC_SR, kk != 0);
             mma_commit(c.bar(B_S + (n & 1)));
             if (pending && !output(n - 1, pending_first, pending_steps)) return false;
             pending = true;
@@ -494,33 +595,17 @@ __device__ __forceinline__ bool mma_role(const LatentDecodeArgs &a, const Maps &
     return !pending || output(n - 1, pending_first, pending_steps);
 }
 
-// A barrier between softmax warps, with the bound of every other wait.
-struct Meet {
-    uint32_t bar, phase;
-    __device__ __forceinline__ bool sync()
-    {
-        mbar_arrive(bar);
-        return wait();
-    }
-    __device__ __forceinline__ bool wait() // after the arrival
-    {
-        const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, phase));
-        phase ^= 1;
-        return ok;
-    }
-};
-
-// A warp's 4 rows of a run's queries, on their way from memory.
+// 4 rows of a run's queries (of the kRB / 8 that a warp has), on their way from memory.
 struct Queries {
     uint4 u[4][2];
     uint32_t w[4];
-    __device__ __forceinline__ void fetch(const LatentDecodeArgs &a, const LatentRun &run, int warp, int lane)
+    __device__ __forceinline__ void fetch(const LatentDecodeArgs &a, const LatentRun &run, int row0, int lane)
     {
         const int n_rows = min(kRB, a.Lq * a.H - run.rb * kRB);
         const uint16_t *q = a.q + (run.b * a.Lq * a.H + run.rb * kRB) * (int64_t)(kR + kRd);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int r = 4 * warp + i;
+            const int r = row0 + i;
             u[i][0] = u[i][1] = make_uint4(0, 0, 0, 0);
             w[i] = 0;
             if (r < n_rows) {
@@ -533,14 +618,13 @@ struct Queries {
     }
 };
 
-// Into shared memory, as hi and lo; *factor takes a score of this lane's row to the log2 domain.  (Rows one after
+// Into shared memory, as hi and lo, with the factor that takes a row's scores to the log2 domain.  (Rows one after
 // another: code that runs once a run comes from far away, and its length is what it costs.)
-__device__ __forceinline__ bool store_queries(const LatentDecodeArgs &a, const Ctx &c, Queries &in, int warp, int lane, Meet &all,
-                                              float *factor)
+static __device__ __forceinline__ void store_queries(const LatentDecodeArgs &a, const Ctx &c, Queries &in, int row0, int lane)
 {
 #pragma unroll 1
     for (int i = 0; i < 4; ++i) {
-        const int r = 4 * warp + i;
+        const int r = row0 + i;
         float2 x[8];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -566,78 +650,38 @@ __device__ __forceinline__ bool store_queries(const LatentDecodeArgs &a, const C
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e].x *= up, x[e].y *= up;
         uint32_t hi[4], lo[4];
-        split16(x, 1.f, hi, lo);
+        split16<false>(x, 1.f, hi, lo);
         // lane holds channels 16 lane .. 16 lane + 15: byte 16 (lane & 7) of slice lane / 8
-        const uint32_t row = 32u * (uint32_t)(r >> 4) + (uint32_t)(r & 15), q = c.base + OFF_Q, at = q + (uint32_t)(lane >> 3) * kQSlice;
+        const uint32_t row = kStacked ? 32u * (uint32_t)(r >> 4) + (uint32_t)(r & 15) : (uint32_t)r, q = c.base + OFF_Q, at = q + (uint32_t)(lane >> 3) * kQSlice;
         sts4(at + sw128(row, 16u * (uint32_t)(lane & 7)), hi);
-        sts4(at + sw128(row + 16, 16u * (uint32_t)(lane & 7)), lo);
-        sts1(q + 4 * kQSlice + sw128(row, 4u * (uint32_t)lane), uint32_t(f32_to_bf16_bits(rx * up)) | (uint32_t(f32_to_bf16_bits(ry * up)) << 16));
-        sts1(q + 4 * kQSlice + sw128(row + 16, 4u * (uint32_t)lane), 0);
+        sts4(at + (kStacked ? sw128(row + 16, 16u * (uint32_t)(lane & 7)) : 4 * kQSlice + sw128(row, 16u * (uint32_t)(lane & 7))), lo);
+        const uint32_t rot = q + (kQSlices - 1) * kQSlice;
+        sts1(rot + sw128(row, 4u * (uint32_t)lane), uint32_t(f32_to_bf16_bits(rx * up)) | (uint32_t(f32_to_bf16_bits(ry * up)) << 16));
+        if constexpr (kStacked) sts1(rot + sw128(row + 16, 4u * (uint32_t)lane), 0);
         // a row that is not finite makes NaN of its scores
         const float f = finite ? a.scale * kLog2e * exp2i(-k) : NAN;
         if (lane == 0) sts1(c.base + OFF_XCH + 4u * (uint32_t)r, __float_as_uint(f));
 #pragma unroll
         for (int n = 0; n < 3; ++n) in.u[n][0] = in.u[n + 1][0], in.u[n][1] = in.u[n + 1][1], in.w[n] = in.w[n + 1];
     }
-    fence_proxy_async_smem();
-    if (!all.sync()) return false;
-    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(*factor) : "r"(c.base + OFF_XCH + 4u * (uint32_t)(16 * (warp & 1) + (lane & 15))) : "memory");
-    return all.sync(); // the factors are read before the place is used again
 }
 
-__device__ __forceinline__ float2 mul2(float2 a, float2 b)
-{
-    float2 d;
-    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
-        "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return d;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b)
-{
-    float2 d;
-    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
-        "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return d;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
-{
-    float2 d;
-    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
-        "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return d;
-}
-__device__ __forceinline__ void tmem_ld32_pairs(uint32_t taddr, float2 (&r)[16])
-{
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-                 : "=f"(r[0].x), "=f"(r[0].y), "=f"(r[1].x), "=f"(r[1].y), "=f"(r[2].x), "=f"(r[2].y), "=f"(r[3].x), "=f"(r[3].y),
-                   "=f"(r[4].x), "=f"(r[4].y), "=f"(r[5].x), "=f"(r[5].y), "=f"(r[6].x), "=f"(r[6].y), "=f"(r[7].x), "=f"(r[7].y),
-                   "=f"(r[8].x), "=f"(r[8].y), "=f"(r[9].x), "=f"(r[9].y), "=f"(r[10].x), "=f"(r[10].y), "=f"(r[11].x), "=f"(r[11].y),
-                   "=f"(r[12].x), "=f"(r[12].y), "=f"(r[13].x), "=f"(r[13].y), "=f"(r[14].x), "=f"(r[14].y), "=f"(r[15].x), "=f"(r[15].y)
-                 : "r"(taddr));
-}
-
-// Softmax and output (warps 0-7).  Warp w has rows 16 g .. 16 g + 15 (g = w & 1) and quarter kq of a tile's 128
-// keys; its lanes l and l + 16 hold the hi and lo parts of row 16 g + (l & 15) for the 32 keys, and after an
-// exchange the whole scores of 16 keys each.  Warps w and w + 4 reach the same lanes of TMEM, and take one of
-// O's two accumulators each.
-__device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, const Ctx &c, Walk walk, int warp, int lane)
+// Softmax and output (warps 0-7).  The rows lie in two halves g, and of a tile's keys a warp has quarter kq.  Warps w and
+// w + 4 reach the same lanes of TMEM, and take one of O's two accumulators each.
+//   Stacked: lanes l and l + 16 hold the hi and lo parts of row 16 g + (l & 15) for the quarter's 32 keys, and after
+//   an exchange the whole scores of 16 keys each.
+//   Otherwise lane l holds the scores of row 32 g + l for the quarter's 16 keys.
+static __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, const Ctx &c, Walk walk, int warp, int lane)
 {
     const int g = warp & 1, half = (warp >> 1) & 1, sub = warp >> 2, kq = 2 * half + sub;
-    const int part = lane >> 4, r16 = lane & 15, row = 16 * g + r16, key = 32 * kq + 16 * part;
+    const int part = kStacked ? lane >> 4 : 0, r16 = lane & 15, row = kStacked ? 16 * g + r16 : 32 * g + lane;
+    const int key = kStacked ? 32 * kq + 16 * part : 16 * kq;
     const uint32_t tw = c.tmem + ((uint32_t)(32 * (warp & 3)) << 16), tO = tw + kColO + 128u * (uint32_t)sub;
     Meet all{c.bar(B_ALL), 0}, rows{c.bar(B_ROWS + g), 0}; // the eight warps; those that share the rows
     // one value of the row from each quarter of the keys, in the quarters' order, so that all reduce them alike
     const uint32_t xch = c.base + OFF_XCH + 4u * (uint32_t)row;
     auto put_part = [&](uint32_t buf, float v) {
-        if (part == 0) asm volatile("st.shared.f32 [%0], %1;" ::"r"(xch + 512u * buf + 128u * (uint32_t)kq), "f"(v) : "memory");
+        if (part == 0) asm volatile("st.shared.f32 [%0], %1;" ::"r"(xch + 16u * kRB * buf + 4u * kRB * (uint32_t)kq), "f"(v) : "memory");
         mbar_arrive(rows.bar);
     };
     auto put = [&](uint32_t buf, float v) {
@@ -646,13 +690,20 @@ __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, const Ct
     };
     auto get = [&](uint32_t buf, float (&v)[4]) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[i]) : "r"(xch + 512u * buf + 128u * i) : "memory");
+        for (int i = 0; i < 4; ++i) asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[i]) : "r"(xch + 16u * kRB * buf + 4u * kRB * i) : "memory");
     };
     auto max4 = [](const float (&v)[4]) { return fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])); };
     auto sum4 = [](const float (&v)[4]) { return (v[0] + v[1]) + (v[2] + v[3]); };
     auto other_part = [](float v) { return __shfl_xor_sync(0xffffffffu, v, 16); };
+    auto row_max = [&](float v) { // over the lanes that share the row
+        if constexpr (kStacked) v = fmaxf(v, other_part(v));
+        return v;
+    };
+    auto row_sum = [&](float v) {
+        if constexpr (kStacked) v += other_part(v);
+        return v;
+    };
     LatentRun run, next_run;
-    Queries queries;
     uint32_t n = 0;
     float cq = 0.f, ref = 0.f, l = 0.f; // factor; reference and sum of p over this thread's keys
     // the run's last O, and the row's sum over the eight threads that share it
@@ -663,36 +714,44 @@ __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, const Ct
         // the run's last O, and the row's sum over the eight warps
         if (!__all_sync(0xffffffffu, mbar_wait(c.bar(B_KEMPTY + n % kStages), (n / kStages) & 1))) return false;
         tc_fence_after();
-        if (!rows.sync() || !put(0, l + other_part(l))) return false;
+        if (!rows.sync() || !put(0, row_sum(l))) return false;
         get(0, other);
         l = sum4(other);
         const int64_t out_row = run.b * n_rows + rr;
         const float inv = l != 0.f ? 1.f / l : 0.f;
         float *rec = a.part + ((2 * (int64_t)blockIdx.x + run.first) * kRB + row) * (kR + 4);
+        auto put_out = [&](const auto &x, int ch) { // consecutive channels of the row
+            constexpr int n = sizeof(x) / 4;
+            if (run.whole) {
+#pragma unroll
+                for (int e = 0; e < n; e += 8) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        w[u] = uint32_t(f32_to_bf16_bits(x[e + 2 * u] * inv)) | (uint32_t(f32_to_bf16_bits(x[e + 2 * u + 1] * inv)) << 16);
+                    *reinterpret_cast<uint4 *>(a.o + out_row * kR + ch + e) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < n; e += 4)
+                    *reinterpret_cast<float4 *>(rec + 4 + ch + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+            }
+        };
 #pragma unroll 1
         for (int k = 0; k < 4; ++k) {
             uint32_t o[32];
             tmem_ld32(tO + 32u * k, o);
             tmem_ld_wait();
-            float x[16]; // hi + lo / 16 of channels 256 sub + 128 half + 32 k + 16 part + e
+            if constexpr (kStacked) { // hi + lo / 16 of channels 256 sub + 128 half + 32 k + 16 part + e
+                float x[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const float a0 = __uint_as_float(o[e]), a1 = __uint_as_float(o[16 + e]), got = other_part(part ? a0 : a1);
-                x[e] = part ? fmaf(a1, 1.f / 16.f, got) : fmaf(got, 1.f / 16.f, a0);
-            }
-            const int ch = 256 * sub + 128 * half + 32 * k + 16 * part;
-            if (valid && run.whole) {
-                uint32_t w[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    w[e] = uint32_t(f32_to_bf16_bits(x[2 * e] * inv)) | (uint32_t(f32_to_bf16_bits(x[2 * e + 1] * inv)) << 16);
-                uint4 *d = reinterpret_cast<uint4 *>(a.o + out_row * kR + ch);
-                d[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                d[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                for (int e = 0; e < 16; ++e) {
+                    const float a0 = __uint_as_float(o[e]), a1 = __uint_as_float(o[16 + e]), got = other_part(part ? a0 : a1);
+                    x[e] = part ? fmaf(a1, 1.f / 16.f, got) : fmaf(got, 1.f / 16.f, a0);
+                }
+                if (valid) put_out(x, 256 * sub + 128 * half + 32 * k + 16 * part);
             } else if (valid) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    *reinterpret_cast<float4 *>(rec + 4 + ch + 4 * e) = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+                put_out(*reinterpret_cast<float(*)[32]>(o), 256 * sub + 128 * half + 32 * k);
             }
         }
         if (valid && kq == 0 && part == 0) {
@@ -712,9 +771,17 @@ __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, const Ct
         const bool more = walk.next(a, next_run);
         float cq_next = 0.f;
         if (more) {
-            queries.fetch(a, next_run, warp, lane);
-            if (!all.sync()) return false; // the last exchange has been read
-            if (!store_queries(a, c, queries, warp, lane, all, &cq_next)) return false;
+            if (have && !all.sync()) return false; // the last exchange has been read
+#pragma unroll 1
+            for (int r = 0; r < kRB / 8; r += 4) {
+                Queries queries;
+                queries.fetch(a, next_run, kRB / 8 * warp + r, lane);
+                store_queries(a, c, queries, kRB / 8 * warp + r, lane);
+            }
+            fence_proxy_async_smem();
+            if (!all.sync()) return false;
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(cq_next) : "r"(c.base + OFF_XCH + 4u * (uint32_t)row) : "memory");
+            if (!all.sync()) return false; // the factors are read before the place is used again
             mbar_arrive(c.bar(B_Q));
         }
         if (have && !output(n - 1)) return false;
@@ -735,15 +802,12 @@ __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, const Ct
             if (!__all_sync(0xffffffffu, mbar_wait(c.bar(B_KFULL + n % kStages), (n / kStages) & 1))) return false;
             float2 z[8], s[8], v[8];
             bool odd = (t + 1) * kKT > seen_least; // some key may not be seen by some row
-            {
+            const uint32_t sc = c.base + OFF_SC + (n % kStages) * kKT * 4 + (kStacked ? 128u : 64u) * (uint32_t)kq;
+            const uint32_t tS = tw + kSCols * buf + kSCols / 2 * (uint32_t)sub;
+            if constexpr (kStacked) {
                 float2 sn[16], sr[16], sk[16];
-                const uint32_t sc = c.base + OFF_SC + (n % kStages) * kKT * 4 + 128u * (uint32_t)kq;
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                                 : "=f"(sk[2 * e].x), "=f"(sk[2 * e].y), "=f"(sk[2 * e + 1].x), "=f"(sk[2 * e + 1].y)
-                                 : "r"(sc + 16u * e)
-                                 : "memory");
+                for (int e = 0; e < 8; ++e) lds4(sc + 16u * e, sk[2 * e], sk[2 * e + 1]);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     s[e] = part ? sk[8 + e] : sk[e];
@@ -751,8 +815,8 @@ __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, const Ct
                 }
                 if (!__all_sync(0xffffffffu, mbar_wait(c.bar(B_S + buf), (n >> 1) & 1))) return false;
                 tc_fence_after();
-                tmem_ld32_pairs(tw + kColSn + 64u * buf + 32u * (uint32_t)sub, sn);
-                tmem_ld32_pairs(tw + kColSr + 64u * buf + 32u * (uint32_t)sub, sr);
+                tmem_ld32_pairs(tS + kColSn, sn);
+                tmem_ld32_pairs(tS + kColSr, sr);
                 tmem_ld_wait();
 #pragma unroll
                 for (int e = 0; e < 16; ++e) sn[e] = fma2(sn[e], sk[e], sr[e]);
@@ -762,6 +826,19 @@ __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, const Ct
                     const float2 send = part ? sn[e] : sn[8 + e], keep = part ? sn[8 + e] : sn[e];
                     z[e] = add2(keep, make_float2(other_part(send.x), other_part(send.y)));
                 }
+            } else {
+                float2 sn[8];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) lds4(sc + 16u * e, s[2 * e], s[2 * e + 1]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) odd |= __float_as_uint(s[e].x) == kNoKey || __float_as_uint(s[e].y) == kNoKey;
+                if (!__all_sync(0xffffffffu, mbar_wait(c.bar(B_S + buf), (n >> 1) & 1))) return false;
+                tc_fence_after();
+                tmem_ld16_pairs(tS + kColSn, sn);
+                tmem_ld16_pairs(tS + kColSr, z);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 8; ++e) z[e] = fma2(sn[e], s[e], z[e]);
             }
             uint32_t open = 0xffffu; // bit e: key e is seen
             if (odd) {
@@ -809,7 +886,7 @@ __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, const Ct
                     if (open >> (2 * e) & 1u) zt = fmaxf(zt, fmaf(z[e].x, cq, __log2f(fmaxf(s[e].x, kSmallestScale))));
                     if (open >> (2 * e) & 2u) zt = fmaxf(zt, fmaf(z[e].y, cq, __log2f(fmaxf(s[e].y, kSmallestScale))));
                 }
-                return fmaxf(zt, other_part(zt));
+                return row_max(zt);
             };
             // weigh with the reference as it is, and again if that turns out to move; a run's first tile sets it first
             uint32_t hi[4], lo[4];
@@ -819,8 +896,8 @@ __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, const Ct
                 weigh();
                 // a row without a reference, or whose p leave fp32 (scales far below those that it was set by), takes one
                 top = begun && !(pt > 1e37f) ? top : INFINITY;
-                put_part(buf, fmaxf(top, other_part(top)));
-                split16(v, 16.f, hi, lo); // while the others arrive; seldom in vain
+                put_part(buf, row_max(top));
+                split16<!kStacked>(v, kStacked ? 16.f : 1.f, hi, lo); // while the others arrive; seldom in vain
                 if (!rows.wait()) return false;
                 get(buf, other);
                 row_top = max4(other);
@@ -834,7 +911,7 @@ __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, const Ct
                 const float zt = max4(other);
                 bool move = raise;
                 if (t > run.t0) { // low: what is still to come against what is summed
-                    if (!put(buf, vs + other_part(vs))) return false;
+                    if (!put(buf, row_sum(vs))) return false;
                     get(buf, other);
                     const float left = (float)(run.t1 - t) * kKT;
                     move = raise || (row_top < kLow && row_top > 1e-30f && left * row_top > sum4(other) * (1.f / 256.f));
@@ -863,13 +940,18 @@ __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, const Ct
                     tmem_st_wait();
                 }
                 weigh();
-                split16(v, 16.f, hi, lo);
+                split16<!kStacked>(v, kStacked ? 16.f : 1.f, hi, lo);
             }
             l += pt;
             vs += vt;
             const uint32_t at = c.base + OFF_P + kPTile * buf;
-            sts4(at + sw128((uint32_t)(32 * g + r16), (uint32_t)key), hi);
-            sts4(at + sw128((uint32_t)(32 * g + 16 + r16), (uint32_t)key), lo);
+            if constexpr (kStacked) {
+                sts4(at + sw128((uint32_t)(32 * g + r16), (uint32_t)key), hi);
+                sts4(at + sw128((uint32_t)(32 * g + 16 + r16), (uint32_t)key), lo);
+            } else {
+                sts4(at + sw128((uint32_t)row, (uint32_t)key), hi);
+                sts4(at + sw128((uint32_t)row, 64u + (uint32_t)key), lo);
+            }
             fence_proxy_async_smem();
             tc_fence_before();
             mbar_arrive(c.bar(B_P + buf));
@@ -878,9 +960,8 @@ __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, const Ct
     return true;
 }
 
-__global__ void __launch_bounds__(kThreads, 1) latent_decode_tc_kernel(LatentDecodeArgs a, const __grid_constant__ Maps maps)
+static __device__ __forceinline__ void run(const LatentDecodeArgs &a, const Maps &maps, uint8_t *smem_raw)
 {
-    extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
     uint8_t *sp = smem_raw + (base - raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -937,14 +1018,28 @@ __global__ void __launch_bounds__(kThreads, 1) latent_decode_tc_kernel(LatentDec
     if (warp == kMmaWarp) tmem_dealloc(c.tmem, kTmemCols);
 }
 
+};
+
+template <int RB> __global__ void __launch_bounds__(kThreads, 1) latent_decode_tc_kernel(LatentDecodeArgs a, const __grid_constant__ Maps maps)
+{
+    extern __shared__ uint8_t smem_raw[];
+    Decode<RB>::run(a, maps, smem_raw);
+}
+
 } // namespace
 
 bool latent_decode_tc_eligible(int R, int rd) { return R == kR && rd == kRd; }
 
+// Blocks of 32 rows where that is all there are, else of 64.  A tile of 128 keys takes 3,050 to 3,400 cycles for 32 rows
+// and, as two tiles of 64, TWO64 for 64.
+static bool one_block(int Lq, int H) { return Lq * H <= 32; }
+
+
 size_t latent_decode_tc_workspace(int64_t B, int Lq, int H, int64_t max_len, int *grid, int *par)
 {
-    Split::plan(B, Lq, H, max_len, device_sms(), grid, par);
-    return (size_t)*grid * 2 * kRB * (kR + 4) * sizeof(float);
+    if (one_block(Lq, H)) Decode<32>::Split::plan(B, Lq, H, max_len, device_sms(), grid, par);
+    else Decode<64>::Split::plan(B, Lq, H, max_len, device_sms(), grid, par);
+    return (size_t)*grid * 2 * (one_block(Lq, H) ? 32 : 64) * (kR + 4) * sizeof(float);
 }
 
 // Boxes with the 128-byte swizzle; what lies outside reads as zeros.
@@ -957,15 +1052,16 @@ static bool encode_u8(CUtensorMap *m, const void *base, int rank, const cuuint64
                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-cudaError_t launch_latent_decode_tc(const LatentDecodeArgs &a, cudaStream_t st)
+template <int RB> static cudaError_t launch(const LatentDecodeArgs &a, cudaStream_t st)
 {
+    constexpr int kKT = Decode<RB>::kKT;
     // a box is 128 rows of a contiguous run or of pages of whole tiles, or a page of 8, 16, 32 or 64 rows (in groups of 8,
     // as the swizzle has them); other pages are copied row by row: 3,700 cycles of issue a tile where a box takes one
     Maps maps{};
     const int pr = a.map.page_rows;
     const uint64_t n = (uint64_t)a.rows.n;
     maps.page_tiles = 1;
-    maps.slice = kSlice;
+    maps.slice = Decode<RB>::kSlice;
     maps.group = 1024;
     if (n >= 1 && n < (1ull << 31)) { // TMA coordinates are int32
         if (!a.map.pages) maps.box = kKT;
@@ -994,12 +1090,14 @@ cudaError_t launch_latent_decode_tc(const LatentDecodeArgs &a, cudaStream_t st)
         if (!ok || !encode_u8(&maps.rope, a.rows.rope, 2, dims, strides, box)) return cudaErrorNotSupported;
     }
     static std::atomic<bool> done[64];
-    cudaError_t e = prepare_kernel(latent_decode_tc_kernel, SMEM_ALLOC, kRegs, done);
+    cudaError_t e = prepare_kernel(latent_decode_tc_kernel<RB>, Decode<RB>::SMEM_ALLOC, kRegs, done);
     if (e != cudaSuccess) return e;
-    latent_decode_tc_kernel<<<(unsigned)a.grid, kThreads, SMEM_ALLOC, st>>>(a, maps);
+    latent_decode_tc_kernel<RB><<<(unsigned)a.grid, kThreads, Decode<RB>::SMEM_ALLOC, st>>>(a, maps);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_latent_merge_32x128(a, st);
+    return launch_latent_merge_tc(a, RB, st);
 }
+
+cudaError_t launch_latent_decode_tc(const LatentDecodeArgs &a, cudaStream_t st) { return one_block(a.Lq, a.H) ? launch<32>(a, st) : launch<64>(a, st); }
 
 } // namespace csa

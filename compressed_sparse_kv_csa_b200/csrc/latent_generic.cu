@@ -18,7 +18,8 @@ constexpr int kKT = 32;                    // keys of a tile
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 using Split = LatentSplit<kRB, kKT, 1>;
-using TcSplit = LatentSplit<32, 128, 2>; // of the tensor-core kernel
+using TcSplit32 = LatentSplit<32, 128, 4>; // of the tensor-core kernels
+using TcSplit64 = LatentSplit<64, 64, 4>;
 
 // One tile of up to 32 keys for one query row: q [dk] and kt [32, ldk] in shared memory, score of
 // key `lane` masked by `seen`, values vt[j * ldv + ch], ch < dv.
@@ -313,7 +314,10 @@ template <class Split, int RB> static cudaError_t launch_merge(const LatentDecod
     return cudaLaunchKernelEx(&cfg, latent_merge_kernel<Split, RB>, a);
 }
 
-cudaError_t launch_latent_merge_32x128(const LatentDecodeArgs &a, cudaStream_t st) { return launch_merge<TcSplit, 32>(a, st); }
+cudaError_t launch_latent_merge_tc(const LatentDecodeArgs &a, int rows, cudaStream_t st)
+{
+    return rows == 32 ? launch_merge<TcSplit32, 32>(a, st) : launch_merge<TcSplit64, 64>(a, st);
+}
 
 cudaError_t launch_latent_decode_generic(LatentDecodeArgs a, cudaStream_t st)
 {

@@ -65,12 +65,13 @@ def check_attention(o, lse, ref, dk, n_keys, p_step, name=""):
     and the output's rounding at the end.  `small` is not zero where the probabilities times the row
     scales, w, are held as 8-bit floats in two terms: with M their largest, the unit that they are
     held in is at most 2^-2.5 M (it is set so that the largest becomes 2^2.5 to 2^3.5, and only a larger one,
-    or one that would matter beside the sum, sets it again), and below 2^-6 units they are off by up to
-    2^-14 units, so each by at most 2^-16.5 M beyond p_step."""
+    or one that would matter beside the sum, sets it again), and below 2^-6 units, where the first term is
+    off by up to 2^-10, the second has 3 bits of that left: they are off by up to 2^-13 units, so each by
+    at most 2^-15.5 M beyond p_step."""
     ro, rl, size, mag, small = ref
     dz = (dk + 8) * 2.0 ** -24 * mag
     tau = 2 * dz + p_step + (n_keys + 8) * 2.0 ** -24 + 2.0 ** -20
-    tol = STEP[o.dtype] * ro.abs() + (tau[..., None] * size + 2.0 ** -16.5 * small) * 1.01 + 1e-30
+    tol = STEP[o.dtype] * ro.abs() + (tau[..., None] * size + 2.0 ** -15.5 * small) * 1.01 + 1e-30
     got = o.cpu().to(F64)
     assert torch.isfinite(got).all(), name
     bad = (got - ro).abs() > tol
