@@ -58,9 +58,14 @@ struct Desc {
     __device__ __forceinline__ Desc at(uint32_t bytes) const { return Desc(lo + (bytes >> 4), hi); }
 };
 
-template <bool F8> __device__ __forceinline__ void mma_ws(uint32_t d, Desc a, Desc b, uint32_t idesc, uint32_t accumulate)
+template <bool F8, bool WS = true> __device__ __forceinline__ void mma(uint32_t d, Desc a, Desc b, uint32_t idesc, uint32_t accumulate)
 {
-    if constexpr (F8)
+    if constexpr (F8 && !WS)
+        asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\t"
+                     "setp.ne.b32 p, %6, 0;\n\tmov.b64 x, {%1, %2};\n\tmov.b64 y, {%3, %4};\n\t"
+                     "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %5, p;\n\t}" ::"r"(d), "r"(a.lo), "r"(a.hi), "r"(b.lo), "r"(b.hi),
+                     "r"(idesc), "r"(accumulate));
+    else if constexpr (F8)
         asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\t"
                      "setp.ne.b32 p, %6, 0;\n\tmov.b64 x, {%1, %2};\n\tmov.b64 y, {%3, %4};\n\t"
                      "tcgen05.mma.ws.cta_group::1.kind::f8f6f4 [%0], x, y, %5, p;\n\t}" ::"r"(d), "r"(a.lo), "r"(a.hi), "r"(b.lo), "r"(b.hi),
@@ -223,12 +228,13 @@ template <int RB> struct Decode {
 static constexpr int kRB = RB, kKT = RB == 32 ? 128 : 64, kStages = RB == 32 ? 2 : 3;
 static constexpr bool kStacked = RB == 32; // hi and lo as rows of one operand
 // operand tiles of 128-byte rows, 128-byte swizzle: 64 rows of q and v, kKT keys
-static constexpr uint32_t kQSlice = 8192, kPTile = 8192, kSlice = kKT * 128, kStage = 5 * kSlice;
-static constexpr int kQSlices = kStacked ? 5 : 9;            // of q: 4 (hi and lo, or hi, then lo), and the rotated channels
-static constexpr uint32_t OFF_P = 0;                         // v: two buffers
-static constexpr uint32_t OFF_K = 2 * kPTile;                // stages of 5 slices: 4 of 128 latent channels, 1 of the rotated ones
+static constexpr uint32_t kQSlice = 2 * kRB * 128, kQRope = 4 * kQSlice, kPTile = 8192, kSlice = kKT * 128, kStage = 5 * kSlice;
+static constexpr uint32_t kPBufs = kStacked ? 2 : 1, kExch = kStacked ? 0 : 16384;
+static constexpr uint32_t OFF_P = 0;                         // v
+static constexpr uint32_t OFF_K = kPBufs * kPTile;           // stages of 5 slices: 4 of 128 latent channels, 1 of the rotated ones
 static constexpr uint32_t OFF_Q = OFF_K + kStages * kStage;
-static constexpr uint32_t OFF_SC = OFF_Q + kQSlices * kQSlice;
+static constexpr uint32_t OFF_EX = OFF_Q + kQRope + 8192;       // after q: 4 slices (hi and lo rows), the rotated channels
+static constexpr uint32_t OFF_SC = OFF_EX + kExch;              // parts of scores that change hands
 static constexpr uint32_t OFF_XCH = OFF_SC + kStages * kKT * 4; // [2 buffers][4 key quarters][rows]
 static constexpr uint32_t OFF_BAR = OFF_XCH + 2 * 4 * kRB * 4;
 static constexpr uint32_t OFF_AT = OFF_BAR + 160; // where the CTA's walk begins (4 x int64)
@@ -238,8 +244,8 @@ static_assert(SMEM_ALLOC <= 232448, "shared memory per block");
 enum { B_KFULL = 0, B_KEMPTY = B_KFULL + kStages, B_S = B_KEMPTY + kStages, B_P = B_S + 2, B_Q = B_P + 2, B_ALL, B_ROWS, B_TAIL = B_ROWS + 2, B_FINAL, NUM_BARS };
 static_assert(8 * NUM_BARS <= 160, "barrier space");
 // TMEM columns: O (two N = 256 accumulators, 128 columns each), S_n and S_r (two buffers each)
-static constexpr uint32_t kSCols = kKT / 2, kColO = 0, kColSn = 256, kColSr = 256 + 2 * kSCols, kTmemCols = 512;
-static constexpr uint32_t IDESC_SN = (1u << 4) | ((uint32_t)(kKT >> 3) << 17) | (4u << 24); // M = 64, E4M3 x E4M3
+static constexpr uint32_t kSrCols = kKT / 2, kColO = 0, kColSn = 256, kColSr = 384, kTmemCols = 512;
+static constexpr uint32_t IDESC_SN = (1u << 4) | ((uint32_t)(kKT >> 3) << 17) | ((uint32_t)(2 * kRB >> 4) << 24); // M = 2 RB, E4M3 x E4M3
 static constexpr uint32_t IDESC_SR = idesc_bf16_f32(64, kKT, false, false);
 static constexpr uint32_t IDESC_O = (1u << 4) | (1u << 16) | ((uint32_t)(256 >> 3) << 17) | (4u << 24); // M = 64, B MN-major
 static constexpr uint32_t IDESC_O_LO = IDESC_O | (kStacked ? 0u : 1u << 7);                             // lo in E5M2
@@ -543,15 +549,15 @@ static __device__ __forceinline__ bool mma_role(const LatentDecodeArgs &a, const
     auto output = [&](uint32_t k, bool first, int steps) { // O (+)= v code of tile k
         if (!mbar_wait(c.bar(B_P + (k & 1)), (k >> 1) & 1)) return false;
         tc_fence_after();
-        const Desc dp = p_desc.at(kPTile * (k & 1)), dv = v_desc.at((k % kStages) * kStage);
+        const Desc dp = p_desc.at(kPTile * (k % kPBufs)), dv = v_desc.at((k % kStages) * kStage);
 #pragma unroll
         for (int kk = 0; kk < kKT / 32; ++kk)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
                 if (kk < steps) {
                     const Desc b = dv.at(2u * h * M.slice + 4u * kk * M.group);
-                    mma_ws<true>(c.tmem + kColO + 128u * h, dp.at(32u * kk), b, IDESC_O, !first || kk > 0);
-                    if constexpr (!kStacked) mma_ws<true>(c.tmem + kColO + 128u * h, dp.at(64u + 32u * kk), b, IDESC_O_LO, 1);
+                    mma<true>(c.tmem + kColO + 128u * h, dp.at(32u * kk), b, IDESC_O, !first || kk > 0);
+                    if constexpr (!kStacked) mma<true>(c.tmem + kColO + 128u * h, dp.at(64u + 32u * kk), b, IDESC_O_LO, 1);
                 }
         mma_commit(c.bar(B_KEMPTY + k % kStages));
         return true;
@@ -576,15 +582,14 @@ static __device__ __forceinline__ bool mma_role(const LatentDecodeArgs &a, const
             fence_proxy_async_smem(); // cp.async writes for the generic proxy
             tc_fence_after();
             const Desc dk = k_desc.at((n % kStages) * kStage), dr = r_desc.at((n % kStages) * kStage + 4 * kSlice);
-            const uint32_t buf = kSCols * (n & 1);
 #pragma unroll
-            for (int s = 0; s < kQSlices - 1; ++s)
+            for (int s = 0; s < 4; ++s)
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    mma_ws<true>(c.tmem + kColSn + buf, q_desc.at(s * kQSlice + 32u * kk), dk.at((s & 3) * M.slice + 32u * kk), IDESC_SN, (s | kk) != 0);
+                    mma<true, kStacked>(c.tmem + kColSn + 64u * (n & 1), q_desc.at(s * kQSlice + 32u * kk), dk.at(s * M.slice + 32u * kk), IDESC_SN, (s | kk) != 0);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-                mma_ws<false>(c.tmem + kColSr + buf, q_desc.at((kQSlices - 1) * kQSlice + 32u * kk), dr.at(32u * kk), IDESC_SR, kk != 0);
+                mma<false>(c.tmem + kColSr + kSrCols * (n & 1), q_desc.at(kQRope + 32u * kk), dr.at(32u * kk), IDESC_SR, kk != 0);
             mma_commit(c.bar(B_S + (n & 1)));
             if (pending && !output(n - 1, pending_first, pending_steps)) return false;
             pending = true;
@@ -654,8 +659,8 @@ static __device__ __forceinline__ void store_queries(const LatentDecodeArgs &a, 
         // lane holds channels 16 lane .. 16 lane + 15: byte 16 (lane & 7) of slice lane / 8
         const uint32_t row = kStacked ? 32u * (uint32_t)(r >> 4) + (uint32_t)(r & 15) : (uint32_t)r, q = c.base + OFF_Q, at = q + (uint32_t)(lane >> 3) * kQSlice;
         sts4(at + sw128(row, 16u * (uint32_t)(lane & 7)), hi);
-        sts4(at + (kStacked ? sw128(row + 16, 16u * (uint32_t)(lane & 7)) : 4 * kQSlice + sw128(row, 16u * (uint32_t)(lane & 7))), lo);
-        const uint32_t rot = q + (kQSlices - 1) * kQSlice;
+        sts4(at + sw128(row + (kStacked ? 16 : 64), 16u * (uint32_t)(lane & 7)), lo);
+        const uint32_t rot = q + kQRope;
         sts1(rot + sw128(row, 4u * (uint32_t)lane), uint32_t(f32_to_bf16_bits(rx * up)) | (uint32_t(f32_to_bf16_bits(ry * up)) << 16));
         if constexpr (kStacked) sts1(rot + sw128(row + 16, 4u * (uint32_t)lane), 0);
         // a row that is not finite makes NaN of its scores
@@ -670,7 +675,8 @@ static __device__ __forceinline__ void store_queries(const LatentDecodeArgs &a, 
 // w + 4 reach the same lanes of TMEM, and take one of O's two accumulators each.
 //   Stacked: lanes l and l + 16 hold the hi and lo parts of row 16 g + (l & 15) for the quarter's 32 keys, and after
 //   an exchange the whole scores of 16 keys each.
-//   Otherwise lane l holds the scores of row 32 g + l for the quarter's 16 keys.
+//   Otherwise lane l has row 32 g + l, warps with half 0 its hi and with half 1 its lo part for all keys; they exchange what
+//   the other finishes, and hold the whole scores of the quarter's 16 keys.
 static __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, const Ctx &c, Walk walk, int warp, int lane)
 {
     const int g = warp & 1, half = (warp >> 1) & 1, sub = warp >> 2, kq = 2 * half + sub;
@@ -803,7 +809,6 @@ static __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, c
             float2 z[8], s[8], v[8];
             bool odd = (t + 1) * kKT > seen_least; // some key may not be seen by some row
             const uint32_t sc = c.base + OFF_SC + (n % kStages) * kKT * 4 + (kStacked ? 128u : 64u) * (uint32_t)kq;
-            const uint32_t tS = tw + kSCols * buf + kSCols / 2 * (uint32_t)sub;
             if constexpr (kStacked) {
                 float2 sn[16], sr[16], sk[16];
 #pragma unroll
@@ -815,8 +820,8 @@ static __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, c
                 }
                 if (!__all_sync(0xffffffffu, mbar_wait(c.bar(B_S + buf), (n >> 1) & 1))) return false;
                 tc_fence_after();
-                tmem_ld32_pairs(tS + kColSn, sn);
-                tmem_ld32_pairs(tS + kColSr, sr);
+                tmem_ld32_pairs(tw + kColSn + 64u * buf + 32u * (uint32_t)sub, sn);
+                tmem_ld32_pairs(tw + kColSr + kSrCols * buf + 32u * (uint32_t)sub, sr);
                 tmem_ld_wait();
 #pragma unroll
                 for (int e = 0; e < 16; ++e) sn[e] = fma2(sn[e], sk[e], sr[e]);
@@ -827,18 +832,29 @@ static __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, c
                     z[e] = add2(keep, make_float2(other_part(send.x), other_part(send.y)));
                 }
             } else {
-                float2 sn[8];
+                float2 sn[8], give[8];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) lds4(sc + 16u * e, s[2 * e], s[2 * e + 1]);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) odd |= __float_as_uint(s[e].x) == kNoKey || __float_as_uint(s[e].y) == kNoKey;
                 if (!__all_sync(0xffffffffu, mbar_wait(c.bar(B_S + buf), (n >> 1) & 1))) return false;
                 tc_fence_after();
-                tmem_ld16_pairs(tS + kColSn, sn);
-                tmem_ld16_pairs(tS + kColSr, z);
+                // this warp has hi or lo of all 64 keys, and gives the warp with the other part what that one has to finish
+                tmem_ld16_pairs(tw + kColSn + 64u * buf + 32u * (uint32_t)(half ^ 1) + 16u * (uint32_t)sub, give);
+                tmem_ld16_pairs(tw + kColSn + 64u * buf + 32u * (uint32_t)half + 16u * (uint32_t)sub, sn);
+                tmem_ld16_pairs(tw + kColSr + kSrCols * buf + 16u * (uint32_t)sub, z);
                 tmem_ld_wait();
+                const uint32_t ex = c.base + OFF_EX + 16u * (uint32_t)lane;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) z[e] = fma2(sn[e], s[e], z[e]);
+                for (int e = 0; e < 4; ++e)
+                    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(ex + 2048u * (uint32_t)(warp ^ 2) + 512u * e), "f"(give[2 * e].x),
+                                 "f"(give[2 * e].y), "f"(give[2 * e + 1].x), "f"(give[2 * e + 1].y)
+                                 : "memory");
+                if (!rows.sync()) return false;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) lds4(ex + 2048u * (uint32_t)warp + 512u * e, give[2 * e], give[2 * e + 1]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) z[e] = fma2(add2(sn[e], give[e]), s[e], z[e]);
             }
             uint32_t open = 0xffffu; // bit e: key e is seen
             if (odd) {
@@ -944,7 +960,10 @@ static __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, c
             }
             l += pt;
             vs += vt;
-            const uint32_t at = c.base + OFF_P + kPTile * buf;
+            const uint32_t at = c.base + OFF_P + kPTile * (n % kPBufs);
+            if constexpr (!kStacked) { // one buffer: O of the tile before has read it
+                if (n > 0 && !__all_sync(0xffffffffu, mbar_wait(c.bar(B_KEMPTY + (n - 1) % kStages), ((n - 1) / kStages) & 1))) return false;
+            }
             if constexpr (kStacked) {
                 sts4(at + sw128((uint32_t)(32 * g + r16), (uint32_t)key), hi);
                 sts4(at + sw128((uint32_t)(32 * g + 16 + r16), (uint32_t)key), lo);
