@@ -6,8 +6,8 @@
 // 8-bit terms whose products add up in the fp32 accumulators:
 //   q 2^k = hi + lo, both E4M3 (2^k brings the row's largest latent entry to [128, 256)): 8 bits of
 //     bf16 split into 4 + 4, exact down to 2^-10 of the largest entry, then off by at most 2^-18 of it;
-//   v = hi + lo / 16, both E4M3 (the two have accumulators of their own): off by at most 2^-8 relative
-//     for v >= 2^-6, as a bf16 probability is, and by 2^-14 absolute below.
+//   v = hi + lo, hi E4M3 and lo E5M2, or E4M3 of 16 times itself where the two have accumulators of their own: off by
+//     at most 2^-8 relative for v >= 2^-6, as a bf16 probability is, and by 2^-14 absolute below.
 // With s the scale of a key's row, S_n = sum_r (q 2^k)_r code_r and S_r = sum_r (q 2^k)_r rope_r,
 //   z = (S_n s + S_r) scale log2e 2^-k,  p = 2^(z - ref),  l = sum p,  v = p s,  O = sum v code
 // and o = O / l.  A row's ref is kept so that its v stay in E4M3's range: it is moved (and O and l
@@ -15,20 +15,27 @@
 // still to come could matter beside what has been summed: behind a key that outweighs all others the
 // reference comes down again, and the many small ones keep their 8 bits.
 //
-// A work item's rows are 32 (head, token) pairs.  All MMAs are weight-stationary (tcgen05.mma.ws), which spread
-// a small accumulator over all 128 lanes and are bound by what they read of shared memory, 128 bytes a cycle
-// (M = 64, N = 256 at 16 bits: 80 cycles, measured; without .ws 128).  Per tile of 128 keys
-//   S_n (M = 64: hi and lo rows of q, N = 128, K = 512, FP8), S_r (M = 64, N = 128, K = 64, BF16),
-//   O (+)= v code (M = 64: hi and lo rows of v; two N = 256, K = 128; the codes read MN-major): 28 MMAs, 1,600
-// cycles.  Rows 32 g + 16 part + r of an operand are part 0 (hi) and 1 (lo) of row 16 g + r, so the two parts of a
-// score lie in lanes l and l + 16 of one warp and meet by shuffle.  (Two passes with M = 32 need no shuffle, but
-// 680 more cycles of the chain below; measured 5,100 cycles a tile.)  One exchange a tile, of the rows' largest v,
-// lets the softmax warps decide alike whether a reference moves.
+// A work item's rows are RB = 32 or 64 (head, token) pairs.  The MMAs are bound by what they read of shared memory,
+// 128 bytes a cycle, behind 46 cycles each for the issue; those with M = 64 are weight-stationary (tcgen05.mma.ws),
+// which spread an accumulator over all 128 lanes (M = 64, N = 256 at 16 bits: 80 cycles, measured; without .ws 128).
+//   RB = 32, tiles of 128 keys, two stages of 80 KB: hi and lo are rows of one operand with M = 64.  S_n (N = 128,
+//     K = 512, FP8), S_r (N = 128, K = 64, BF16), O (+)= v code (two N = 256, K = 128; the codes read MN-major): 28
+//     MMAs, 1,600 cycles.  Rows 32 g + 16 part + r of an operand are part 0 (hi) and 1 (lo) of row 16 g + r, so the
+//     two parts of a score lie in lanes l and l + 16 of one warp and meet by shuffle.  (Two passes with M = 32 need
+//     no shuffle, but 680 more cycles of the chain below; measured 5,100 cycles a tile.)  3,050 to 3,400 cycles a
+//     tile, which is HBM's rate.
+//   RB = 64, tiles of 64 keys, three stages of 40 KB: S_n with M = 128, hi over lo, whose parts meet through shared
+//     memory (two passes with M = 64 read the keys twice: 1,650 cycles for S instead of 930, and as long a tile;
+//     4 x 1M keys x 64 rows in a loop of seconds 0.79 ms, so 0.77 ms); S_r with M = 64; O from hi, then from lo.
+//     2,300 cycles a tile: the chain load (2,000 cycles) - S (1,200) - softmax (1,700) - O (1,200) over the stages.
+//     At that rate the chip is at its power limit too (990 W, 1.5 GHz).
+// One exchange a tile, of the rows' largest v, lets the softmax warps decide alike whether a reference moves.
 //
-// Roles: warps 0-7 softmax and output; warp 8 copies the keys by TMA, in boxes of a page or of 128 rows, and
-// warp 9 brings the tile after into L2 (with pages that no box fits, both copy by cp.async); warp 10 MMA.  Two stages of 80 KB.  Rows that are not to
-// be seen are zeros in shared memory, or not read: the probability 0 times whatever they held would not be 0.
-// Bound by HBM for up to 32 query rows a key, by the chain load - S - softmax - O over two stages above.
+// Roles: warps 0-7 softmax and output; warp 8 copies the keys by TMA, in boxes of a page or of a tile, and warp 9
+// brings the tiles after into L2 (with pages that no box fits, both copy by cp.async); warp 10 MMA.  Rows that are
+// not to be seen are zeros in shared memory, or not read: the probability 0 times whatever they held would not be 0.
+// Measured: 64 sequences of 1k to 16k keys x 16 heads 63 us (4.4 TB/s), 32 of them x 128 heads x 2 tokens 183 us,
+// 4 x 1M keys x 64 heads 0.67 ms (4.0 TB/s).
 #include "latent.cuh"
 #include "tc_common.cuh"
 #include "tma_host.cuh"
@@ -346,7 +353,7 @@ static __device__ __forceinline__ bool tma_role(const LatentDecodeArgs &a, const
         float sc_next[kKT / 32];
         scales(run.t0, sc_next);
         for (int64_t t = run.t0; t < run.t1; ++t, ++n) {
-            const int32_t page = now, row = B.row(t, now);
+            const int32_t page = now, row = B.row(t, now), row0 = __shfl_sync(0xffffffffu, row, 0);
             const bool whole = B.whole(row);
             float sc_now[kKT / 32];
 #pragma unroll
@@ -374,7 +381,14 @@ static __device__ __forceinline__ bool tma_role(const LatentDecodeArgs &a, const
                 break;
             }
             const uint32_t st = c.stage(n), full = c.bar(B_KFULL + n % kStages), sc = c.base + OFF_SC + (n % kStages) * kKT * 4;
-            if (whole && paged) {
+            if (whole && paged && B.n == 1) {
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(full, (uint32_t)kKT * 644u);
+                    tma_load_4d(st, &M.lat, 0, 0, 0, row0 >> 3, full);
+                    tma_load_2d(st + 4 * kSlice, &M.rope, 0, row0, full);
+                    bulk_load(sc, a.rows.scale + row0, (uint32_t)kKT * 4u, full);
+                }
+            } else if (whole && paged) {
                 if (elect_one()) mbar_arrive_expect_tx(full, (uint32_t)kKT * 644u);
                 for (int i = 0; i < B.n; ++i) {
                     const int32_t r = __shfl_sync(0xffffffffu, row, i);
@@ -387,11 +401,10 @@ static __device__ __forceinline__ bool tma_role(const LatentDecodeArgs &a, const
             } else if (whole) {
 #pragma unroll
                 for (int k = 0; k < kKT / 32; ++k) sts1(sc + 4u * (uint32_t)(32 * k + lane), __float_as_uint(sc_now[k]));
-                const int32_t r = __shfl_sync(0xffffffffu, row, 0);
                 if (elect_one()) {
                     mbar_arrive_expect_tx(full, (uint32_t)kKT * 640u);
-                    tma_load_3d(st, &M.lat, 0, r, 0, full);
-                    tma_load_2d(st + 4 * kSlice, &M.rope, 0, r, full);
+                    tma_load_3d(st, &M.lat, 0, row0, 0, full);
+                    tma_load_2d(st + 4 * kSlice, &M.rope, 0, row0, full);
                 }
             } else {
                 // some rows are not to be seen, or not there: their places are zeroed once no box is on its way
@@ -444,28 +457,30 @@ static __device__ __forceinline__ bool tma_role(const LatentDecodeArgs &a, const
     return ok;
 }
 
-// The next tile into L2 (warp 9): its stage is not free yet when this one's is, and the way from HBM is most of what a
-// load takes.  It follows the tiles that warp 8 has asked for, and nothing waits for it: what it is too late for it
+// The next kAhead tiles into L2 (warp 9): their stages are not free yet, and the way from HBM is most of what a load
+// takes.  It follows the tiles that warp 8 has asked for, and nothing waits for it: what it is too late for it
 // leaves out.
+static constexpr int kAhead = kStages;
 static __device__ __forceinline__ void prefetch_role(const LatentDecodeArgs &a, const Maps &M, Walk walk, const volatile uint32_t *issued, int lane)
 {
     LatentRun run;
-    uint32_t n = 0;
+    uint32_t n = 0; // the run's first tile
     Boxes B(a, M, lane);
     while (walk.next(a, run)) {
         B.begin(run);
         int32_t next = B.page(run.t0 + 1);
-        for (int64_t t = run.t0; t < run.t1; ++t, ++n) {
-            const int32_t row = t + 1 < run.t1 ? B.row(t + 1, next) : -1;
-            next = B.page(t + 2);
+        for (int64_t t = run.t0 + 1; t < run.t1; ++t) {
+            const uint32_t k = n + (uint32_t)(t - run.t0); // this tile, counted as warp 8 counts
+            const int32_t row = B.row(t, next);
+            next = B.page(t + 1);
             uint32_t at = *issued;
             const uint64_t t0 = globaltimer();
-            while (at <= n) {
+            while (at + kAhead <= k && at <= k) { // (it ends at 2^32 - 1)
                 __nanosleep(100);
                 if (globaltimer() - t0 > 2000000000ull) return;
                 at = *issued;
             }
-            if (!__all_sync(0xffffffffu, at == n + 1) || !B.whole(row)) continue;
+            if (!__all_sync(0xffffffffu, at <= k) || !B.whole(row)) continue;
             if (lane < B.n) asm volatile("prefetch.global.L2 [%0];" ::"l"(a.rows.scale + row));
             for (int i = 0; i < B.n; ++i) {
                 const int32_t r = __shfl_sync(0xffffffffu, row, i);
@@ -476,6 +491,7 @@ static __device__ __forceinline__ void prefetch_role(const LatentDecodeArgs &a, 
                 }
             }
         }
+        n += (uint32_t)(run.t1 - run.t0);
     }
 }
 
@@ -1050,7 +1066,7 @@ template <int RB> __global__ void __launch_bounds__(kThreads, 1) latent_decode_t
 bool latent_decode_tc_eligible(int R, int rd) { return R == kR && rd == kRd; }
 
 // Blocks of 32 rows where that is all there are, else of 64.  A tile of 128 keys takes 3,050 to 3,400 cycles for 32 rows
-// and, as two tiles of 64, TWO64 for 64.
+// and, as two tiles of 64, 4,600 for 64.
 static bool one_block(int Lq, int H) { return Lq * H <= 32; }
 
 
