@@ -34,7 +34,7 @@
 // Roles: warps 0-7 softmax and output; warp 8 copies the keys by TMA, in boxes of a page or of a tile, and warp 9
 // brings the tiles after into L2 (with pages that no box fits, both copy by cp.async); warp 10 MMA.  Rows that are
 // not to be seen are zeros in shared memory, or not read: the probability 0 times whatever they held would not be 0.
-// Measured: 64 sequences of 1k to 16k keys x 16 heads 63 us (4.4 TB/s), 32 of them x 128 heads x 2 tokens 183 us,
+// Measured: 64 sequences of 1k to 16k keys x 16 heads 63 us (3.7 TB/s), 32 of them x 128 heads x 2 tokens 183 us,
 // 4 x 1M keys x 64 heads 0.67 ms (4.0 TB/s).
 #include "latent.cuh"
 #include "tc_common.cuh"
