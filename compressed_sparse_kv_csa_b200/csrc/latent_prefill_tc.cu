@@ -37,10 +37,11 @@ constexpr int kRegs = 168, kRegsSoft = 208, kRegsRest = 88;
 static_assert(256 * kRegsSoft + 128 * kRegsRest <= kThreads * kRegs, "register split");
 constexpr uint32_t kSlot = 16384;
 constexpr int kSlots = 8;
+constexpr int kParts = 2; // P is handed over in parts, so that P V begins while the rest is computed
 constexpr uint32_t OFF_Q = 0, OFF_RING = 2 * 3 * kSlot, OFF_BAR = OFF_RING + kSlots * kSlot, OFF_TMEM = OFF_BAR + 256;
 constexpr uint32_t SMEM_ALLOC = OFF_TMEM + 64 + 1024; // slack to align the base to 1024 bytes
 static_assert(SMEM_ALLOC <= 232448, "shared memory per block");
-enum { B_Q = 0, B_FULL, B_EMPTY = B_FULL + kSlots, B_S = B_EMPTY + kSlots, B_P = B_S + 2, B_O = B_P + 2, B_VTAIL = B_O + 2,
+enum { B_Q = 0, B_FULL, B_EMPTY = B_FULL + kSlots, B_S = B_EMPTY + kSlots, B_P = B_S + 2, B_O = B_P + 2 * kParts, B_VTAIL = B_O + 2,
        B_FINAL, NUM_BARS };
 static_assert(8 * NUM_BARS <= 256, "barrier space");
 constexpr uint32_t IDESC_S = idesc_bf16_f32(128, 128, false, false), IDESC_PV = idesc_bf16_f32(128, 128, false, true);
@@ -102,6 +103,22 @@ __device__ __forceinline__ uint32_t pk_bf16(float lo, float hi)
 {
     __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<uint32_t *>(&h);
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float y;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[32]) { tmem_st32(taddr, r); }
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
+                 "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+                 : "memory");
 }
 
 // Two fp32 operations in one instruction.
@@ -249,13 +266,16 @@ __device__ __forceinline__ bool mma_role(const Job &j, uint32_t base, uint32_t t
         const int lo = min(v.slot[0], v.slot[1]), hi = max(v.slot[0], v.slot[1]);
         for (int t = 0; t < 2; ++t) {
             if (i < j.n[t]) {
-                if (!mbar_wait(bar(B_P + t), ph)) return false;
-                tc_fence_after();
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
+                for (int kk = 0; kk < 8; ++kk) {
+                    if (kk % (8 / kParts) == 0) {
+                        if (!mbar_wait(bar(B_P + kParts * t + kk / (8 / kParts)), ph)) return false;
+                        tc_fence_after();
+                    }
                     mma_bf16_ts(tmem + kColO + 128u * t, tmem + kColS + 128u * t + 8u * kk,
                                 sdesc_sw128(base + OFF_RING + (uint32_t)lo * kSlot + 2048u * kk, (uint32_t)(hi - lo) * kSlot, 1024),
                                 IDESC_PV, (i | kk) != 0);
+                }
                 if (i + 1 == j.n[t]) mma_commit(bar(B_O + t));
             }
             if (t == 1) free_slots(2, v);
@@ -302,8 +322,12 @@ __device__ __forceinline__ bool softmax_role(const LatentPrefillArgs &a, const J
         }
         float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-        for (int e = 4; e < kT; ++e) mx[e & 3] = fmaxf(mx[e & 3], s[e]);
-        const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
+        for (int e = 4; e + 8 <= kT; e += 8)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) mx[u] = max3(mx[u], s[e + u], s[e + 4 + u]);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) mx[u] = fmaxf(mx[u], s[kT - 4 + u]);
+        const float mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * sl2;
         float f = 1.f;
         if (mt > m + 8.f || m == -INFINITY) {
             f = m == -INFINITY ? 0.f : ex2(m - mt); // O of a row that has seen nothing is 0 (or not yet written)
@@ -326,22 +350,23 @@ __device__ __forceinline__ bool softmax_role(const LatentPrefillArgs &a, const J
         const float2 sl2v = make_float2(sl2, sl2), subv = make_float2(sub, sub);
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-            uint32_t p[32];
+        for (int g = 0; g < kParts; ++g) {
+            uint32_t p[64 / kParts];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-                float2 z = fma2(make_float2(s[64 * g + 2 * e], s[64 * g + 2 * e + 1]), sl2v, subv);
+            for (int e = 0; e < 64 / kParts; ++e) {
+                const int k = kT / kParts * g + 2 * e;
+                float2 z = fma2(make_float2(s[k], s[k + 1]), sl2v, subv);
                 z.x = ex2(z.x);
                 z.y = ex2(z.y);
                 sum[e & 1] = add2(sum[e & 1], z);
                 p[e] = pk_bf16(z.x, z.y);
             }
-            tmem_st32(tS + 32u * g, p);
+            tmem_st(tS + (uint32_t)(64 / kParts) * g, p);
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(bar(B_P + kParts * t + g));
         }
         l = fmaf(l, f, (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y));
-        tmem_st_wait();
-        tc_fence_before();
-        mbar_arrive(bar(B_P + t));
     }
     if (j.n[t] > 0) {
         if (!__all_sync(0xffffffffu, mbar_wait(bar(B_O + t), 0))) return false;
@@ -384,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_tc_kernel(LatentPr
     uint8_t *sp = smem_raw + (base - raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
-        for (int b = 0; b < NUM_BARS; ++b) mbar_init(base + OFF_BAR + 8u * (uint32_t)b, b == B_P || b == B_P + 1 ? 128u : 1u);
+        for (int b = 0; b < NUM_BARS; ++b) mbar_init(base + OFF_BAR + 8u * (uint32_t)b, b >= B_P && b < B_O ? 128u : 1u);
         mbar_init_fence();
     }
     if (warp == kMmaWarp) tmem_alloc(base + OFF_TMEM, 512);
