@@ -78,7 +78,7 @@ struct LatentDecodeArgs {
     int64_t max_len;
     uint16_t *o; // [B, Lq, H, R] bf16
     float *lse;  // [B, Lq, H] or null
-    float *part; // partials: 2 slots per CTA of RB rows, R + 2 floats each
+    float *part; // partials: 2 slots per CTA (latent_part)
     int grid;    // CTAs of the split
     int par;     // CTAs side by side on the same keys, one for each row block; 1: a CTA's runs may be of any row block
     int *err;
@@ -90,6 +90,21 @@ __device__ __forceinline__ int64_t latent_visible(const LatentDecodeArgs &a, int
     int64_t p = a.pos[b];
     p = (p < a.max_len ? p : a.max_len) + j + 1;
     return p < 0 ? 0 : (p < a.max_len ? p : a.max_len);
+}
+
+// A partial: the rows' (maximum, sum), then their outputs, four channels of all rows beside one another, so that the lanes
+// of a warp write whole sectors where they hold rows, and read them where they hold four rows of eight such fours.
+template <int RB> __host__ __device__ __forceinline__ int64_t latent_part_size(int R) { return (int64_t)RB * (R + 4); } // floats
+template <int RB> __device__ __forceinline__ float *latent_part(const LatentDecodeArgs &a, int R, int64_t slot)
+{
+    return a.part + slot * latent_part_size<RB>(R);
+}
+template <int RB> __device__ __forceinline__ int latent_part_at(int row, int ch) { return 4 * RB + ((ch >> 2) * RB + row) * 4 + (ch & 3); }
+
+// x / y of numbers that are not negative, in 32 bits where they fit (a fifth of the time).
+__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y)
+{
+    return ((x | y) >> 32) == 0 ? (int64_t)((uint32_t)x / (uint32_t)y) : x / y;
 }
 
 // The split of a decode call: every (sequence, block of RB query rows) is a run of key tiles, and all runs lie one
@@ -112,14 +127,18 @@ template <int RB, int KT, int COST> struct LatentSplit {
         return t < 1 ? 1 : t;
     }
     static __host__ __device__ __forceinline__ int64_t row_blocks(int Lq, int H) { return ((int64_t)Lq * H + RB - 1) / RB; }
-    // Grid and par for at most `most` CTAs; side by side where that leaves at most a tenth of them idle.
+    // Grid and par for at most `most` CTAs; side by side where that leaves at most a tenth of them idle.  Of short work only as
+    // many CTAs as keep the largest share as it is: the SMs left over bring up the merge meanwhile, and it has fewer
+    // parts to read (1 x 32k keys x 16 heads: 31 us with 148 CTAs, 21 with 130).
     static void plan(int64_t B, int Lq, int H, int64_t max_len, int most, int *grid, int *par)
     {
         const int64_t nrb = row_blocks(Lq, H), t = (max_len + KT - 1) / KT, tiles = B * (t < 1 ? 1 : t); // a CTA for each tile at most
         const bool side = nrb <= most && most / nrb * nrb * 10 >= 9 * (int64_t)most;
         *par = side ? (int)nrb : 1;
-        const int64_t work = side ? tiles : tiles * nrb, groups = most / *par;
-        *grid = (int)((work < groups ? work : groups) * *par);
+        const int64_t runs = side ? B : B * nrb, work = side ? tiles : tiles * nrb, groups = most / *par;
+        const int64_t places = work + COST * runs, share = (places + groups - 1) / groups, few = share <= 8 ? (places + share - 1) / share : groups;
+        const int64_t n = work < few ? work : few;
+        *grid = (int)((n < groups ? n : groups) * *par);
     }
     static __device__ __forceinline__ int64_t length(const LatentDecodeArgs &a, int64_t b) { return tiles(a, b) + COST; }
     // Lengths of the runs of the sequences [b0, b1), one warp.
@@ -171,10 +190,10 @@ template <class Split> struct LatentWalk {
     static __device__ __forceinline__ void begin(const LatentDecodeArgs &a, int lane, int64_t (&out)[4])
     {
         const int64_t nrb = a.par > 1 ? 1 : Split::row_blocks(a.Lq, a.H), G = gridDim.x / a.par, i = blockIdx.x / a.par;
-        const int64_t T = Split::warp_total(a, 0, a.B, lane) * nrb, at = T * i / G;
+        const int64_t T = Split::warp_total(a, 0, a.B, lane) * nrb, at = quotient(T * i, G);
         int64_t b, before;
         Split::warp_find(a, at, nrb, lane, &b, &before);
-        if (lane == 0) out[0] = b, out[1] = before, out[2] = at, out[3] = T * (i + 1) / G;
+        if (lane == 0) out[0] = b, out[1] = before, out[2] = at, out[3] = quotient(T * (i + 1), G);
     }
     __device__ __forceinline__ LatentWalk(const LatentDecodeArgs &a, const int64_t (&from)[4])
     {
@@ -193,7 +212,7 @@ template <class Split> struct LatentWalk {
             r.b = b;
             r.rb = rb0;
             if (nrb > 1) {
-                r.rb = (int)(in / length);
+                r.rb = (int)quotient(in, length);
                 in -= r.rb * length;
             }
             const int64_t out = min(length, in + (end - at));

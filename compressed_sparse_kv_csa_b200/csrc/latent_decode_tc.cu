@@ -34,8 +34,8 @@
 // Roles: warps 0-7 softmax and output; warp 8 copies the keys by TMA, in boxes of a page or of a tile, and warp 9
 // brings the tiles after into L2 (with pages that no box fits, both copy by cp.async); warp 10 MMA.  Rows that are
 // not to be seen are zeros in shared memory, or not read: the probability 0 times whatever they held would not be 0.
-// Measured: 64 sequences of 1k to 16k keys x 16 heads 63 us (3.7 TB/s), 32 of them x 128 heads x 2 tokens 183 us,
-// 4 x 1M keys x 64 heads 0.67 ms (4.0 TB/s).
+// Measured: 64 sequences of 1k to 16k keys x 16 heads 63 us (3.7 TB/s), 32 of them x 128 heads x 2 tokens 175 us,
+// 4 x 1M keys x 64 heads 0.65 ms (4.1 TB/s).
 #include "latent.cuh"
 #include "tc_common.cuh"
 #include "tma_host.cuh"
@@ -741,7 +741,7 @@ static __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, c
         l = sum4(other);
         const int64_t out_row = run.b * n_rows + rr;
         const float inv = l != 0.f ? 1.f / l : 0.f;
-        float *rec = a.part + ((2 * (int64_t)blockIdx.x + run.first) * kRB + row) * (kR + 4);
+        float *rec = latent_part<kRB>(a, kR, 2 * (int64_t)blockIdx.x + run.first);
         auto put_out = [&](const auto &x, int ch) { // consecutive channels of the row
             constexpr int n = sizeof(x) / 4;
             if (run.whole) {
@@ -756,7 +756,7 @@ static __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, c
             } else {
 #pragma unroll
                 for (int e = 0; e < n; e += 4)
-                    *reinterpret_cast<float4 *>(rec + 4 + ch + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+                    *reinterpret_cast<float4 *>(rec + latent_part_at<kRB>(row, ch + e)) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
             }
         };
 #pragma unroll 1
@@ -780,8 +780,8 @@ static __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, c
             if (run.whole) {
                 if (a.lse) a.lse[out_row] = l != 0.f ? (ref + log2f(l)) * kLn2 : -INFINITY;
             } else {
-                rec[0] = l != 0.f ? ref : -INFINITY;
-                rec[1] = l;
+                rec[2 * row] = l != 0.f ? ref : -INFINITY;
+                rec[2 * row + 1] = l;
             }
         }
         tc_fence_before();
@@ -1074,7 +1074,7 @@ size_t latent_decode_tc_workspace(int64_t B, int Lq, int H, int64_t max_len, int
 {
     if (one_block(Lq, H)) Decode<32>::Split::plan(B, Lq, H, max_len, device_sms(), grid, par);
     else Decode<64>::Split::plan(B, Lq, H, max_len, device_sms(), grid, par);
-    return (size_t)*grid * 2 * (one_block(Lq, H) ? 32 : 64) * (kR + 4) * sizeof(float);
+    return (size_t)*grid * 2 * (one_block(Lq, H) ? latent_part_size<32>(kR) : latent_part_size<64>(kR)) * sizeof(float);
 }
 
 // Boxes with the 128-byte swizzle; what lies outside reads as zeros.

@@ -126,99 +126,141 @@ __global__ void __launch_bounds__(32 * kWarps) latent_decode_generic_kernel(Late
                     if (lane + 32 * i < R) a.o[row * R + lane + 32 * i] = f32_to_bf16_bits(acc[u][i] * inv);
                 if (a.lse && lane == 0) a.lse[row] = l[u] != 0.f ? (m[u] + log2f(l[u])) * kLn2 : -INFINITY;
             } else {
-                float *p = a.part + ((2 * (int64_t)blockIdx.x + first) * kRB + r) * (R + 4);
-                if (lane == 0) p[0] = m[u], p[1] = l[u];
+                float *p = latent_part<kRB>(a, R, 2 * (int64_t)blockIdx.x + first);
+                if (lane == 0) p[2 * r] = m[u], p[2 * r + 1] = l[u];
 #pragma unroll
                 for (int i = 0; i < kMaxNV; ++i)
-                    if (lane + 32 * i < R) p[4 + lane + 32 * i] = acc[u][i];
+                    if (lane + 32 * i < R) p[latent_part_at<kRB>(r, lane + 32 * i)] = acc[u][i];
             }
         }
     }
 }
 
-// Merge of the parts of a run that the split cut: one CTA per query row.  With part i holding the
-// maximum m_i (log2 domain), the sum l_i and the unnormalised output O_i, the run's are
-// m = max m_i, l = sum 2^(m_i - m) l_i, O = sum 2^(m_i - m) O_i; the output is O / l.
+// Merge of the parts of a run that the split cut.  With part i holding the maximum m_i (log2 domain), the sum l_i and the
+// unnormalised output O_i, the run's are m = max m_i, l = sum 2^(m_i - m) l_i, O = sum 2^(m_i - m) O_i; the output is
+// O / l.  Bound by latency, its own (where the run lies takes some 3 us to find) and that of its loads, of which a thread
+// has 8 under way.  Of many parts a CTA takes 4 rows and 128 channels, and up to 4 groups of 128 threads share the
+// parts (1 x 64k keys x 16 heads, 148 parts: 12 us behind the parts' kernel; one group 45).  Of few parts of many rows it
+// takes 16 rows and all channels, four rows a thread (32 x 256 rows in 2 or 3 parts: 16 us; 4 rows a CTA 33; but
+// 64 x 16 rows 13 us where 4 rows a CTA take 6).
 constexpr int kMaxParts = 512;
 
-template <class Split, int RB> __global__ void __launch_bounds__(128) latent_merge_kernel(LatentDecodeArgs a)
+template <class Split, int RB, int ROWS> __global__ void __launch_bounds__(512) latent_merge_kernel(LatentDecodeArgs a)
 {
+    constexpr int U = ROWS / 4, kLoads = 8 / U, kLanes = ROWS == 4 ? 128 : 512; // rows a thread, parts at a time, threads of a group
+    static_assert(RB % ROWS == 0, "a CTA's rows lie in one row block");
     __shared__ int64_t s_at[2];
-    __shared__ float red[4], weight[kMaxParts];
-    const int tid = threadIdx.x, lane = tid & 31;
-    const int64_t rows = (int64_t)a.Lq * a.H, b = blockIdx.x / rows;
-    const int r = (int)(blockIdx.x % rows), rb = r / RB;
+    __shared__ float red[2][16][ROWS];
+    extern __shared__ float4 merge_smem[]; // sums of the groups behind the first, weights and sums of the parts
+    const int tid = threadIdx.x, lane = tid & 31, warps = blockDim.x >> 5;
+    const int rows = a.Lq * a.H, blocks = (rows + ROWS - 1) / ROWS;
+    const int64_t b = blockIdx.x / blocks;
+    const int r0 = (int)(blockIdx.x % blocks) * ROWS, rb = r0 / RB;
     const int R = a.rows.c - a.rows.rope_dims;
     const int64_t nrb = a.par > 1 ? 1 : Split::row_blocks(a.Lq, a.H), G = a.grid / a.par;
+    float4 *sums = merge_smem;
+    float *weight = reinterpret_cast<float *>(sums + (blockDim.x - kLanes)), *part_sum = weight + ROWS * G;
     if (tid < 64) { // the length before this sequence (warp 0), from it on (warp 1)
         const int64_t s = tid < 32 ? Split::warp_total(a, 0, b, lane) : Split::warp_total(a, b, a.B, lane);
         if (lane == 0) s_at[tid >> 5] = s * nrb;
     }
+    const int64_t length = Split::length(a, b);
     __syncthreads();
-    const int64_t length = Split::length(a, b), T = s_at[0] + s_at[1], begin = s_at[0] + (a.par > 1 ? 0 : rb * length);
+    const int64_t T = s_at[0] + s_at[1], begin = s_at[0] + (a.par > 1 ? 0 : rb * length);
     const int64_t s0 = begin + Split::kCost, s1 = begin + length - 1; // the places of its first and last tile
     // the CTAs (or groups) that hold the run's first and last tile: the largest i with floor(i T / G) <= place
-    const int64_t i0 = ((s0 + 1) * G - 1) / T, i1 = ((s1 + 1) * G - 1) / T;
+    const int64_t i0 = quotient((s0 + 1) * G - 1, T), i1 = quotient((s1 + 1) * G - 1, T);
     // launched beside the kernel that writes the parts: every block waits for it, those with nothing to do too, since
     // what follows in the stream waits for this kernel alone
     cudaGridDependencySynchronize();
     if (i0 == i1) return; // finished by the CTA that holds it
-    const int64_t ld = R + 4;
     const int n = (int)(i1 - i0 + 1);
     // part k: slot 2 i + 1 where the run begins, slot 2 i behind; a CTA without tiles has none
-    const int64_t cta0 = i0 * a.par + (a.par > 1 ? rb : 0), step = 2 * (int64_t)a.par * RB * ld;
-    const float *first = a.part + ((2 * cta0 + 1) * RB + (r % RB)) * ld, *rest = a.part + (2 * cta0 * RB + (r % RB)) * ld;
+    const int64_t cta0 = i0 * a.par + (a.par > 1 ? rb : 0), step = 2 * a.par * latent_part_size<RB>(R);
+    const float *first = latent_part<RB>(a, R, 2 * cta0 + 1), *rest = latent_part<RB>(a, R, 2 * cta0);
     auto part = [&](int k) { return k == 0 ? first : rest + k * step; };
-    float m = -INFINITY, ml[kMaxParts / 128][2];
+    const int wr = tid % ROWS; // the row that this thread weighs parts of
+    auto over_threads = [&](float (&at)[16][ROWS], float v, auto op) { // of those with this row
 #pragma unroll
-    for (int u = 0; u < kMaxParts / 128; ++u) {
-        const int k = tid + 128 * u;
-        ml[u][0] = -INFINITY, ml[u][1] = 0.f;
-        if (k < n && T * (i0 + k) / G < T * (i0 + k + 1) / G) {
-            const float2 v = *reinterpret_cast<const float2 *>(part(k));
-            ml[u][0] = v.x, ml[u][1] = v.y;
-            m = fmaxf(m, v.x);
-        }
+        for (int o = ROWS; o < 32; o <<= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
+        if (lane < ROWS) at[tid >> 5][lane] = v;
+        __syncthreads();
+        v = at[0][wr];
+        for (int w = 1; w < warps; ++w) v = op(v, at[w][wr]);
+        return v;
+    };
+    float m = -INFINITY;
+    const int row_at = 2 * ((r0 + wr) % RB), stride = blockDim.x / ROWS;
+#pragma unroll 4
+    for (int k = tid / ROWS; k < n; k += stride) {
+        float2 v = make_float2(-INFINITY, 0.f);
+        if (r0 + wr < rows && (T >= G || quotient(T * (i0 + k), G) < quotient(T * (i0 + k + 1), G)))
+            v = __ldcg(reinterpret_cast<const float2 *>(part(k) + row_at));
+        weight[ROWS * k + wr] = v.x;
+        part_sum[ROWS * k + wr] = v.y;
+        m = fmaxf(m, v.x);
     }
-    m = warp_max(m);
-    if (lane == 0) red[tid >> 5] = m;
-    __syncthreads();
-    m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+    m = over_threads(red[0], m, [](float x, float y) { return fmaxf(x, y); });
     float l = 0.f;
-#pragma unroll
-    for (int u = 0; u < kMaxParts / 128; ++u) {
-        const int k = tid + 128 * u;
-        if (k >= n) break;
-        const float w = ml[u][0] == -INFINITY ? 0.f : exp2f(ml[u][0] - m);
-        weight[k] = w;
-        l = fmaf(w, ml[u][1], l);
+    for (int k = tid / ROWS; k < n; k += stride) {
+        const float mk = weight[ROWS * k + wr], w = mk == -INFINITY ? 0.f : exp2f(mk - m);
+        weight[ROWS * k + wr] = w;
+        l = fmaf(w, part_sum[ROWS * k + wr], l);
     }
-    l = warp_sum(l);
+    l = over_threads(red[1], l, [](float x, float y) { return x + y; }); // (and every weight is there)
+    if (tid < ROWS) { // (this thread's row)
+        red[0][0][tid] = l != 0.f ? 1.f / l : 0.f;
+        if (a.lse && r0 + tid < rows && blockIdx.y == 0) a.lse[b * rows + r0 + tid] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    }
     __syncthreads();
-    if (lane == 0) red[tid >> 5] = l;
-    __syncthreads();
-    l = (red[0] + red[1]) + (red[2] + red[3]);
-    const float inv = l != 0.f ? 1.f / l : 0.f;
-    for (int j = 4 * tid; j < R; j += 512) {
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int k0 = 0; k0 < n; k0 += 8) { // 8 loads on their way together
-            float4 v[8];
+    // every group takes an equal share of the parts
+    const int t = tid % kLanes, group = tid / kLanes, groups = blockDim.x / kLanes, k1 = n * (group + 1) / groups;
+    const int ch = kLanes * (int)blockIdx.y + 4 * (t >> 2), u0 = t & 3;
+    int at[U];
+    bool there[U];
+    float4 acc[U];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) v[u] = __ldcs(reinterpret_cast<const float4 *>(part(min(k0 + u, n - 1)) + 4 + j));
+    for (int i = 0; i < U; ++i) {
+        at[i] = latent_part_at<RB>((r0 + u0 + 4 * i) % RB, ch);
+        there[i] = r0 + u0 + 4 * i < rows && ch < R;
+        acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    for (int k0 = n * group / groups; k0 < k1; k0 += kLoads) { // 8 loads on their way together
+        float4 v[kLoads][U];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                const float w = k0 + u < n ? weight[k0 + u] : 0.f;
+        for (int e = 0; e < kLoads; ++e)
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+                if (there[i]) v[e][i] = __ldcg(reinterpret_cast<const float4 *>(part(min(k0 + e, k1 - 1)) + at[i]));
+#pragma unroll
+        for (int e = 0; e < kLoads; ++e)
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const float w = there[i] && k0 + e < k1 ? weight[ROWS * (k0 + e) + u0 + 4 * i] : 0.f;
                 if (w != 0.f) { // else nothing was seen there, or nothing was written
-                    acc.x = fmaf(w, v[u].x, acc.x);
-                    acc.y = fmaf(w, v[u].y, acc.y);
-                    acc.z = fmaf(w, v[u].z, acc.z);
-                    acc.w = fmaf(w, v[u].w, acc.w);
+                    acc[i].x = fmaf(w, v[e][i].x, acc[i].x);
+                    acc[i].y = fmaf(w, v[e][i].y, acc[i].y);
+                    acc[i].z = fmaf(w, v[e][i].z, acc[i].z);
+                    acc[i].w = fmaf(w, v[e][i].w, acc[i].w);
                 }
             }
-        }
-        st4(a.o, (int64_t)blockIdx.x * R + j, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
     }
-    if (a.lse && tid == 0) a.lse[blockIdx.x] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    if constexpr (U == 1)
+        if (groups > 1) {
+            if (group > 0) sums[kLanes * (group - 1) + t] = acc[0];
+            __syncthreads();
+            if (group > 0) return;
+            for (int i = 0; i < groups - 1; ++i) {
+                const float4 v = sums[kLanes * i + t];
+                acc[0].x += v.x, acc[0].y += v.y, acc[0].z += v.z, acc[0].w += v.w;
+            }
+        }
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+        if (there[i]) {
+            const float inv = red[0][0][u0 + 4 * i];
+            st4(a.o, (b * rows + r0 + u0 + 4 * i) * R + ch, make_float4(acc[i].x * inv, acc[i].y * inv, acc[i].z * inv, acc[i].w * inv));
+        }
 }
 
 // ---- expanded form -------------------------------------------------------------------------
@@ -294,24 +336,28 @@ template <typename T> __global__ void __launch_bounds__(32 * kWarps) latent_pref
 size_t latent_decode_generic_workspace(int64_t B, int Lq, int H, int R, int64_t max_len, int *grid, int *par)
 {
     Split::plan(B, Lq, H, max_len, device_sms(), grid, par);
-    return (size_t)*grid * 2 * kRB * (R + 4) * sizeof(float);
+    return (size_t)*grid * 2 * latent_part_size<kRB>(R) * sizeof(float);
 }
 
 template <class Split, int RB> static cudaError_t launch_merge(const LatentDecodeArgs &a, cudaStream_t st)
 {
     if (a.grid == a.par) return cudaSuccess; // one CTA, or one group, cuts no run
     if (a.grid > kMaxParts) return cudaErrorInvalidValue;
-    // its blocks come up while the parts are written, and wait for them
+    const int64_t parts = (a.grid / a.par + a.B - 1) / a.B; // of a run of the average length
+    const bool few = parts <= 8 && a.B * a.Lq * a.H >= 16 * 2 * device_sms(); // and rows enough for all SMs
+    const int rows = few ? 16 : 4, threads = few || parts > 16 ? 512 : parts > 8 ? 256 : 128, R = a.rows.c - a.rows.rope_dims;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(a.B * a.Lq * a.H));
-    cfg.blockDim = dim3(128);
+    cfg.gridDim = dim3((unsigned)(a.B * ((a.Lq * a.H + rows - 1) / rows)), few ? 1u : (unsigned)((R + 127) / 128));
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (few ? 0 : (size_t)(threads - 128) * sizeof(float4)) + 2 * (size_t)(a.grid / a.par) * rows * sizeof(float);
     cfg.stream = st;
+    // its blocks come up while the parts are written, and wait for them
     cudaLaunchAttribute at;
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, latent_merge_kernel<Split, RB>, a);
+    return few ? cudaLaunchKernelEx(&cfg, latent_merge_kernel<Split, RB, 16>, a) : cudaLaunchKernelEx(&cfg, latent_merge_kernel<Split, RB, 4>, a);
 }
 
 cudaError_t launch_latent_merge_tc(const LatentDecodeArgs &a, int rows, cudaStream_t st)
