@@ -33,7 +33,7 @@ EXPORTED = ("csa_compress", "hca_compress", "csa_quantize_kv", "csa_quantize_fp4
             "indexer_topk_workspace_size", "indexer_topk", "hybrid_attn_prefill",
             "hybrid_attn_decode_workspace_size", "hybrid_attn_decode", "csa_device_error",
             "latent_append", "latent_gather", "latent_attn_decode_workspace_size", "latent_attn_decode",
-            "latent_attn_prefill", "csa_status_string", "csa_abi_version", "csa_last_path", "csa_set_wait_limit_ns")
+            "latent_attn_prefill_workspace_size", "latent_attn_prefill", "csa_status_string", "csa_abi_version", "csa_last_path", "csa_set_wait_limit_ns")
 
 
 class CsaError(RuntimeError):
@@ -90,7 +90,8 @@ def _load():
         "latent_gather": ([P_kv, vp, vp, i64, vp, i32, i32, vp, i64, vp, vp, i32, vp], ctypes.c_int),
         "latent_attn_decode_workspace_size": ([i64, i32, i32, i32, i64], sz),
         "latent_attn_decode": ([vp, P_kv, vp, vp, i32, i32, vp, f32, i64, i32, i32, i64, vp, vp, vp, sz, vp], ctypes.c_int),
-        "latent_attn_prefill": ([vp, vp, vp, vp, vp, i64, i64, i64, i32, i32, i32, i32, i64, f32, i32, i32, vp, vp, vp],
+        "latent_attn_prefill_workspace_size": ([i64, i64, i64, i32, i32, i32, i32, i64, i32], sz),
+        "latent_attn_prefill": ([vp, vp, vp, vp, vp, i64, i64, i64, i32, i32, i32, i32, i64, f32, i32, i32, vp, vp, vp, sz, vp],
                                 ctypes.c_int),
         "csa_device_error": ([vp, ctypes.POINTER(i32)], ctypes.c_int),
         "csa_status_string": ([i32], ctypes.c_char_p),
@@ -502,6 +503,14 @@ def _launch(fn: str, dev: int, stream, args):
     _check(fn, getattr(_lib, fn)(*args, int(st)))
 
 
+def _on_device(dev: int, f, *args):
+    """f(*args) with the operands' device current."""
+    if dev < 0 or dev == torch.cuda.current_device():
+        return f(*args)
+    with torch.cuda.device(dev):
+        return f(*args)
+
+
 def _float_dtype(name: str, t):
     if t.dtype is torch.bfloat16:
         return CSA_BF16
@@ -567,11 +576,7 @@ def latent_attn_decode(q, rows: KvRows, pos, scale: float, max_len: int, pages=N
         o = q.new_empty((B, Lq, H, R), dtype=torch.bfloat16)
     op, lp = _in("o", o, torch.bfloat16, (B, Lq, H, R), dev), _opt("lse", lse, torch.float32, (B, Lq, H), dev)
     if workspace is None:
-        if dev >= 0 and dev != torch.cuda.current_device():
-            with torch.cuda.device(dev):
-                need = latent_attn_decode_workspace_size(B, Lq, H, R, max_len)
-        else:
-            need = latent_attn_decode_workspace_size(B, Lq, H, R, max_len)
+        need = _on_device(dev, _lib.latent_attn_decode_workspace_size, B, Lq, H, R, max_len)
         workspace = q.new_empty((need,), dtype=torch.uint8)
     ws = workspace.numel()
     wp = _in("workspace", workspace, torch.uint8, (ws,), dev)
@@ -579,8 +584,13 @@ def latent_attn_decode(q, rows: KvRows, pos, scale: float, max_len: int, pages=N
     return o
 
 
+def latent_attn_prefill_workspace_size(B: int, Tq: int, Tk: int, H: int, dn: int, dr: int, dv: int, max_q: int,
+                                       dtype=torch.bfloat16) -> int:
+    return int(_lib.latent_attn_prefill_workspace_size(B, Tq, Tk, H, dn, dr, dv, max_q, CSA_BF16 if dtype is torch.bfloat16 else CSA_F32))
+
+
 def latent_attn_prefill(q, kv, k_rope, cu_q, cu_k, max_q: int, scale: float, causal: bool = True, o=None, lse=None,
-                        stream=None):
+                        workspace=None, stream=None):
     """Expanded latent attention over packed sequences: q [Tq, H, dn + dr], kv [Tk, H, dn + dv] (a head's
     unrotated key, then its value), k_rope [Tk, dr] shared by the heads.  Returns o [Tq, H, dv]."""
     dev, t, dt = q.get_device(), q.dtype, _float_dtype("q", q)
@@ -595,8 +605,14 @@ def latent_attn_prefill(q, kv, k_rope, cu_q, cu_k, max_q: int, scale: float, cau
             raise ValueError(f"kv has {dkv} channels a head, of which {dn} are the key's")
         o = q.new_empty((Tq, H, dv))
     op, lp = _in("o", o, t, (Tq, H, dv), dev), _opt("lse", lse, torch.float32, (Tq, H), dev)
+    if workspace is None and dev >= 0:
+        need = _on_device(dev, _lib.latent_attn_prefill_workspace_size, B, Tq, Tk, H, dn, dr, dv, max_q, dt)
+        if need:
+            workspace = q.new_empty((need,), dtype=torch.uint8)
+    ws = 0 if workspace is None else workspace.numel()
+    wp = _opt("workspace", workspace, torch.uint8, (ws,), dev)
     _launch("latent_attn_prefill", dev, stream,
-            (qp, kp, rp, cq, ck, B, Tq, Tk, H, dn, dr, dv, max_q, scale, 1 if causal else 0, dt, op, lp))
+            (qp, kp, rp, cq, ck, B, Tq, Tk, H, dn, dr, dv, max_q, scale, 1 if causal else 0, dt, op, lp, wp, ws))
     return o
 
 

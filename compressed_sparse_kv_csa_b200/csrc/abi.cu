@@ -638,9 +638,19 @@ int latent_attn_decode(const void *q, const csa_kv_rows *rows, const int64_t *po
     return status_of(launch_latent_decode_generic(a, S(stream)));
 }
 
+size_t latent_attn_prefill_workspace_size(int64_t B, int64_t Tq, int64_t Tk, int32_t H, int32_t dn, int32_t dr, int32_t dv,
+                                          int64_t max_q, int32_t dtype)
+{
+    if (B < 1 || B >= ((int64_t)1 << 31) || Tq < 1 || Tk < 1 || H < 1 || H > 128 || max_q < 1) return 0;
+    LatentPrefillArgs a{};
+    a.B = B, a.Tq = Tq, a.Tk = Tk, a.H = H, a.dn = dn, a.dr = dr, a.dv = dv, a.max_q = max_q < Tq ? max_q : Tq;
+    const size_t need = latent_prefill_tc_eligible(a, dtype) ? latent_prefill_tc_workspace(a) : 0;
+    return need ? need + kAlign : 0;
+}
+
 int latent_attn_prefill(const void *q, const void *kv, const void *k_rope, const int64_t *cu_q, const int64_t *cu_k, int64_t B,
                         int64_t Tq, int64_t Tk, int32_t H, int32_t dn, int32_t dr, int32_t dv, int64_t max_q, float scale,
-                        int32_t causal, int32_t dtype, void *o, float *lse, void *stream)
+                        int32_t causal, int32_t dtype, void *o, float *lse, void *ws, size_t ws_bytes, void *stream)
 {
     if (!q || !cu_q || !cu_k || !o || B < 0 || Tq < 0 || Tk < 0 || max_q < 0 || !dtype_ok(dtype)) return CSA_ERR_INVALID_ARG;
     if (Tk > 0 && (!kv || !k_rope)) return CSA_ERR_INVALID_ARG;
@@ -653,8 +663,15 @@ int latent_attn_prefill(const void *q, const void *kv, const void *k_rope, const
     const LatentPrefillArgs a{q, kv, k_rope, cu_q, cu_k, B, Tq, Tk, max_q, H, dn, dr, dv, scale, causal ? 1 : 0, o, lse,
                               dev_error_word()};
     if (latent_prefill_tc_eligible(a, dtype)) {
+        LatentKeyParts parts{nullptr, 1};
+        if (ws) {
+            const size_t need = latent_prefill_tc_workspace(a);
+            if (need && ws_bytes < need + kAlign) return CSA_ERR_WORKSPACE;
+            parts.part = reinterpret_cast<float *>((reinterpret_cast<uintptr_t>(ws) + kAlign - 1) / kAlign * kAlign);
+            parts.n = latent_prefill_tc_parts(a);
+        }
         note_path(CSA_PATH_LATENT_PREFILL_TC);
-        return status_of(launch_latent_prefill_tc(a, S(stream)));
+        return status_of(launch_latent_prefill_tc(a, parts, S(stream)));
     }
     note_path(CSA_PATH_LATENT_PREFILL_GENERIC);
     return status_of(launch_latent_prefill_generic(a, dtype, S(stream)));

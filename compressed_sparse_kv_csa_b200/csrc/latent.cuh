@@ -95,10 +95,7 @@ __device__ __forceinline__ int64_t latent_visible(const LatentDecodeArgs &a, int
 // A partial: the rows' (maximum, sum), then their outputs, four channels of all rows beside one another, so that the lanes
 // of a warp write whole sectors where they hold rows, and read them where they hold four rows of eight such fours.
 template <int RB> __host__ __device__ __forceinline__ int64_t latent_part_size(int R) { return (int64_t)RB * (R + 4); } // floats
-template <int RB> __device__ __forceinline__ float *latent_part(const LatentDecodeArgs &a, int R, int64_t slot)
-{
-    return a.part + slot * latent_part_size<RB>(R);
-}
+template <int RB> __device__ __forceinline__ float *latent_part(float *part, int R, int64_t slot) { return part + slot * latent_part_size<RB>(R); }
 template <int RB> __device__ __forceinline__ int latent_part_at(int row, int ch) { return 4 * RB + ((ch >> 2) * RB + row) * 4 + (ch & 3); }
 
 // x / y of numbers that are not negative, in 32 bits where they fit (a fifth of the time).
@@ -271,6 +268,10 @@ struct LatentPrefillArgs {
     float *lse; // [Tq, H] or null
     int *err;
 };
+struct LatentKeyParts {
+    float *part; // their partials (latent_part of 256 rows), block after block
+    int n;       // of a block of queries; 1: the keys are not split
+};
 
 // The rows of sequence b in a packed array of T rows.
 __device__ __forceinline__ void packed_range(const int64_t *cu, int64_t b, int64_t T, int64_t *beg, int64_t *end)
@@ -281,7 +282,9 @@ __device__ __forceinline__ void packed_range(const int64_t *cu, int64_t b, int64
 }
 
 bool latent_prefill_tc_eligible(const LatentPrefillArgs &a, int dtype);
-cudaError_t launch_latent_prefill_tc(const LatentPrefillArgs &a, cudaStream_t st);
+int latent_prefill_tc_parts(const LatentPrefillArgs &a); // key parts, 1: none
+size_t latent_prefill_tc_workspace(const LatentPrefillArgs &a);
+cudaError_t launch_latent_prefill_tc(const LatentPrefillArgs &a, const LatentKeyParts &parts, cudaStream_t st);
 cudaError_t launch_latent_prefill_generic(const LatentPrefillArgs &a, int dtype, cudaStream_t st);
 
 } // namespace csa

@@ -56,15 +56,6 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr uint32_t kNoKey = 0xffffffffu; // in place of a row's scale: the key is not to be seen
 constexpr float kTop = 448.f, kLow = 1.f / 16.f, kSmallestScale = 7.8886090522101181e-31f; // 2^-100
 
-// A descriptor as two words, so that a step along an operand is one 32-bit addition (the issuing thread's
-// instructions between two MMAs bound the chain as much as the MMAs do).
-struct Desc {
-    uint32_t lo, hi;
-    __device__ __forceinline__ explicit Desc(uint64_t d) : lo((uint32_t)d), hi((uint32_t)(d >> 32)) {}
-    __device__ __forceinline__ Desc(uint32_t l, uint32_t h) : lo(l), hi(h) {}
-    __device__ __forceinline__ Desc at(uint32_t bytes) const { return Desc(lo + (bytes >> 4), hi); }
-};
-
 template <bool F8, bool WS = true> __device__ __forceinline__ void mma(uint32_t d, Desc a, Desc b, uint32_t idesc, uint32_t accumulate)
 {
     if constexpr (F8 && !WS)
@@ -741,7 +732,7 @@ static __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, c
         l = sum4(other);
         const int64_t out_row = run.b * n_rows + rr;
         const float inv = l != 0.f ? 1.f / l : 0.f;
-        float *rec = latent_part<kRB>(a, kR, 2 * (int64_t)blockIdx.x + run.first);
+        float *rec = latent_part<kRB>(a.part, kR, 2 * (int64_t)blockIdx.x + run.first);
         auto put_out = [&](const auto &x, int ch) { // consecutive channels of the row
             constexpr int n = sizeof(x) / 4;
             if (run.whole) {

@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(32 * kWarps) latent_decode_generic_kernel(Late
                     if (lane + 32 * i < R) a.o[row * R + lane + 32 * i] = f32_to_bf16_bits(acc[u][i] * inv);
                 if (a.lse && lane == 0) a.lse[row] = l[u] != 0.f ? (m[u] + log2f(l[u])) * kLn2 : -INFINITY;
             } else {
-                float *p = latent_part<kRB>(a, R, 2 * (int64_t)blockIdx.x + first);
+                float *p = latent_part<kRB>(a.part, R, 2 * (int64_t)blockIdx.x + first);
                 if (lane == 0) p[2 * r] = m[u], p[2 * r + 1] = l[u];
 #pragma unroll
                 for (int i = 0; i < kMaxNV; ++i)
@@ -177,7 +177,7 @@ template <class Split, int RB, int ROWS> __global__ void __launch_bounds__(512) 
     const int n = (int)(i1 - i0 + 1);
     // part k: slot 2 i + 1 where the run begins, slot 2 i behind; a CTA without tiles has none
     const int64_t cta0 = i0 * a.par + (a.par > 1 ? rb : 0), step = 2 * a.par * latent_part_size<RB>(R);
-    const float *first = latent_part<RB>(a, R, 2 * cta0 + 1), *rest = latent_part<RB>(a, R, 2 * cta0);
+    const float *first = latent_part<RB>(a.part, R, 2 * cta0 + 1), *rest = latent_part<RB>(a.part, R, 2 * cta0);
     auto part = [&](int k) { return k == 0 ? first : rest + k * step; };
     const int wr = tid % ROWS; // the row that this thread weighs parts of
     auto over_threads = [&](float (&at)[16][ROWS], float v, auto op) { // of those with this row

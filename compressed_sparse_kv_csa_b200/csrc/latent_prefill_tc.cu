@@ -17,8 +17,12 @@
 // Shared memory: Q 96 KB, and a ring of eight 16 KB slots of [128 rows x 64 channels] that the key
 // (three slots a tile) and value (two) boxes pass through in order, so that the loads run up to 1.6
 // tiles ahead.  Everything arrives by TMA.
+// P is handed over in two halves, and one instruction takes the maximum of three: 16k queries and keys of 16 heads 3%
+// faster than without.  Where query blocks are few their keys are split (latent_prefill_tc_parts).
 // Roles: warps 0-3 and 4-7 softmax, rescale and output of the two query tiles (one row a thread), warp 8
-// TMA, warp 9 MMA.  Bound by the tensor cores: 2 * 128 * 128 * 320 flops a tile pair.
+// TMA, warp 9 MMA.  Per pair of query tiles and tile of keys the tensor cores need 2,560 cycles and the chain S - softmax - P V
+// of each, beside the other's MMAs, 3,800; in long calls the chip's power limits what is left (990 W, 1.5 GHz): 16k
+// x 16 heads causal 1.03 ms in a short run (1.33 PFLOP/s), 1.12 ms in a loop of seconds; 4k 70 us.
 #include "latent.cuh"
 #include "tc_common.cuh"
 #include "tma_host.cuh"
@@ -56,13 +60,14 @@ struct Maps {
 struct Job {
     int64_t q0, k0;
     int h, i0, nq, nk, lag, n[2], tiles; // n[t]: key tiles of query tile t
+    int c0;                              // the first of them, behind those of the parts before
 };
 
-__device__ __forceinline__ bool find_job(const LatentPrefillArgs &a, Job &j)
+__device__ __forceinline__ bool find_job(const LatentPrefillArgs &a, int64_t id, int part, int parts, Job &j)
 {
     // the query blocks that see the most keys first
     const int per = (int)((a.max_q + 2 * kT - 1) / (2 * kT));
-    const int64_t bh = a.B * a.H, id = blockIdx.x;
+    const int64_t bh = a.B * a.H;
     const int64_t r = id % bh, b = r / a.H;
     j.h = (int)(r % a.H);
     j.i0 = (per - 1 - (int)(id / bh)) * 2 * kT;
@@ -81,15 +86,15 @@ __device__ __forceinline__ bool find_job(const LatentPrefillArgs &a, Job &j)
         j.n[t] = seen <= 0 ? 0 : (int)((seen + kT - 1) / kT);
         j.tiles = max(j.tiles, j.n[t]);
     }
+    j.c0 = 0;
+    if (part >= 0) {
+        const int c1 = (int)((int64_t)j.tiles * (part + 1) / parts);
+        j.c0 = (int)((int64_t)j.tiles * part / parts);
+        j.tiles = c1 - j.c0;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) j.n[t] = max(0, min(j.n[t], c1) - j.c0);
+    }
     return j.i0 < j.nq;
-}
-
-__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate)
-{
-    asm volatile("{\n\t.reg .pred p;\n\t"
-                 "setp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc),
-                 "r"(accumulate));
 }
 
 __device__ __forceinline__ float ex2(float x)
@@ -167,8 +172,8 @@ __device__ __forceinline__ bool tma_role(const Job &j, const Maps &M, uint32_t b
     Ring r;
     uint32_t lap = 0; // the first lap's slots are empty
     for (int i = 0; i < j.tiles; ++i) {
-        const int y = (int)(j.k0 + (int64_t)i * kT);
-        const int tail = j.nk - i * kT; // rows of the sequence in this tile, when less than kT
+        const int y = (int)(j.k0 + (int64_t)(j.c0 + i) * kT);
+        const int tail = j.nk - (j.c0 + i) * kT; // rows of the sequence in this tile, when less than kT
         int v_slot[2];
         for (int s = 0; s < 5; ++s) {
             const int slot = r.slot;
@@ -228,6 +233,7 @@ __device__ __forceinline__ bool mma_role(const Job &j, uint32_t base, uint32_t t
     auto bar = [&](int b) { return bars + 8u * (uint32_t)b; };
     if (!mbar_wait(bar(B_Q), 0)) return false;
     tc_fence_after();
+    const Desc q_desc(sdesc_sw128(base + OFF_Q, 16, 1024)), ring_desc(sdesc_sw128(base + OFF_RING, 16, 1024));
     Ring r;
     struct Box {
         int slot[3];
@@ -249,8 +255,8 @@ __device__ __forceinline__ bool mma_role(const Job &j, uint32_t base, uint32_t t
         for (int s = 0; s < 3; ++s)
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-                mma_bf16(tmem + kColS + 128u * t, sdesc_sw128(base + OFF_Q + (uint32_t)(3 * t + s) * kSlot + 32u * kk, 16, 1024),
-                         sdesc_sw128(base + OFF_RING + (uint32_t)k.slot[s] * kSlot + 32u * kk, 16, 1024), IDESC_S, (s | kk) != 0);
+                mma_bf16(tmem + kColS + 128u * t, q_desc.at((uint32_t)(3 * t + s) * kSlot + 32u * kk),
+                         ring_desc.at((uint32_t)k.slot[s] * kSlot + 32u * kk), IDESC_S, (s | kk) != 0);
         mma_commit(bar(B_S + t));
     };
     Box k, v;
@@ -264,6 +270,8 @@ __device__ __forceinline__ bool mma_role(const Job &j, uint32_t base, uint32_t t
         const uint32_t ph = (uint32_t)(i & 1);
         if (!take(2, v)) return false;
         const int lo = min(v.slot[0], v.slot[1]), hi = max(v.slot[0], v.slot[1]);
+        const Desc dv(sdesc_sw128(base + OFF_RING + (uint32_t)lo * kSlot, (uint32_t)(hi - lo) * kSlot, 1024));
+#pragma unroll
         for (int t = 0; t < 2; ++t) {
             if (i < j.n[t]) {
 #pragma unroll
@@ -273,8 +281,7 @@ __device__ __forceinline__ bool mma_role(const Job &j, uint32_t base, uint32_t t
                         tc_fence_after();
                     }
                     mma_bf16_ts(tmem + kColO + 128u * t, tmem + kColS + 128u * t + 8u * kk,
-                                sdesc_sw128(base + OFF_RING + (uint32_t)lo * kSlot + 2048u * kk, (uint32_t)(hi - lo) * kSlot, 1024),
-                                IDESC_PV, (i | kk) != 0);
+                                dv.at(2048u * kk), IDESC_PV, (i | kk) != 0);
                 }
                 if (i + 1 == j.n[t]) mma_commit(bar(B_O + t));
             }
@@ -287,8 +294,9 @@ __device__ __forceinline__ bool mma_role(const Job &j, uint32_t base, uint32_t t
     return true;
 }
 
-// Softmax, rescale and output of query tile t: one row per thread.
-__device__ __forceinline__ bool softmax_role(const LatentPrefillArgs &a, const Job &j, uint32_t base, uint32_t tmem, int warp, int lane)
+// Softmax, rescale and output of query tile t: one row per thread.  Of a part of the keys, the maximum, the sum and O as
+// it is go to the part's record.
+template <bool PARTS> __device__ __forceinline__ bool softmax_role(const LatentPrefillArgs &a, const LatentKeyParts &parts, const Job &j, uint32_t base, uint32_t tmem, int warp, int lane)
 {
     const uint32_t bars = base + OFF_BAR;
     auto bar = [&](int b) { return bars + 8u * (uint32_t)b; };
@@ -304,6 +312,7 @@ __device__ __forceinline__ bool softmax_role(const LatentPrefillArgs &a, const J
     const bool turn = a.scale < 0.f;
     const float sl2 = fmaxf(fabsf(a.scale) * kLog2e, 1e-37f);
     float m = -INFINITY, l = 0.f; // maximum in use (scaled, log2 domain), sum
+    const int c0 = PARTS ? j.c0 : 0;
     for (int c = 0; c < j.n[t]; ++c) {
         if (!__all_sync(0xffffffffu, mbar_wait(bar(B_S + t), (uint32_t)(c & 1)))) return false;
         tc_fence_after();
@@ -315,8 +324,8 @@ __device__ __forceinline__ bool softmax_role(const LatentPrefillArgs &a, const J
 #pragma unroll
             for (int e = 0; e < kT; ++e) s[e] = -s[e];
         }
-        if (c * kT + kT - 1 > last_all) {
-            const int n = last - c * kT; // the last visible key of the tile
+        if ((c + c0) * kT + kT - 1 > last_all) {
+            const int n = last - (c + c0) * kT; // the last visible key of the tile
 #pragma unroll
             for (int e = 0; e < kT; ++e) s[e] = e <= n ? s[e] : -INFINITY;
         }
@@ -372,6 +381,25 @@ __device__ __forceinline__ bool softmax_role(const LatentPrefillArgs &a, const J
         if (!__all_sync(0xffffffffu, mbar_wait(bar(B_O + t), 0))) return false;
         tc_fence_after();
     }
+    if constexpr (PARTS) {
+        const int row = t * kT + 32 * (warp & 3) + lane;
+        float *rec = latent_part<2 * kT>(parts.part, kDv, blockIdx.x);
+        if (i < j.nq) *reinterpret_cast<float2 *>(rec + 2 * row) = make_float2(l == 0.f ? -INFINITY : m == -INFINITY ? 0.f : m, l);
+        if (j.n[t] > 0) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                uint32_t o[32];
+                tmem_ld32(tO + 32u * g, o);
+                tmem_ld_wait();
+                if (i < j.nq)
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        *reinterpret_cast<uint4 *>(rec + latent_part_at<2 * kT>(row, 32 * g + e)) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            }
+        }
+        tc_fence_before();
+        return true;
+    }
     const float inv = l != 0.f ? 1.f / l : 0.f;
     const int64_t row = (j.q0 + i) * a.H + j.h;
     uint4 *out = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.o) + row * kDv);
@@ -400,11 +428,14 @@ __device__ __forceinline__ bool softmax_role(const LatentPrefillArgs &a, const J
     return true;
 }
 
-__global__ void __launch_bounds__(kThreads, 1) latent_prefill_tc_kernel(LatentPrefillArgs a, const __grid_constant__ Maps maps)
+template <bool PARTS>
+__global__ void __launch_bounds__(kThreads, 1) latent_prefill_tc_kernel(LatentPrefillArgs a, const __grid_constant__ Maps maps, LatentKeyParts parts)
 {
     extern __shared__ uint8_t smem_raw[];
+    if constexpr (PARTS) cudaTriggerProgrammaticLaunchCompletion(); // the merge may come up
     Job j;
-    if (!find_job(a, j)) return; // no queries here (the same on every thread)
+    const int64_t block = PARTS ? blockIdx.x / parts.n : blockIdx.x;
+    if (!find_job(a, block, PARTS ? (int)(blockIdx.x % parts.n) : -1, parts.n, j)) return; // no queries here (the same on every thread)
     const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
     uint8_t *sp = smem_raw + (base - raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -420,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_tc_kernel(LatentPr
     bool ok = true;
     if (warp < kTmaWarp) {
         regs_inc<kRegsSoft>();
-        ok = softmax_role(a, j, base, tmem, warp, lane);
+        ok = softmax_role<PARTS>(a, parts, j, base, tmem, warp, lane);
     } else {
         regs_dec<kRegsRest>();
         if (warp == kTmaWarp) ok = tma_role(j, maps, base, lane);
@@ -436,6 +467,54 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_tc_kernel(LatentPr
     __syncthreads();
     tc_fence_after();
     if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+// Merge of a block's key parts, 16 rows x 128 channels a CTA: with part i holding the maximum m_i, the sum l_i and O_i,
+// o = sum 2^(m_i - m) O_i / l, l = sum 2^(m_i - m) l_i, m = max m_i.  Bound by the latency of its loads.
+constexpr int kMergeRows = 16;
+__global__ void __launch_bounds__(32 * kMergeRows) latent_prefill_merge_kernel(LatentPrefillArgs a, LatentKeyParts parts)
+{
+    constexpr int kBlocks = 2 * kT / kMergeRows;
+    // four rows of eight fours of channels a warp
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int r = (int)(blockIdx.x % kBlocks) * kMergeRows + 4 * (warp >> 2) + (lane & 3), ch = 32 * (warp & 3) + 4 * (lane >> 2);
+    const int64_t block = blockIdx.x / kBlocks;
+    Job j;
+    const bool there = find_job(a, block, -1, 1, j) && j.i0 + r < j.nq;
+    cudaGridDependencySynchronize(); // every block waits: what follows in the stream waits for this kernel alone
+    if (!there) return;
+    const int64_t step = latent_part_size<2 * kT>(kDv);
+    const float *rec = latent_part<2 * kT>(parts.part, kDv, block * parts.n);
+    float m = -INFINITY, l = 0.f;
+#pragma unroll 8
+    for (int k = 0; k < parts.n; ++k) m = fmaxf(m, __ldcg(rec + k * step + 2 * r));
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int at = latent_part_at<2 * kT>(r, ch);
+    for (int k0 = 0; k0 < parts.n; k0 += 4) {
+        float2 ml[4];
+        float4 v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float *p = rec + min(k0 + e, parts.n - 1) * step;
+            ml[e] = __ldcg(reinterpret_cast<const float2 *>(p + 2 * r));
+            v[e] = __ldcg(reinterpret_cast<const float4 *>(p + at));
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (k0 + e >= parts.n || ml[e].x == -INFINITY) continue; // nothing was seen there, or nothing was written
+            const float w = exp2f(ml[e].x - m);
+            l = fmaf(w, ml[e].y, l);
+            acc.x = fmaf(w, v[e].x, acc.x);
+            acc.y = fmaf(w, v[e].y, acc.y);
+            acc.z = fmaf(w, v[e].z, acc.z);
+            acc.w = fmaf(w, v[e].w, acc.w);
+        }
+    }
+    const float inv = l != 0.f ? 1.f / l : 0.f;
+    const int64_t row = (j.q0 + j.i0 + r) * a.H + j.h;
+    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.o) + row * kDv + ch) =
+        make_uint2(pk_bf16(acc.x * inv, acc.y * inv), pk_bf16(acc.z * inv, acc.w * inv));
+    if (a.lse && ch == 0) a.lse[row] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
 }
 
 // A packed bf16 array [rows, heads, cols] read in boxes of 64 columns of one head x 128 rows with the
@@ -458,19 +537,53 @@ bool latent_prefill_tc_eligible(const LatentPrefillArgs &a, int dtype)
     return dtype == CSA_BF16 && a.dn == kDn && a.dr == kDr && a.dv == kDv && a.Tk > 0;
 }
 
-cudaError_t launch_latent_prefill_tc(const LatentPrefillArgs &a, cudaStream_t st)
+static int64_t query_blocks(const LatentPrefillArgs &a) { return a.B * a.H * ((a.max_q + 2 * kT - 1) / (2 * kT)); }
+
+// Where the query blocks leave at least half of the SMs idle, their keys are split into parts of at least 4 tiles (of a
+// sequence of the average length), as many as the SMs have room for at once.  256 queries of 16 heads after 64k keys: 142
+// us in 9 parts, 914 whole; after 1k: 18.6 in 2, 22.1 whole; 74 blocks after 8k: 88 in 2, 125 whole.
+int latent_prefill_tc_parts(const LatentPrefillArgs &a)
+{
+    const int64_t blocks = query_blocks(a), room = blocks > 0 ? device_sms() / blocks : 0, tiles = (a.Tk / a.B + kT - 1) / kT;
+    const int64_t parts = room < tiles / 4 ? room : tiles / 4;
+    return parts < 2 ? 1 : (int)parts;
+}
+size_t latent_prefill_tc_workspace(const LatentPrefillArgs &a)
+{
+    const int parts = latent_prefill_tc_parts(a);
+    return parts < 2 ? 0 : (size_t)(query_blocks(a) * parts * latent_part_size<2 * kT>(kDv)) * sizeof(float);
+}
+
+template <bool PARTS> static cudaError_t launch(const LatentPrefillArgs &a, const Maps &maps, const LatentKeyParts &parts, int64_t ctas, cudaStream_t st)
+{
+    static std::atomic<bool> done[64];
+    cudaError_t e = prepare_kernel(latent_prefill_tc_kernel<PARTS>, SMEM_ALLOC, kRegs, done);
+    if (e != cudaSuccess) return e;
+    latent_prefill_tc_kernel<PARTS><<<(unsigned)ctas, kThreads, SMEM_ALLOC, st>>>(a, maps, parts);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_latent_prefill_tc(const LatentPrefillArgs &a, const LatentKeyParts &parts, cudaStream_t st)
 {
     Maps maps;
     if (!encode_heads(&maps.q, a.q, a.Tq, a.H, kDn + kDr) || !encode_heads(&maps.kv, a.kv, a.Tk, a.H, kDn + kDv) ||
         !tma::encode_bf16_rows(&maps.kr, a.k_rope, (uint64_t)a.Tk, kDr, kT))
         return cudaErrorNotSupported;
-    static std::atomic<bool> done[64];
-    cudaError_t e = prepare_kernel(latent_prefill_tc_kernel, SMEM_ALLOC, kRegs, done);
-    if (e != cudaSuccess) return e;
-    const int64_t blocks = a.B * a.H * ((a.max_q + 2 * kT - 1) / (2 * kT));
+    const int64_t blocks = query_blocks(a);
     if (blocks >= ((int64_t)1 << 31)) return cudaErrorInvalidValue;
-    latent_prefill_tc_kernel<<<(unsigned)blocks, kThreads, SMEM_ALLOC, st>>>(a, maps);
-    return cudaGetLastError();
+    if (parts.n < 2) return launch<false>(a, maps, parts, blocks, st);
+    cudaError_t e = launch<true>(a, maps, parts, blocks * parts.n, st);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{}; // its blocks come up while the parts are written, and wait for them
+    cfg.gridDim = dim3((unsigned)(blocks * (2 * kT / kMergeRows)));
+    cfg.blockDim = dim3(32 * kMergeRows);
+    cfg.stream = st;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, latent_prefill_merge_kernel, a, parts);
 }
 
 } // namespace csa

@@ -260,6 +260,30 @@ __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr, uint32_t lbo_byt
     return d;
 }
 
+// A descriptor as two words, so that a step along an operand is one 32-bit addition (the issuing thread's
+// instructions between two MMAs bound the chain as much as the MMAs do).
+struct Desc {
+    uint32_t lo, hi;
+    __device__ __forceinline__ explicit Desc(uint64_t d) : lo((uint32_t)d), hi((uint32_t)(d >> 32)) {}
+    __device__ __forceinline__ Desc(uint32_t l, uint32_t h) : lo(l), hi(h) {}
+    __device__ __forceinline__ Desc at(uint32_t bytes) const { return Desc(lo + (bytes >> 4), hi); }
+};
+__device__ __forceinline__ void mma_bf16(uint32_t d_tmem, Desc a, Desc b, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\t"
+                 "setp.ne.b32 p, %6, 0;\n\tmov.b64 x, {%1, %2};\n\tmov.b64 y, {%3, %4};\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %5, p;\n\t}" ::"r"(d_tmem), "r"(a.lo), "r"(a.hi), "r"(b.lo), "r"(b.hi),
+                 "r"(idesc), "r"(accumulate));
+}
+// A in TMEM.
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, Desc b, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 y;\n\t"
+                 "setp.ne.b32 p, %5, 0;\n\tmov.b64 y, {%2, %3};\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t}" ::"r"(d_tmem), "r"(a_tmem), "r"(b.lo), "r"(b.hi),
+                 "r"(idesc), "r"(accumulate));
+}
+
 // 64-byte-swizzled K-major operand descriptor (rows of 64 bytes, 8-row atoms of 512 bytes):
 // SBO = byte stride between 8-row groups.
 __device__ __forceinline__ uint64_t sdesc_sw64(uint32_t saddr, uint32_t sbo_bytes)

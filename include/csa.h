@@ -486,15 +486,21 @@ int latent_attn_decode(const void *q, const csa_kv_rows *rows, const int64_t *po
  *   it are not computed).  Rows of q outside the sequences get no output: o and lse keep what
  *   they held.  Rows of kv and k_rope outside a sequence are not part of its result whatever they
  *   hold; a non-finite value in a sequence's own rows may reach all of its outputs.
+ *   ws       workspace of latent_attn_prefill_workspace_size(...) bytes, queried with the device current (0
+ *            where none is of use), or NULL: with it, a few queries' many keys are split over the SMs and the
+ *            parts merged, without it they are not.  Calls that may overlap need one each
+ * The order of a row's sums depends on the sizes and the device's SM count, not on timing.
  * Limits: dn, dr, dv multiples of 16, dn + dr <= 256, dv <= 256, H <= 128, Tq and Tk < 2^31,
  * B * H * ceil(max_q / 32) < 2^31.
- * Errors: CSA_ERR_INVALID_ARG for a null q, cu_q, cu_k or o, a null kv or k_rope with Tk > 0, negative
+ * Errors: CSA_ERR_WORKSPACE for a ws that is too small; CSA_ERR_INVALID_ARG for a null q, cu_q, cu_k or o, a null kv or k_rope with Tk > 0, negative
  * sizes, H, dn, dr or dv < 1, a bad dtype, a non-finite scale, or q, kv, k_rope or o not 16-byte aligned;
  * CSA_ERR_UNSUPPORTED outside the limits.
  */
+size_t latent_attn_prefill_workspace_size(int64_t B, int64_t Tq, int64_t Tk, int32_t H, int32_t dn, int32_t dr, int32_t dv,
+                                          int64_t max_q, int32_t dtype);
 int latent_attn_prefill(const void *q, const void *kv, const void *k_rope, const int64_t *cu_q, const int64_t *cu_k, int64_t B,
                         int64_t Tq, int64_t Tk, int32_t H, int32_t dn, int32_t dr, int32_t dv, int64_t max_q, float scale,
-                        int32_t causal, int32_t dtype, void *o, float *lse, void *stream);
+                        int32_t causal, int32_t dtype, void *o, float *lse, void *ws, size_t ws_bytes, void *stream);
 
 /* ----------------------------------------------------------------------------------------- */
 

@@ -455,6 +455,48 @@ def run_prefill(C, nq, nk, H, dims, dtype, causal, seed=0, scale=None, gap=3, si
     return o, lse
 
 
+SPLIT = [([1], [1100], 1), ([256], [5000], 4), ([100, 300], [2500, 900], 2), ([5, 0, 40], [4000, 700, 0], 3), ([130], [20000], 1),
+         ([33, 7], [1, 9000], 2)]
+
+
+@pytest.mark.parametrize("nq,nk,H", SPLIT)
+@pytest.mark.parametrize("causal", [True, False])
+def test_prefill_few_queries_many_keys(C, nq, nk, H, causal):
+    """Keys split over the SMs: a row's parts merged, parts with nothing to see, sequences shorter than the parts."""
+    n = [sum(x) + 3 for x in (nq, nk)]
+    assert C.latent_attn_prefill_workspace_size(len(nq), *n, H, 128, 64, 128, max(nq)) > 0
+    run_prefill(C, nq, nk, H, (128, 64, 128), BF16, causal, seed=H, size=3.0)
+
+
+@pytest.mark.parametrize("scale", [-0.2, 0.0, 20.0])
+def test_prefill_split_scales(C, scale):
+    run_prefill(C, [70], [2000], 2, (128, 64, 128), BF16, True, scale=scale)
+
+
+def test_prefill_split_or_not(C):
+    """With and without a workspace the sums differ in their order alone; a workspace that is too small is refused; what is
+    not finite in a part reaches its rows."""
+    g = rng(3)
+    q, kv, kr = (torch.randn(s, generator=g).to(BF16).cuda() for s in ((40, 2, 192), (4000, 2, 256), (4000, 64)))
+    cq, ck = ints(0, 40), ints(0, 4000)
+    size = C.latent_attn_prefill_workspace_size(1, 40, 4000, 2, 128, 64, 128, 40)
+    o, whole = torch.empty((2, 40, 2, 128), dtype=BF16, device="cuda")
+    lse, whole_lse = torch.empty((2, 40, 2), device="cuda")
+    ws = torch.empty((size,), dtype=torch.uint8, device="cuda")
+    C.latent_attn_prefill(q, kv, kr, cq, ck, 40, 0.1, o=o, lse=lse, workspace=ws)
+    args = [t.data_ptr() for t in (q, kv, kr, cq, ck)] + [1, 40, 4000, 2, 128, 64, 128, 40, 0.1, 1, C.CSA_BF16]
+    st = torch.cuda.current_stream().cuda_stream
+    assert C.lib().latent_attn_prefill(*args, whole.data_ptr(), whole_lse.data_ptr(), None, 0, st) == C.CSA_OK
+    # each is off the formula's result by a rounding of P and of o: two bf16 steps of either, of values below 4
+    assert (o.float() - whole.float()).abs().max() <= 4 * 2 ** -8 * whole.float().abs().max()
+    assert (lse - whole_lse).abs().max() < 1e-5
+    with pytest.raises(C.CsaError):
+        C.latent_attn_prefill(q, kv, kr, cq, ck, 40, 0.1, workspace=ws[:size - 1])
+    kv[3000, 1, :] = float("nan")
+    bad = C.latent_attn_prefill(q, kv, kr, cq, ck, 40, 0.1)
+    assert bad[:, 1].isnan().all() and torch.equal(bad[:, 0], o[:, 0])
+
+
 RAGGED = [([1], [1]), ([128], [128]), ([129, 0, 1, 127], [129, 0, 1, 127]), ([5, 300, 64], [5, 300, 64]),
           ([3, 1, 130, 20], [200, 129, 130, 0]), ([40, 260], [17, 255]), ([0, 0], [4, 0]), ([257], [513])]
 

@@ -66,7 +66,7 @@ def test_decode_refusals(C):
 
 def test_prefill_refusals(C):
     def call(q=f, kv=f, kr=f, cq=f, ck=f, B=2, Tq=8, Tk=8, H=4, dn=128, dr=64, dv=128, mq=8, scale=1.0, dt=1, o=f):
-        return C.lib().latent_attn_prefill(q, kv, kr, cq, ck, B, Tq, Tk, H, dn, dr, dv, mq, scale, 1, dt, o, None, None)
+        return C.lib().latent_attn_prefill(q, kv, kr, cq, ck, B, Tq, Tk, H, dn, dr, dv, mq, scale, 1, dt, o, None, None, 0, None)
     I, U = C.CSA_ERR_INVALID_ARG, C.CSA_ERR_UNSUPPORTED
     for k in ("q", "kv", "kr", "cq", "ck", "o"):
         assert call(**{k: None}) == I
@@ -80,6 +80,17 @@ def test_prefill_refusals(C):
     assert call(Tq=1 << 31) == U and call(Tk=1 << 31) == U
     assert call(B=0) == C.CSA_OK and call(Tq=0) == C.CSA_OK and call(mq=0) == C.CSA_OK
     assert call(Tq=0, Tk=0, kv=None, kr=None) == C.CSA_OK
+
+
+def test_prefill_workspace(C):
+    size = C.latent_attn_prefill_workspace_size
+    one = size(1, 1, 65536, 1, 128, 64, 128, 1)
+    assert one > 0 and size(1, 256, 65536, 1, 128, 64, 128, 256) == one  # by blocks of 256 queries
+    assert size(1, 256, 500, 1, 128, 64, 128, 256) == 0                  # keys too few to split
+    assert size(1, 65536, 65536, 128, 128, 64, 128, 65536) == 0          # blocks enough
+    assert size(1, 1, 65536, 1, 64, 64, 128, 1) == 0 and size(1, 1, 65536, 1, 128, 64, 128, 1, torch.float32) == 0
+    assert size(0, 1, 65536, 1, 128, 64, 128, 1) == 0 and size(1, 1, -5, 1, 128, 64, 128, 1) == 0
+    assert size(2 ** 40, 1, 2 ** 50, 1, 128, 64, 128, 1) == 0
 
 
 def test_binding_refuses_operands_it_would_misread(C):
