@@ -503,6 +503,13 @@ def _launch(fn: str, dev: int, stream, args):
     _check(fn, getattr(_lib, fn)(*args, int(st)))
 
 
+def _stream_current(stream, dev: int):
+    """The named stream as the current one: what a call allocates (outputs, workspaces) belongs to the stream that uses it."""
+    if hasattr(stream, "cuda_stream"):
+        stream = stream.cuda_stream
+    return torch.cuda.stream(torch.cuda.ExternalStream(int(stream), device=dev) if int(stream) else torch.cuda.default_stream(dev))
+
+
 def _on_device(dev: int, f, *args):
     """f(*args) with the operands' device current."""
     if dev < 0 or dev == torch.cuda.current_device():
@@ -540,6 +547,9 @@ def latent_gather(rows: KvRows, cu, n: int | None = None, start=None, pages=None
     rows cu[b] ..; returns (lat [n, R], rope [n, rd]).  With lat and rope None both are allocated with n
     rows of ``dtype``; with one of them given only that one is written."""
     dev = rows.fp8.get_device()
+    if stream is not None and dev >= 0:
+        with _stream_current(stream, dev):
+            return latent_gather(rows, cu, n, start, pages, page_rows, off, lat, rope, dtype)
     r = _rows("rows", rows, dev)
     B, p, mp, pr, of = _row_map(pages, page_rows, off, dev)
     cp, sp = _in("cu", cu, torch.int64, (B + 1,), dev), _opt("start", start, torch.int64, (B,), dev)
@@ -565,6 +575,9 @@ def latent_attn_decode(q, rows: KvRows, pos, scale: float, max_len: int, pages=N
     """Absorbed latent attention of Lq new tokens per sequence, q [B, Lq, H, R + rd] bf16, over the latent
     cache; token j sits at pos[b] + j and sees every position up to its own.  Returns o [B, Lq, H, R]."""
     dev = q.get_device()
+    if stream is not None and dev >= 0:
+        with _stream_current(stream, dev):
+            return latent_attn_decode(q, rows, pos, scale, max_len, pages, page_rows, off, o, lse, workspace)
     r = _rows("rows", rows, dev)
     B, Lq, H, _ = q.shape
     R = r.c - r.rope_dims
@@ -594,6 +607,9 @@ def latent_attn_prefill(q, kv, k_rope, cu_q, cu_k, max_q: int, scale: float, cau
     """Expanded latent attention over packed sequences: q [Tq, H, dn + dr], kv [Tk, H, dn + dv] (a head's
     unrotated key, then its value), k_rope [Tk, dr] shared by the heads.  Returns o [Tq, H, dv]."""
     dev, t, dt = q.get_device(), q.dtype, _float_dtype("q", q)
+    if stream is not None and dev >= 0:
+        with _stream_current(stream, dev):
+            return latent_attn_prefill(q, kv, k_rope, cu_q, cu_k, max_q, scale, causal, o, lse, workspace)
     (Tq, H, dk), (Tk, _, dkv), dr, B = q.shape, kv.shape, k_rope.shape[1], cu_q.shape[0] - 1
     dn = dk - dr
     dv = dkv - dn

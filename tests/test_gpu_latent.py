@@ -721,3 +721,30 @@ def test_a_side_stream_is_used(C):
     C.latent_attn_decode(late, rows, pos, 0.05, 1024, off=off, o=b, workspace=ws, stream=s)
     s.synchronize()
     assert torch.equal(a, ref) and torch.equal(b, ref)
+
+
+@pytest.mark.parametrize("as_handle", [False, True])
+def test_what_a_call_allocates_belongs_to_its_stream(C, as_handle):
+    """Workspaces and outputs of a call on a named stream are not given to the current stream's tensors while it runs."""
+    rows = cache(C, 4096, 512, 64)
+    q = torch.randn((1, 1, 16, 576), generator=rng(1)).to(BF16).cuda()
+    pos, off = ints(4000), ints(0)
+    qp, kv, kr = (torch.randn(s, generator=rng(2)).to(BF16).cuda() for s in ((8, 2, 192), (4000, 2, 256), (4000, 64)))
+    cu, cq, ck = ints(0, 4000), ints(0, 8), ints(0, 4000)
+
+    def calls(stream):
+        return (C.latent_attn_decode(q, rows, pos, 0.05, 4096, off=off, stream=stream),
+                C.latent_attn_prefill(qp, kv, kr, cq, ck, 8, 0.1, stream=stream), *C.latent_gather(rows, cu, n=4000, off=off, stream=stream))
+    ref = calls(None)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(50_000_000)
+    got = calls(s.cuda_stream if as_handle else s)
+    n = [C.latent_attn_decode_workspace_size(1, 1, 16, 512, 4096), C.latent_attn_prefill_workspace_size(1, 8, 4000, 2, 128, 64, 128, 8)]
+    over = [torch.full((k,), 255, dtype=torch.uint8, device="cuda") for k in n for _ in range(3)]  # would be NaN in the workspaces
+    s.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, ref)) and len(over) == 6
+    bare = calls(0)  # the default stream, by its handle
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(bare, ref))
