@@ -285,6 +285,17 @@ def test_decode_splits(C, lens):
     run_decode(C, lens, 8, 1, 512, 64, 64, seed=len(lens))
 
 
+@pytest.mark.parametrize("lens,H,Lq,R,rd", [
+    ([150 + 37 * i for i in range(38)], 128, 1, 512, 64),                 # few parts of many rows: 16 rows at a time
+    ([3 * i for i in range(41)] + [900] * 9, 101, 1, 512, 64),            # of which the last are 5
+    ([260 + 11 * i for i in range(45)], 107, 1, 160, 32),                 # channels that are no whole groups of 128
+    ([20000], 17, 1, 512, 64), ([20000], 3, 3, 96, 16), ([9000], 66, 1, 512, 64),  # many parts: 4 rows at a time, 1 or 2 left
+    ([1200, 2500, 1700, 5, 2900], 5, 1, 512, 64), ([300, 2500, 100], 9, 1, 224, 16),
+    ([1200] * 12, 7, 1, 512, 64)])                                        # parts between the two
+def test_decode_merges(C, lens, H, Lq, R, rd):
+    run_decode(C, lens, H, Lq, R, rd, 64, seed=H)
+
+
 @pytest.mark.parametrize("R", [512, 256])
 def test_decode_many_row_blocks(C, R):
     """More row blocks than lie side by side (40 of 32 rows), and some that do, over cut runs."""
