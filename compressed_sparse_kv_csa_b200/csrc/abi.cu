@@ -663,12 +663,12 @@ int latent_attn_prefill(const void *q, const void *kv, const void *k_rope, const
     const LatentPrefillArgs a{q, kv, k_rope, cu_q, cu_k, B, Tq, Tk, max_q, H, dn, dr, dv, scale, causal ? 1 : 0, o, lse,
                               dev_error_word()};
     if (latent_prefill_tc_eligible(a, dtype)) {
-        LatentKeyParts parts{nullptr, 1};
+        LatentKeyParts parts{nullptr, 0, 1};
         if (ws) {
             const size_t need = latent_prefill_tc_workspace(a);
             if (need && ws_bytes < need + kAlign) return CSA_ERR_WORKSPACE;
+            parts = latent_prefill_tc_parts(a);
             parts.part = reinterpret_cast<float *>((reinterpret_cast<uintptr_t>(ws) + kAlign - 1) / kAlign * kAlign);
-            parts.n = latent_prefill_tc_parts(a);
         }
         note_path(CSA_PATH_LATENT_PREFILL_TC);
         return status_of(launch_latent_prefill_tc(a, parts, S(stream)));

@@ -270,7 +270,8 @@ struct LatentPrefillArgs {
 };
 struct LatentKeyParts {
     float *part; // their partials (latent_part of 256 rows), block after block
-    int n;       // of a block of queries; 1: the keys are not split
+    int whole;   // blocks of queries whose keys are not split
+    int n;       // parts of each of the others; 1: there are none
 };
 
 // The rows of sequence b in a packed array of T rows.
@@ -282,7 +283,7 @@ __device__ __forceinline__ void packed_range(const int64_t *cu, int64_t b, int64
 }
 
 bool latent_prefill_tc_eligible(const LatentPrefillArgs &a, int dtype);
-int latent_prefill_tc_parts(const LatentPrefillArgs &a); // key parts, 1: none
+LatentKeyParts latent_prefill_tc_parts(const LatentPrefillArgs &a);
 size_t latent_prefill_tc_workspace(const LatentPrefillArgs &a);
 cudaError_t launch_latent_prefill_tc(const LatentPrefillArgs &a, const LatentKeyParts &parts, cudaStream_t st);
 cudaError_t launch_latent_prefill_generic(const LatentPrefillArgs &a, int dtype, cudaStream_t st);

@@ -18,7 +18,7 @@
 // (three slots a tile) and value (two) boxes pass through in order, so that the loads run up to 1.6
 // tiles ahead.  Everything arrives by TMA.
 // P is handed over in two halves, and one instruction takes the maximum of three: 16k queries and keys of 16 heads 3%
-// faster than without.  Where query blocks are few their keys are split (latent_prefill_tc_parts).
+// faster than without.  Where query blocks do not fill the SMs to the end, keys are split (latent_prefill_tc_parts).
 // Roles: warps 0-3 and 4-7 softmax, rescale and output of the two query tiles (one row a thread), warp 8
 // TMA, warp 9 MMA.  Per pair of query tiles and tile of keys the tensor cores need 2,560 cycles and the chain S - softmax - P V
 // of each, beside the other's MMAs, 3,800; in long calls the chip's power limits what is left (990 W, 1.5 GHz): 16k
@@ -294,9 +294,12 @@ __device__ __forceinline__ bool mma_role(const Job &j, uint32_t base, uint32_t t
     return true;
 }
 
+// What a grid's blocks are: none of them split, all, or those behind the first.
+enum Keys { kWhole, kSplit, kSome };
+
 // Softmax, rescale and output of query tile t: one row per thread.  Of a part of the keys, the maximum, the sum and O as
 // it is go to the part's record.
-template <bool PARTS> __device__ __forceinline__ bool softmax_role(const LatentPrefillArgs &a, const LatentKeyParts &parts, const Job &j, uint32_t base, uint32_t tmem, int warp, int lane)
+template <Keys KEYS> __device__ __forceinline__ bool softmax_role(const LatentPrefillArgs &a, const LatentKeyParts &parts, const Job &j, uint32_t base, uint32_t tmem, int warp, int lane)
 {
     const uint32_t bars = base + OFF_BAR;
     auto bar = [&](int b) { return bars + 8u * (uint32_t)b; };
@@ -312,7 +315,7 @@ template <bool PARTS> __device__ __forceinline__ bool softmax_role(const LatentP
     const bool turn = a.scale < 0.f;
     const float sl2 = fmaxf(fabsf(a.scale) * kLog2e, 1e-37f);
     float m = -INFINITY, l = 0.f; // maximum in use (scaled, log2 domain), sum
-    const int c0 = PARTS ? j.c0 : 0;
+    const int c0 = KEYS != kWhole ? j.c0 : 0;
     for (int c = 0; c < j.n[t]; ++c) {
         if (!__all_sync(0xffffffffu, mbar_wait(bar(B_S + t), (uint32_t)(c & 1)))) return false;
         tc_fence_after();
@@ -381,9 +384,9 @@ template <bool PARTS> __device__ __forceinline__ bool softmax_role(const LatentP
         if (!__all_sync(0xffffffffu, mbar_wait(bar(B_O + t), 0))) return false;
         tc_fence_after();
     }
-    if constexpr (PARTS) {
+    if (KEYS == kSplit || (KEYS == kSome && blockIdx.x >= (uint32_t)parts.whole)) {
+        float *rec = latent_part<2 * kT>(parts.part, kDv, KEYS == kSplit ? blockIdx.x : blockIdx.x - (uint32_t)parts.whole);
         const int row = t * kT + 32 * (warp & 3) + lane;
-        float *rec = latent_part<2 * kT>(parts.part, kDv, blockIdx.x);
         if (i < j.nq) *reinterpret_cast<float2 *>(rec + 2 * row) = make_float2(l == 0.f ? -INFINITY : m == -INFINITY ? 0.f : m, l);
         if (j.n[t] > 0) {
 #pragma unroll
@@ -428,14 +431,20 @@ template <bool PARTS> __device__ __forceinline__ bool softmax_role(const LatentP
     return true;
 }
 
-template <bool PARTS>
+template <Keys KEYS>
 __global__ void __launch_bounds__(kThreads, 1) latent_prefill_tc_kernel(LatentPrefillArgs a, const __grid_constant__ Maps maps, LatentKeyParts parts)
 {
     extern __shared__ uint8_t smem_raw[];
-    if constexpr (PARTS) cudaTriggerProgrammaticLaunchCompletion(); // the merge may come up
+    if constexpr (KEYS != kWhole) cudaTriggerProgrammaticLaunchCompletion(); // the merge may come up
     Job j;
-    const int64_t block = PARTS ? blockIdx.x / parts.n : blockIdx.x;
-    if (!find_job(a, block, PARTS ? (int)(blockIdx.x % parts.n) : -1, parts.n, j)) return; // no queries here (the same on every thread)
+    int64_t block = blockIdx.x;
+    int part = -1;
+    if (KEYS == kSplit || (KEYS == kSome && block >= parts.whole)) {
+        const uint32_t i = (uint32_t)(KEYS == kSplit ? block : block - parts.whole);
+        part = (int)(i % (uint32_t)parts.n);
+        block = (KEYS == kSplit ? 0 : parts.whole) + i / (uint32_t)parts.n;
+    }
+    if (!find_job(a, block, part, parts.n, j)) return; // no queries here (the same on every thread)
     const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
     uint8_t *sp = smem_raw + (base - raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -451,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_tc_kernel(LatentPr
     bool ok = true;
     if (warp < kTmaWarp) {
         regs_inc<kRegsSoft>();
-        ok = softmax_role<PARTS>(a, parts, j, base, tmem, warp, lane);
+        ok = softmax_role<KEYS>(a, parts, j, base, tmem, warp, lane);
     } else {
         regs_dec<kRegsRest>();
         if (warp == kTmaWarp) ok = tma_role(j, maps, base, lane);
@@ -478,9 +487,9 @@ __global__ void __launch_bounds__(32 * kMergeRows) latent_prefill_merge_kernel(L
     // four rows of eight fours of channels a warp
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int r = (int)(blockIdx.x % kBlocks) * kMergeRows + 4 * (warp >> 2) + (lane & 3), ch = 32 * (warp & 3) + 4 * (lane >> 2);
-    const int64_t block = blockIdx.x / kBlocks;
+    const int64_t block = blockIdx.x / kBlocks; // of those that are split
     Job j;
-    const bool there = find_job(a, block, -1, 1, j) && j.i0 + r < j.nq;
+    const bool there = find_job(a, parts.whole + block, -1, 1, j) && j.i0 + r < j.nq;
     cudaGridDependencySynchronize(); // every block waits: what follows in the stream waits for this kernel alone
     if (!there) return;
     const int64_t step = latent_part_size<2 * kT>(kDv);
@@ -539,27 +548,43 @@ bool latent_prefill_tc_eligible(const LatentPrefillArgs &a, int dtype)
 
 static int64_t query_blocks(const LatentPrefillArgs &a) { return a.B * a.H * ((a.max_q + 2 * kT - 1) / (2 * kT)); }
 
-// Where the query blocks leave at least half of the SMs idle, their keys are split into parts of at least 4 tiles (of a
-// sequence of the average length), as many as the SMs have room for at once.  256 queries of 16 heads after 64k keys: 142
-// us in 9 parts, 914 whole; after 1k: 18.6 in 2, 22.1 whole; 74 blocks after 8k: 88 in 2, 125 whole.
-int latent_prefill_tc_parts(const LatentPrefillArgs &a)
+// Which blocks' keys are split, and into how many parts, so that the SMs are busy to the end: of the blocks behind the last
+// full round of all SMs the keys are cut into the number of parts that takes the least time, by the time of a key tile,
+// what a CTA takes beside its tiles, and what the partials cost to write, read and merge.  The lengths are
+// taken as the average's.  With as many queries as keys, causal blocks differ so much that the short ones fill the last
+// round by themselves: full rounds are then followed by none that is split.
+//   256 queries of 16 heads (16 blocks) after 64k keys: 150 us in 9 parts, 914 whole; after 2k: 20 in 4, 36 whole;
+//   80 blocks after 8k: 116 in 3, 126 whole; 100 blocks: 129 whole, 141 in 4;
+//   2,560 queries of 16 heads after 8k (148 blocks whole, 12 in 12): 147 us, 191 whole;
+//   3 x 1,024 after 4k (148 whole, 44 in 3): 105, 118 whole; 2 x 2,048 after 14k: 487 whole, 505 with 108 blocks in 4.
+LatentKeyParts latent_prefill_tc_parts(const LatentPrefillArgs &a)
 {
-    const int64_t blocks = query_blocks(a), room = blocks > 0 ? device_sms() / blocks : 0, tiles = (a.Tk / a.B + kT - 1) / kT;
-    const int64_t parts = room < tiles / 4 ? room : tiles / 4;
-    return parts < 2 ? 1 : (int)parts;
+    constexpr double kTile = 1.9, kCta = 10, kMerge = 6, kPartial = 0.06; // us
+    const int64_t blocks = query_blocks(a), sms = device_sms(), nk = a.Tk / a.B, nq = a.Tq / a.B;
+    const LatentKeyParts none{nullptr, 0, 1};
+    const int64_t whole = blocks / sms * sms, rest = blocks - whole;
+    if (blocks >= ((int64_t)1 << 31) || rest == 0 || (whole > 0 && 2 * nq > nk) || whole > 8 * sms) return none;
+    const double tiles = (double)(nk > nq ? nk - nq / 2 : nk) / kT;
+    LatentKeyParts best = none;
+    double least = 0.95 * (tiles * kTile + kCta);
+    for (int n = 2; n <= sms && 3.5 * n <= tiles; ++n) {
+        const double rounds = (double)((rest * n + sms - 1) / sms), t = rounds * (tiles / n * kTile + kCta) + kMerge + kPartial * (double)(rest * n);
+        if (t < least) least = t, best.whole = (int)whole, best.n = n;
+    }
+    return best;
 }
 size_t latent_prefill_tc_workspace(const LatentPrefillArgs &a)
 {
-    const int parts = latent_prefill_tc_parts(a);
-    return parts < 2 ? 0 : (size_t)(query_blocks(a) * parts * latent_part_size<2 * kT>(kDv)) * sizeof(float);
+    const LatentKeyParts p = latent_prefill_tc_parts(a);
+    return p.n < 2 ? 0 : (size_t)((query_blocks(a) - p.whole) * p.n * latent_part_size<2 * kT>(kDv)) * sizeof(float);
 }
 
-template <bool PARTS> static cudaError_t launch(const LatentPrefillArgs &a, const Maps &maps, const LatentKeyParts &parts, int64_t ctas, cudaStream_t st)
+template <Keys KEYS> static cudaError_t launch(const LatentPrefillArgs &a, const Maps &maps, const LatentKeyParts &parts, int64_t ctas, cudaStream_t st)
 {
     static std::atomic<bool> done[64];
-    cudaError_t e = prepare_kernel(latent_prefill_tc_kernel<PARTS>, SMEM_ALLOC, kRegs, done);
+    cudaError_t e = prepare_kernel(latent_prefill_tc_kernel<KEYS>, SMEM_ALLOC, kRegs, done);
     if (e != cudaSuccess) return e;
-    latent_prefill_tc_kernel<PARTS><<<(unsigned)ctas, kThreads, SMEM_ALLOC, st>>>(a, maps, parts);
+    latent_prefill_tc_kernel<KEYS><<<(unsigned)ctas, kThreads, SMEM_ALLOC, st>>>(a, maps, parts);
     return cudaGetLastError();
 }
 
@@ -571,11 +596,12 @@ cudaError_t launch_latent_prefill_tc(const LatentPrefillArgs &a, const LatentKey
         return cudaErrorNotSupported;
     const int64_t blocks = query_blocks(a);
     if (blocks >= ((int64_t)1 << 31)) return cudaErrorInvalidValue;
-    if (parts.n < 2) return launch<false>(a, maps, parts, blocks, st);
-    cudaError_t e = launch<true>(a, maps, parts, blocks * parts.n, st);
+    if (parts.n < 2) return launch<kWhole>(a, maps, parts, blocks, st);
+    const int64_t ctas = parts.whole + (blocks - parts.whole) * parts.n;
+    cudaError_t e = parts.whole ? launch<kSome>(a, maps, parts, ctas, st) : launch<kSplit>(a, maps, parts, ctas, st);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{}; // its blocks come up while the parts are written, and wait for them
-    cfg.gridDim = dim3((unsigned)(blocks * (2 * kT / kMergeRows)));
+    cfg.gridDim = dim3((unsigned)((blocks - parts.whole) * (2 * kT / kMergeRows)));
     cfg.blockDim = dim3(32 * kMergeRows);
     cfg.stream = st;
     cudaLaunchAttribute at;

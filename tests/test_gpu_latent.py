@@ -467,7 +467,7 @@ def run_prefill(C, nq, nk, H, dims, dtype, causal, seed=0, scale=None, gap=3, si
 
 
 SPLIT = [([1], [1100], 1), ([256], [5000], 4), ([100, 300], [2500, 900], 2), ([5, 0, 40], [4000, 700, 0], 3), ([130], [20000], 1),
-         ([33, 7], [1, 9000], 2)]
+         ([33, 7], [1, 9000], 2), ([1300], [4100], 30), ([700, 1, 300], [3900, 4000, 8000], 18)]  # the last two: full rounds, then parts
 
 
 @pytest.mark.parametrize("nq,nk,H", SPLIT)
