@@ -141,8 +141,8 @@ __global__ void __launch_bounds__(32 * kWarps) latent_decode_generic_kernel(Late
 // O / l.  Bound by latency, its own (where the run lies takes some 3 us to find) and that of its loads, of which a thread
 // has 8 under way.  Of many parts a CTA takes 4 rows and 128 channels, and up to 4 groups of 128 threads share the
 // parts (1 x 64k keys x 16 heads, 148 parts: 12 us behind the parts' kernel; one group 45).  Of few parts of many rows it
-// takes 16 rows and all channels, four rows a thread (32 x 256 rows in 2 or 3 parts: 16 us; 4 rows a CTA 33; but
-// 64 x 16 rows 13 us where 4 rows a CTA take 6).
+// takes 16 rows and all channels, four rows a thread (32 x 256 rows in 2 or 3 parts: 16 us; 4 rows a CTA 33; the
+// whole call of 64 x 64 rows after 1k to 4k keys 61 us, 70; but of 64 x 16 rows 45, 43).
 constexpr int kMaxParts = 512;
 
 template <class Split, int RB, int ROWS> __global__ void __launch_bounds__(512) latent_merge_kernel(LatentDecodeArgs a)
@@ -344,7 +344,7 @@ template <class Split, int RB> static cudaError_t launch_merge(const LatentDecod
     if (a.grid == a.par) return cudaSuccess; // one CTA, or one group, cuts no run
     if (a.grid > kMaxParts) return cudaErrorInvalidValue;
     const int64_t parts = (a.grid / a.par + a.B - 1) / a.B; // of a run of the average length
-    const bool few = parts <= 8 && a.B * a.Lq * a.H >= 16 * 2 * device_sms(); // and rows enough for all SMs
+    const bool few = parts <= 8 && a.B * a.Lq * a.H >= 16 * device_sms(); // and rows enough for all SMs
     const int rows = few ? 16 : 4, threads = few || parts > 16 ? 512 : parts > 8 ? 256 : 128, R = a.rows.c - a.rows.rope_dims;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(a.B * ((a.Lq * a.H + rows - 1) / rows)), few ? 1u : (unsigned)((R + 127) / 128));
