@@ -4,8 +4,8 @@
 //
 // Both are HBM-bound: append reads 2c bytes (bf16) and writes R + 2 rd + 4 a row, gather the other
 // way round.  A lane holds 8 consecutive channels of a row, so that loads and stores of bf16 are 16 bytes a
-// lane beside its neighbour's.  Measured, 512 + 64 channels in pages of 128: append of 65,536 bf16 rows 38 us
-// (3.2 TB/s; the arithmetic of a row bounds it), gather of 190,000 rows 60 us (5.7 TB/s).
+// lane beside its neighbour's.  Measured, 512 + 64 channels in pages of 128: append of 65,536 bf16 rows 34 us
+// (3.5 TB/s; the arithmetic of a row bounds it), gather of 190,000 rows 60 us (5.7 TB/s).
 #include "latent.cuh"
 
 namespace csa {
@@ -92,11 +92,9 @@ __device__ __forceinline__ uint2 encode8(const float2 (&v)[4], float sc, float i
     return make_uint2(plus0(w[0]), plus0(w[1]));
 }
 
-constexpr int kBatch = 4; // rows that a warp works on at once
-
 // Sums (or maxima) over the warp of four values, one a row: lane l returns that of row 2 (l / 16) + (l / 8) % 2.  Six
 // shuffles for the four.
-template <class Op> __device__ __forceinline__ float reduce4(const float (&v)[kBatch], int lane, Op op)
+template <class Op> __device__ __forceinline__ float reduce(const float (&v)[4], int lane, Op op)
 {
     const bool hi = lane & 16, odd = lane & 8;
     const float a = op(hi ? v[2] : v[0], __shfl_xor_sync(0xffffffffu, hi ? v[0] : v[2], 16));
@@ -106,17 +104,24 @@ template <class Op> __device__ __forceinline__ float reduce4(const float (&v)[kB
     for (int o = 4; o > 0; o >>= 1) c = op(c, __shfl_xor_sync(0xffffffffu, c, o));
     return c;
 }
-__device__ __forceinline__ float of_row(float v, int r) { return __shfl_sync(0xffffffffu, v, 16 * (r >> 1) + 8 * (r & 1)); }
+template <class Op> __device__ __forceinline__ float reduce(const float (&v)[1], int, Op op)
+{
+    float c = v[0];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) c = op(c, __shfl_xor_sync(0xffffffffu, c, o));
+    return c;
+}
+template <int N> __device__ __forceinline__ float of_row(float v, int r) { return N == 1 ? v : __shfl_sync(0xffffffffu, v, 16 * (r >> 1) + 8 * (r & 1)); }
 
-// A warp takes `per` rows, four at once: their loads are in flight together, their places are looked up side by side (a
-// lane each), and what a row needs once -- a root, three divisions -- is computed by different lanes for the four.
-// Lane l holds channels 8 l + 256 k .. + 7, k < NV.  64k rows of 512 + 64 bf16 channels: 442 instructions a row and
-// 63 us one row at a time.
+// A warp takes `per` rows, kBatch = 4 at once (or one, where that is all): their loads are in flight together, their
+// places are looked up side by side (a lane each), what a row needs once -- a root, three divisions -- is computed by
+// different lanes for the four, and no branch between the rows keeps their chains apart.  Lane l holds channels
+// 8 l + 256 k .. + 7, k < NV.  64k rows of 512 + 64 bf16 channels: 63 us one row at a time, 38 with a branch a row, 34.
 //
 // The rotation of pair i at position p is by p * base^(-2i/rd).  The frequency of a lane's pair is computed once for all
 // rows, in 64-bit floating point, as a fraction of a turn of 64 bits; a 64-bit product with the position drops
 // the whole turns by itself, and the sine and cosine of what is left are taken in 32 bits.
-template <typename Tin, int NV> __global__ void __launch_bounds__(256, NV > 2 ? 1 : 2) latent_append_kernel(LatentAppendArgs a, double log_base, int per)
+template <typename Tin, int NV, int kBatch> __global__ void __launch_bounds__(256, NV > 2 ? 1 : 2) latent_append_kernel(LatentAppendArgs a, double log_base, int per)
 {
     const int lane = threadIdx.x & 31;
     const int64_t i0 = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * per;
@@ -150,25 +155,40 @@ template <typename Tin, int NV> __global__ void __launch_bounds__(256, NV > 2 ? 
                 if (r0 + r < cnt && j < R) raw[r][k].load(xr + j);
                 else raw[r][k].zero();
             }
+            pair[r] = make_float2(0.f, 0.f);
             if (r0 + r < cnt && 2 * lane < rd) pair[r] = pair_of(xr + R + 2 * lane);
         }
         int64_t row[kBatch]; // negative: skipped, refused or not there
 #pragma unroll
         for (int r = 0; r < kBatch; ++r) row[r] = r0 + r < cnt ? __shfl_sync(0xffffffffu, my_row, (r0 + r) & 31) : -1;
+        // (no branch a row: the four rows' chains run beside one another)
+        uint64_t p[kBatch];
 #pragma unroll
-        for (int r = 0; r < kBatch; ++r) {
-            const uint64_t p = (uint64_t)__shfl_sync(0xffffffffu, my_pos, (r0 + r) & 31);
-            if (row[r] < 0) continue;
-            for (int k = lane; 2 * k < rd; k += 32) {
-                if (k >= 32) pair[r] = pair_of(x + (int64_t)(r0 + r) * a.out.c + R + 2 * k);
-                if (a.base > 0) {
-                    const uint64_t t = p * (k == lane ? turns : turns_of(k));
-                    float sn, cs;
-                    sincospif((float)(int32_t)(t >> 32) * 4.656612873077393e-10f, &sn, &cs); // half turns, -1 .. 1
-                    pair[r] = make_float2(fmaf(pair[r].x, cs, -pair[r].y * sn), fmaf(pair[r].x, sn, pair[r].y * cs));
-                }
-                *reinterpret_cast<uint32_t *>(a.out.rope + row[r] * rd + 2 * k) =
-                    uint32_t(f32_to_bf16_bits(pair[r].x)) | (uint32_t(f32_to_bf16_bits(pair[r].y)) << 16);
+        for (int r = 0; r < kBatch; ++r) p[r] = (uint64_t)__shfl_sync(0xffffffffu, my_pos, (r0 + r) & 31);
+        auto rotate = [](float2 v, uint64_t t) {
+            float sn, cs;
+            sincospif((float)(int32_t)(t >> 32) * 4.656612873077393e-10f, &sn, &cs); // half turns, -1 .. 1
+            return make_float2(fmaf(v.x, cs, -v.y * sn), fmaf(v.x, sn, v.y * cs));
+        };
+        auto put = [&](int r, int k, float2 v) {
+            if (row[r] >= 0)
+                *reinterpret_cast<uint32_t *>(a.out.rope + row[r] * rd + 2 * k) = uint32_t(f32_to_bf16_bits(v.x)) | (uint32_t(f32_to_bf16_bits(v.y)) << 16);
+        };
+        if (2 * lane < rd) {
+            if (a.base > 0) {
+#pragma unroll
+                for (int r = 0; r < kBatch; ++r) pair[r] = rotate(pair[r], p[r] * turns);
+            }
+#pragma unroll
+            for (int r = 0; r < kBatch; ++r) put(r, lane, pair[r]);
+        }
+        for (int k = lane + 32; 2 * k < rd; k += 32) { // more than 64 rotated channels
+            const uint64_t t = a.base > 0 ? turns_of(k) : 0;
+#pragma unroll
+            for (int r = 0; r < kBatch; ++r) {
+                if (row[r] < 0) continue;
+                const float2 u = pair_of(x + (int64_t)(r0 + r) * a.out.c + R + 2 * k);
+                put(r, k, a.base > 0 ? rotate(u, p[r] * t) : u);
             }
         }
         float2 v[kBatch][NV][4];
@@ -187,9 +207,9 @@ template <typename Tin, int NV> __global__ void __launch_bounds__(256, NV > 2 ? 
                     for (int e = 0; e < 4; ++e) ss = fma2(v[r][k][e], v[r][k][e], ss);
                 s[r] = ss.x + ss.y;
             }
-            const float f = 1.f / sqrtf(reduce4(s, lane, [](float x, float y) { return x + y; }) / (float)R + a.eps);
+            const float f = 1.f / sqrtf(reduce(s, lane, [](float x, float y) { return x + y; }) / (float)R + a.eps);
 #pragma unroll
-            for (int r = 0; r < kBatch; ++r) s[r] = of_row(f, r);
+            for (int r = 0; r < kBatch; ++r) s[r] = of_row<kBatch>(f, r);
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 const int j = 8 * (lane + 32 * k);
@@ -210,20 +230,27 @@ template <typename Tin, int NV> __global__ void __launch_bounds__(256, NV > 2 ? 
 #pragma unroll
                 for (int e = 0; e < 4; ++e) s[r] = fmaxf(s[r], fmaxf(fabsf(v[r][k][e].x), fabsf(v[r][k][e].y)));
         }
-        float my_sc = __fdiv_rn(reduce4(s, lane, [](float x, float y) { return fmaxf(x, y); }), 448.f);
+        float my_sc = __fdiv_rn(reduce(s, lane, [](float x, float y) { return fmaxf(x, y); }), 448.f);
         if (!(my_sc > 0.f)) my_sc = 1.f;
         const float my_inv = 1.f / my_sc;
         const bool plain = __all_sync(0xffffffffu, my_sc > 8.0779357e-28f && my_sc < 1.2379400e27f); // 2^-90 .. 2^90
+        uint2 code[kBatch][NV];
 #pragma unroll
         for (int r = 0; r < kBatch; ++r) {
-            const float sc = of_row(my_sc, r), inv = of_row(my_inv, r);
+            const float sc = of_row<kBatch>(my_sc, r), inv = of_row<kBatch>(my_inv, r);
+#pragma unroll
+            for (int k = 0; k < NV; ++k) code[r][k] = encode8(v[r][k], sc, inv, plain);
+            s[r] = sc;
+        }
+#pragma unroll
+        for (int r = 0; r < kBatch; ++r) {
             if (row[r] < 0) continue;
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 const int j = 8 * (lane + 32 * k);
-                if (j < R) *reinterpret_cast<uint2 *>(a.out.fp8 + row[r] * R + j) = encode8(v[r][k], sc, inv, plain);
+                if (j < R) *reinterpret_cast<uint2 *>(a.out.fp8 + row[r] * R + j) = code[r][k];
             }
-            if (lane == 0) a.out.scale[row[r]] = sc;
+            if (lane == 0) a.out.scale[row[r]] = s[r];
         }
     }
 }
@@ -322,13 +349,15 @@ template <typename Tin> static void append(const LatentAppendArgs &a, cudaStream
 {
     // as many rows a warp as make one wave of 16 warps an SM, at most 32 (a lane looks up each)
     const int64_t warps = 16 * (int64_t)device_sms(), p = (a.n + warps - 1) / warps;
-    const int per = p < kBatch ? (int)p : p > 32 ? 32 : (int)(p + kBatch - 1) / kBatch * kBatch;
+    const int per = p < 2 ? 1 : p > 32 ? 32 : (int)(p + 3) / 4 * 4;
     const unsigned grid = (unsigned)((a.n + 8 * per - 1) / (8 * per));
     const double lb = a.base > 0 ? log(a.base) : 0.0;
     const int R = a.out.c - a.out.rope_dims;
-    if (R <= 256) latent_append_kernel<Tin, 1><<<grid, 256, 0, st>>>(a, lb, per);
-    else if (R <= 512) latent_append_kernel<Tin, 2><<<grid, 256, 0, st>>>(a, lb, per);
-    else latent_append_kernel<Tin, 4><<<grid, 256, 0, st>>>(a, lb, per);
+    auto run = [&](auto kernel) { kernel<<<grid, 256, 0, st>>>(a, lb, per); };
+    if (per == 1) // (64 rows: 4.0 us, for four at once 6.8)
+        R <= 256 ? run(latent_append_kernel<Tin, 1, 1>) : R <= 512 ? run(latent_append_kernel<Tin, 2, 1>) : run(latent_append_kernel<Tin, 4, 1>);
+    else
+        R <= 256 ? run(latent_append_kernel<Tin, 1, 4>) : R <= 512 ? run(latent_append_kernel<Tin, 2, 4>) : run(latent_append_kernel<Tin, 4, 4>);
 }
 
 cudaError_t launch_latent_append(const LatentAppendArgs &a, int in_dtype, cudaStream_t st)
