@@ -8,7 +8,7 @@ import torch
 import _latent_ref as L
 
 pytestmark = pytest.mark.gpu
-BF16, F32, I64, I32 = torch.bfloat16, torch.float32, torch.int64, torch.int32
+BF16, F32, I64, I32, I16 = torch.bfloat16, torch.float32, torch.int64, torch.int32, torch.int16
 V_STEP = 2.0 ** -8  # half a step of the decode kernel's probabilities: 8 bits in two terms of 4 (on the tensor cores)
 NAN8 = 0x7f            # the E4M3 code of NaN
 
@@ -164,6 +164,30 @@ def test_append_many_rows(C):
     for i in range(0, n, 4000):
         C.latent_append(x[i:i + 4000], pos[i:i + 4000], b, g=gain, base=10000.0, seq=seq[i:i + 4000], off=off)
     assert torch.equal(a.fp8, b.fp8) and torch.equal(a.rope, b.rope) and torch.equal(a.scale, b.scale)
+
+
+@pytest.mark.parametrize("R,rd", [(512, 64), (32, 16), (240, 32), (1024, 256), (272, 96)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("norm,base", [(True, 10000.0), (False, 0.0)])
+@pytest.mark.parametrize("n", [2500, 5003])
+def test_append_several_rows_a_warp(C, R, rd, dtype, norm, base, n):
+    """Rows that a warp takes side by side, skipped, refused and odd ones among them: those of calls whose warps take one."""
+    g = rng(n + R)
+    x = (torch.randn((n, R + rd), generator=g) * 3).to(dtype).cuda()
+    x[7, 5], x[11, 0], x[13, :R], x[14, :R], x[15, :R] = float("nan"), float("inf"), 0.0, 1e-38, 1e30
+    pos = torch.randperm(n, generator=g).cuda()
+    pos[3::97], pos[5::101] = -1, 1 << 40  # skipped, refused
+    seq, off = torch.zeros((n,), dtype=I32, device="cuda"), ints(0)
+    gain = (1 + 0.1 * torch.randn((R,), generator=g)).cuda() if norm else None
+    a, b = C.KvRows.empty(n, R + rd, rd, "cuda"), C.KvRows.empty(n, R + rd, rd, "cuda")
+    for t in (a, b):
+        t.fp8.fill_(0x55), t.rope.fill_(7.0), t.scale.fill_(7.0)
+    C.latent_append(x, pos, a, g=gain, base=base, seq=seq, off=off)
+    assert C.csa_device_error() == C.CSA_DEVERR_INDEX
+    for i in range(0, n, 500):
+        C.latent_append(x[i:i + 500], pos[i:i + 500], b, g=gain, base=base, seq=seq[i:i + 500], off=off)
+    assert C.csa_device_error() == C.CSA_DEVERR_INDEX
+    assert torch.equal(a.fp8, b.fp8) and torch.equal(a.rope.view(I16), b.rope.view(I16)) and torch.equal(a.scale.view(I32), b.scale.view(I32))
 
 
 def test_append_refused_rows(C):
