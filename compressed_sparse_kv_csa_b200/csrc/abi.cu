@@ -641,7 +641,8 @@ int latent_attn_decode(const void *q, const csa_kv_rows *rows, const int64_t *po
 size_t latent_attn_prefill_workspace_size(int64_t B, int64_t Tq, int64_t Tk, int32_t H, int32_t dn, int32_t dr, int32_t dv,
                                           int64_t max_q, int32_t dtype)
 {
-    if (B < 1 || B >= ((int64_t)1 << 31) || Tq < 1 || Tk < 1 || H < 1 || H > 128 || max_q < 1) return 0;
+    const int64_t most = (int64_t)1 << 31;
+    if (B < 1 || B >= most || Tq < 1 || Tq >= most || Tk < 1 || Tk >= most || H < 1 || H > 128 || max_q < 1) return 0;
     LatentPrefillArgs a{};
     a.B = B, a.Tq = Tq, a.Tk = Tk, a.H = H, a.dn = dn, a.dr = dr, a.dv = dv, a.max_q = max_q < Tq ? max_q : Tq;
     const size_t need = latent_prefill_tc_eligible(a, dtype) ? latent_prefill_tc_workspace(a) : 0;

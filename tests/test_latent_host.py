@@ -90,7 +90,8 @@ def test_prefill_workspace(C):
     assert size(1, 65536, 65536, 128, 128, 64, 128, 65536) == 0          # blocks enough
     assert size(1, 1, 65536, 1, 64, 64, 128, 1) == 0 and size(1, 1, 65536, 1, 128, 64, 128, 1, torch.float32) == 0
     assert size(0, 1, 65536, 1, 128, 64, 128, 1) == 0 and size(1, 1, -5, 1, 128, 64, 128, 1) == 0
-    assert size(2 ** 40, 1, 2 ** 50, 1, 128, 64, 128, 1) == 0
+    assert size(2 ** 40, 1, 2 ** 50, 1, 128, 64, 128, 1) == 0 and size(1, 2 ** 62, 65536, 128, 128, 64, 128, 2 ** 62) == 0
+    assert size(2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1, 128, 128, 64, 128, 2 ** 31 - 1) == 0
 
 
 def test_binding_refuses_operands_it_would_misread(C):
