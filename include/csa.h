@@ -461,8 +461,8 @@ int latent_gather(const csa_kv_rows *rows, const int64_t *cu, const int64_t *sta
  *   max_len  host-side bound of the positions (sizes the split)
  *   ws       workspace of latent_attn_decode_workspace_size(...) bytes, queried with the device
  *            current; calls that may overlap (two streams, two captured graphs) need one each
- * A sequence's tokens are summed in an order that depends on the batch's lengths and the device's SM
- * count, not on timing: the same call gives the same bits.
+ * A sequence's tokens are summed in an order that depends on the batch's lengths, max_len and the
+ * device's SM count, not on timing: the same call gives the same bits.
  * Limits: R a multiple of 32 and <= 512, rd <= 128, H <= 128, Lq <= 64, max_len <= 2^30, B <= 2^18.
  * Errors: CSA_ERR_INVALID_ARG for a null q, rows, pos or o, B < 0, Lq or H < 1, max_len < 0, a
  * non-finite scale, q or o not 16-byte aligned, a bad page table or rows as above;
