@@ -392,6 +392,7 @@ static __device__ __forceinline__ bool tma_role(const LatentDecodeArgs &a, const
             } else if (whole) {
 #pragma unroll
                 for (int k = 0; k < kKT / 32; ++k) sts1(sc + 4u * (uint32_t)(32 * k + lane), __float_as_uint(sc_now[k]));
+                __syncwarp(); // every lane's scales before the one arrival that stands for them
                 if (elect_one()) {
                     mbar_arrive_expect_tx(full, (uint32_t)kKT * 640u);
                     tma_load_3d(st, &M.lat, 0, row0, 0, full);
