@@ -11,9 +11,14 @@
 // With s the scale of a key's row, S_n = sum_r (q 2^k)_r code_r and S_r = sum_r (q 2^k)_r rope_r,
 //   z = (S_n s + S_r) scale log2e 2^-k,  p = 2^(z - ref),  l = sum p,  v = p s,  O = sum v code
 // and o = O / l.  A row's ref is kept so that its v stay in E4M3's range: it is moved (and O and l
-// rescaled) when a tile's largest v leaves it at the top (448), or falls below 1/16 while what is
-// still to come could matter beside what has been summed: behind a key that outweighs all others the
-// reference comes down again, and the many small ones keep their 8 bits.
+// rescaled) when a tile's v leave it at the top, and when they are so small that the 2^-14 which rounding may take
+// off each comes to more than 2^-9 of the row's sum of v.  With a sum of kLost / kAllowed a key (4 for 128
+// keys) a tile's loss is within that by itself, below it is added up and held against the sum so far.  So behind
+// a key that outweighs all others the reference comes down again, as far as the many small ones matter beside
+// it: an output is off by at most 2^-8 of its terms and 2^-8 of the mean of 448 s, weighted by p.  A key
+// whose codes are all zero would spoil that -- its scale stands for nothing, and is 1 as such rows are written
+// -- so its v is taken as 0 (of 4,096 keys one without a value and e^12 above the others: 0.74 of the output's norm was
+// lost with its scale).
 //
 // A work item's rows are RB = 32 or 64 (head, token) pairs.  The MMAs are bound by what they read of shared memory,
 // 128 bytes a cycle, behind 46 cycles each for the issue; those with M = 64 are weight-stationary (tcgen05.mma.ws),
@@ -29,7 +34,7 @@
 //     4 x 1M keys x 64 rows in a loop of seconds 0.79 ms, so 0.77 ms); S_r with M = 64; O from hi, then from lo.
 //     2,300 cycles a tile: the chain load (2,000 cycles) - S (1,200) - softmax (1,700) - O (1,200) over the stages.
 //     At that rate the chip is at its power limit too (990 W, 1.5 GHz).
-// One exchange a tile, of the rows' largest v, lets the softmax warps decide alike whether a reference moves.
+// One exchange a tile, of the threads' sums of a row's v, lets the softmax warps decide alike whether a reference moves.
 //
 // Roles: warps 0-7 softmax and output; warp 8 copies the keys by TMA, in boxes of a page or of a tile, and warp 9
 // brings the tiles after into L2 (with pages that no box fits, both copy by cp.async); warp 10 MMA.  Rows that are
@@ -53,8 +58,13 @@ constexpr int kSoftThreads = 256, kProdWarp0 = 8, kMmaWarp = 10, kThreads = 384;
 constexpr int kRegs = 168, kRegsSoft = 192, kRegsRest = 120;
 static_assert(256 * kRegsSoft + 128 * kRegsRest <= kThreads * kRegs, "register split");
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr uint32_t kNoKey = 0xffffffffu; // in place of a row's scale: the key is not to be seen
-constexpr float kTop = 448.f, kLow = 1.f / 16.f, kSmallestScale = 7.8886090522101181e-31f; // 2^-100
+constexpr uint32_t kNoKey = 0xbf800000u; // -1 in place of a row's scale (scales are positive): the key is not to be seen
+constexpr float kTop = 448.f, kSmallestScale = 7.8886090522101181e-31f; // 2^-100
+constexpr float kLost = 6.103515625e-5f;         // 2^-14: what rounding may take off a small v
+constexpr float kAllowed = 1.f / 512.f;          // share of a row's sum of v that this may come to
+constexpr float kMostP = 3.2451855365842673e32f; // 2^108, of a thread's p in a tile; a row's sum of p stays in fp32's range
+constexpr float kAbove = 2.f;                    // a tile's largest v is 4 to 8 when it sets the reference
+constexpr float kMostL = 104.f;                 // log2 of a row's sum of p that a reference may be brought down to
 
 template <bool F8, bool WS = true> __device__ __forceinline__ void mma(uint32_t d, Desc a, Desc b, uint32_t idesc, uint32_t accumulate)
 {
@@ -233,8 +243,8 @@ static constexpr uint32_t OFF_K = kPBufs * kPTile;           // stages of 5 slic
 static constexpr uint32_t OFF_Q = OFF_K + kStages * kStage;
 static constexpr uint32_t OFF_EX = OFF_Q + kQRope + 8192;       // after q: 4 slices (hi and lo rows), the rotated channels
 static constexpr uint32_t OFF_SC = OFF_EX + kExch;              // parts of scores that change hands
-static constexpr uint32_t OFF_XCH = OFF_SC + kStages * kKT * 4; // [2 buffers][4 key quarters][rows]
-static constexpr uint32_t OFF_BAR = OFF_XCH + 2 * 4 * kRB * 4;
+static constexpr uint32_t OFF_XCH = OFF_SC + kStages * kKT * 4; // [4 places][4 key quarters][rows]
+static constexpr uint32_t OFF_BAR = OFF_XCH + 4 * 4 * kRB * 4;
 static constexpr uint32_t OFF_AT = OFF_BAR + 160; // where the CTA's walk begins (4 x int64)
 static constexpr uint32_t OFF_TMEM = OFF_AT + 32;
 static constexpr uint32_t SMEM_ALLOC = OFF_TMEM + 64 + 1024;
@@ -685,7 +695,7 @@ static __device__ __forceinline__ void store_queries(const LatentDecodeArgs &a, 
 //   an exchange the whole scores of 16 keys each.
 //   Otherwise lane l has row 32 g + l, warps with half 0 its hi and with half 1 its lo part for all keys; they exchange what
 //   the other finishes, and hold the whole scores of the quarter's 16 keys.
-static __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, const Ctx &c, Walk walk, int warp, int lane)
+static __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, const Maps &M, const Ctx &c, Walk walk, int warp, int lane)
 {
     const int g = warp & 1, half = (warp >> 1) & 1, sub = warp >> 2, kq = 2 * half + sub;
     const int part = kStacked ? lane >> 4 : 0, r16 = lane & 15, row = kStacked ? 16 * g + r16 : 32 * g + lane;
@@ -716,6 +726,23 @@ static __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, c
     auto row_sum = [&](float v) {
         if constexpr (kStacked) v += other_part(v);
         return v;
+    };
+    // Bit e: key e of this thread's has no value -- a scale of 1 and no code but +0 and -0.  The warp looks at the quarter's
+    // scales, a lane each, and together at the codes of the rows that may be such.
+    auto no_value = [&](uint32_t st, uint32_t sc) {
+        constexpr uint32_t kKeys = kKT / 4;
+        float x;
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(sc + 4u * ((uint32_t)lane % kKeys)) : "memory");
+        uint32_t none = __ballot_sync(0xffffffffu, x == 1.f);
+#pragma unroll 1
+        for (uint32_t left = none; left; left &= left - 1) {
+            const uint32_t i = (uint32_t)__ffs(left) - 1, j = kKeys * (uint32_t)kq + i % kKeys, e = (uint32_t)lane;
+            uint32_t c[4];
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3])
+                         : "r"(st + (e >> 3) * M.slice + (j >> 3) * M.group + (j & 7u) * 128u + 16u * (e & 7u)) : "memory");
+            if (__any_sync(0xffffffffu, ((c[0] | c[1] | c[2] | c[3]) & 0x7f7f7f7fu) != 0)) none &= ~(left & (0u - left));
+        }
+        return none >> (16 * part);
     };
     LatentRun run, next_run;
     uint32_t n = 0;
@@ -807,15 +834,17 @@ static __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, c
         float other[4];
         const int rr = run.rb * kRB + row, n_rows = a.Lq * a.H;
         const bool valid = rr < n_rows;
+        constexpr float kFew = kLost / kAllowed * kKT;
         const int64_t seen = valid ? latent_visible(a, run.b, rr / a.H) : 0;
         const int64_t seen_least = latent_visible(a, run.b, run.rb * kRB / a.H); // by every row of the block
-        float vs = 0.f;                    // sum of v over this thread's keys
+        float vs = 0.f, vs_row = 0.f;      // sum of v over this thread's keys; and over the row's, at least
+        float spent = 0.f;                 // what rounding may have taken off it
         bool begun = seen <= run.t0 * kKT;  // the row has a reference, or needs none here
         for (int64_t t = run.t0; t < run.t1; ++t, ++n) {
             const uint32_t buf = n & 1;
             if (!__all_sync(0xffffffffu, mbar_wait(c.bar(B_KFULL + n % kStages), (n / kStages) & 1))) return false;
             float2 z[8], s[8], v[8];
-            bool odd = (t + 1) * kKT > seen_least; // some key may not be seen by some row
+            bool odd = false; // some key may not be seen by some row
             const uint32_t sc = c.base + OFF_SC + (n % kStages) * kKT * 4 + (kStacked ? 128u : 64u) * (uint32_t)kq;
             if constexpr (kStacked) {
                 float2 sn[16], sr[16], sk[16];
@@ -824,7 +853,7 @@ static __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, c
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     s[e] = part ? sk[8 + e] : sk[e];
-                    odd |= __float_as_uint(s[e].x) == kNoKey || __float_as_uint(s[e].y) == kNoKey;
+                    odd |= fabsf(s[e].x) == 1.f || fabsf(s[e].y) == 1.f;
                 }
                 if (!__all_sync(0xffffffffu, mbar_wait(c.bar(B_S + buf), (n >> 1) & 1))) return false;
                 tc_fence_after();
@@ -844,7 +873,7 @@ static __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, c
 #pragma unroll
                 for (int e = 0; e < 4; ++e) lds4(sc + 16u * e, s[2 * e], s[2 * e + 1]);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) odd |= __float_as_uint(s[e].x) == kNoKey || __float_as_uint(s[e].y) == kNoKey;
+                for (int e = 0; e < 8; ++e) odd |= fabsf(s[e].x) == 1.f || fabsf(s[e].y) == 1.f;
                 if (!__all_sync(0xffffffffu, mbar_wait(c.bar(B_S + buf), (n >> 1) & 1))) return false;
                 tc_fence_after();
                 // this warp has hi or lo of all 64 keys, and gives the warp with the other part what that one has to finish
@@ -864,28 +893,30 @@ static __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, c
 #pragma unroll
                 for (int e = 0; e < 8; ++e) z[e] = fma2(add2(sn[e], give[e]), s[e], z[e]);
             }
+            odd |= (t + 1) * kKT > seen_least;
             uint32_t open = 0xffffu; // bit e: key e is seen
-            if (odd) {
+            if (__any_sync(0xffffffffu, odd)) {
                 const int n_seen = (int)max((int64_t)0, min((int64_t)16, seen - (t * kKT + key)));
                 open = (1u << n_seen) - 1u;
+                const uint32_t none = no_value(c.stage(n), sc); // a key without a value has its share of l, and its v is 0
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     if (__float_as_uint(s[e].x) == kNoKey) open &= ~(1u << (2 * e)), s[e].x = 0.f;
                     if (__float_as_uint(s[e].y) == kNoKey) open &= ~(2u << (2 * e)), s[e].y = 0.f;
                 }
-            }
-            if (odd) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) { // an unseen key's score: finite, whatever it was
+                for (int e = 0; e < 8; ++e) {
+                    // an unseen key's score: finite, whatever it was
                     if (!(open >> (2 * e) & 1u)) z[e].x = 0.f;
                     if (!(open >> (2 * e) & 2u)) z[e].y = 0.f;
+                    if (none >> (2 * e) & 1u) s[e].x = 0.f;
+                    if (none >> (2 * e) & 2u) s[e].y = 0.f;
                 }
             }
-            float top, pt, vt;
+            float pt, vt;
             auto weigh = [&]() {
                 const float2 mul = make_float2(cq, cq), sub2 = make_float2(-ref, -ref);
                 float2 ps = make_float2(0.f, 0.f), ws = ps;
-                top = 0.f;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     float2 p = fma2(z[e], mul, sub2);
@@ -898,7 +929,6 @@ static __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, c
                     ps = add2(ps, p);
                     v[e] = mul2(p, s[e]);
                     ws = add2(ws, v[e]);
-                    top = fmaxf(top, fmaxf(v[e].x, v[e].y));
                 }
                 pt = ps.x + ps.y;
                 vt = ws.x + ws.y;
@@ -914,40 +944,56 @@ static __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, c
             };
             // weigh with the reference as it is, and again if that turns out to move; a run's first tile sets it first
             uint32_t hi[4], lo[4];
-            bool set = true, raise = true;
-            float row_top = 0.f;
+            bool move = true, set = true; // the row's reference; that of some row of the warp
+            float least = -INFINITY;      // lower bound of the reference
             if (t > run.t0) {
                 weigh();
-                // a row without a reference, or whose p leave fp32 (scales far below those that it was set by), takes one
-                top = begun && !(pt > 1e37f) ? top : INFINITY;
-                put_part(buf, row_max(top));
+                // the largest sum of v in a thread of the row, in place of the largest v.  A row without a reference, or whose p
+                // grow too large (scales far below those that it was set by), takes one
+                put_part(buf, row_max(begun && !(pt > kMostP) ? vt : INFINITY));
                 split16<!kStacked>(v, kStacked ? 16.f : 1.f, hi, lo); // while the others arrive; seldom in vain
                 if (!rows.wait()) return false;
                 get(buf, other);
-                row_top = max4(other);
-                raise = row_top > kTop;
-                set = __any_sync(0xffffffffu, raise || (row_top < kLow && row_top > 1e-30f)); // (alike in the warps of the rows)
+                const float most = max4(other), some = sum4(other); // (the tile's sum, or at least half of it)
+                const bool raise = most > kTop;
+                // What rounding may take off this tile's v counts as spent where they are few; with kFew or more, it is at
+                // most kAllowed of them.
+                const bool few = some < kFew;
+                const float lost = few ? fminf(kStacked ? 2.f * some : some, kLost * kKT) : 0.f;
+                if (!raise) vs_row += some;
+                spent += lost;
+                bool low = few && spent > kAllowed * vs_row;
+                set = __any_sync(0xffffffffu, raise || low); // (alike in the warps of the rows)
+                if (set && __any_sync(0xffffffffu, low)) {
+                    if (!put(2, row_sum(vs))) return false;
+                    get(2, other);
+                    vs_row = sum4(other);
+                    low = few && spent > kAllowed * vs_row;
+                    if (__any_sync(0xffffffffu, low)) { // the sum of p, which keys without a value may make large, has to stay finite
+                        if (!put(buf, row_sum(l))) return false;
+                        get(buf, other);
+                        least = ref + rintf(__log2f(sum4(other))) - kMostL;
+                        low = some < 4.f * kFew && 4.f * spent > kAllowed * vs_row; // rows that are near it come along
+                        if (low) spent -= lost;
+                    }
+                    set = __any_sync(0xffffffffu, raise || low);
+                }
+                move = raise || low;
             }
             if (set) {
-                const uint32_t place = t == run.t0 ? buf : buf ^ 1;
-                if (!put(place, largest())) return false;
-                get(place, other);
+                if (!put(3, largest())) return false;
+                get(3, other);
                 const float zt = max4(other);
-                bool move = raise;
-                if (t > run.t0) { // low: what is still to come against what is summed
-                    if (!put(buf, row_sum(vs))) return false;
-                    get(buf, other);
-                    const float left = (float)(run.t1 - t) * kKT;
-                    move = raise || (row_top < kLow && row_top > 1e-30f && left * row_top > sum4(other) * (1.f / 256.f));
-                }
                 float f = 1.f;
                 if (move && zt > -INFINITY) {
-                    const float next = rintf(zt) - 3.f; // a whole number: O and the sums move by an exact power of two
+                    const float next = fmaxf(floorf(zt) - kAbove, least); // a whole number: O and the sums move by an exact power of two
                     f = begun ? ex2(ref - next) : 0.f;
                     ref = next;
                     begun = true;
                     l *= f;
                     vs *= f;
+                    vs_row *= f;
+                    spent *= f;
                 }
                 if (t > run.t0 && __any_sync(0xffffffffu, f != 1.f)) { // O of the tiles before this one
                     if (!__all_sync(0xffffffffu, mbar_wait(c.bar(B_KEMPTY + (n - 1) % kStages), ((n - 1) / kStages) & 1))) return false;
@@ -1020,7 +1066,7 @@ static __device__ __forceinline__ void run(const LatentDecodeArgs &a, const Maps
     bool ok = true;
     if (warp < kProdWarp0) {
         regs_inc<kRegsSoft>();
-        ok = softmax_role(a, c, walk, warp, lane);
+        ok = softmax_role(a, maps, c, walk, warp, lane);
     } else {
         regs_dec<kRegsRest>();
         if (warp == kMmaWarp) {

@@ -24,6 +24,139 @@ def ints(*v):
     return torch.tensor(v, dtype=I64, device="cuda")
 
 
+# ------------------------------------------------------------------------------------------
+# keys that outweigh the others
+# ------------------------------------------------------------------------------------------
+
+def check_weights(C, lat, score, H, R=512, B=160, lat_q=2.0 ** -10, pages=False, turn=False):
+    """Decode of B sequences that all attend the rows (lat, and a score that the first rotated channel carries), with
+    queries whose latent part is small, against the formula: one sequence lies in a CTA or two, so that a CTA walks through
+    every kind of tile.  A sum over weights w = p * scale is held to 2^-8 of every term, or 2^-8 of the
+    weighted mean of the rows' largest entries (include/csa.h); scores are sums of R + 64 products in fp32."""
+    n = len(lat)
+    x = torch.cat([lat, torch.zeros((n, 64))], 1)
+    x[:, R] = score
+    rows = C.KvRows.empty(n, R + 64, 64, "cuda")
+    C.csa_quantize_kv(x.cuda(), rows)
+    q = torch.randn((1, 1, H, R + 64), generator=rng(7)) * lat_q
+    q[..., R:] = 0
+    q[..., R] = -1.0 if turn else 1.0
+    q = q.to(BF16).cuda()
+    scale = -1.0 if turn else 1.0
+    kw = dict(off=torch.zeros((B,), dtype=I64, device="cuda"))
+    if pages:
+        assert n % 128 == 0
+        kw = dict(pages=torch.arange(n // 128, dtype=I32, device="cuda").repeat(B, 1), page_rows=128)
+    pos = torch.full((B,), n - 1, dtype=I64, device="cuda")
+    lse = torch.empty((B, 1, H), device="cuda")
+    o = C.latent_attn_decode(q.expand(B, -1, -1, -1).contiguous(), rows, pos, scale, n, lse=lse, **kw)
+    assert C.csa_device_error() == 0
+    l, r = (t.cuda() for t in L.dequant(rows.fp8, rows.rope, rows.scale))
+    key, qd = torch.cat([l, r], 1), q[0, 0].to(L.F64)
+    z = qd @ key.T * scale
+    ref_lse = z.logsumexp(1)
+    p = (z - ref_lse[:, None]).exp()
+    ref, size, top = p @ l, p @ l.abs(), p @ l.abs().amax(1)
+    dz = (R + 64 + 8) * 2.0 ** -24 * (qd.abs() @ key.abs().T).amax(1)
+    fp32 = 2 * dz + (n + 8) * 2.0 ** -24 + 2.0 ** -20
+    tol = 2.0 ** -8 * ref.abs() + (2.0 ** -8 + fp32)[:, None] * size + 2.0 ** -8 * top[:, None] + 1e-30
+    err = (o[:, 0].to(L.F64) - ref).abs()
+    assert torch.isfinite(o).all() and torch.isfinite(lse).all()
+    assert (err <= tol).all(), (float((err / tol).max()), float(err.norm() / ref.norm() / B ** 0.5))
+    assert ((lse[:, 0].to(L.F64) - ref_lse).abs() <= dz + (n + 8) * 2.0 ** -24 + 2.0 ** -19 + 2.0 ** -22 * ref_lse.abs()).all()
+    return ref, p
+
+
+def values(n, R=512, seed=1, mean=1.0, std=0.1):
+    return mean + std * torch.randn((n, R), generator=rng(seed))
+
+
+@pytest.mark.parametrize("H", [16, 64])
+@pytest.mark.parametrize("first,middle", [(11.5, 7.25), (12.0, 6.75), (11.0, 7.75), (12.0, 0.0), (16.0, 9.0)])
+def test_decode_small_weights_beside_a_heavy_key(C, H, first, middle):
+    """A first key far above the rest, then a key in 128 that is above its neighbours: what the neighbours add up to (up to
+    12% of the sum here) is held to the same bound as any."""
+    n = 16384
+    score = torch.zeros((n,))
+    score[5::128] = middle
+    score[0] = first
+    _, p = check_weights(C, values(n), score, H)
+    light = p[:, score == 0].sum(1)
+    if first < 16:
+        assert (light > 0.025).all()  # dropping them would be seen
+
+
+@pytest.mark.parametrize("H", [16, 64])
+@pytest.mark.parametrize("std", [0.0, 1.0, 3.0])
+def test_decode_spread_scores(C, H, std):
+    n = 8192
+    check_weights(C, values(n, std=1.0, mean=0.3), std * torch.randn((n,), generator=rng(3)), H, pages=True)
+
+
+@pytest.mark.parametrize("H", [16, 64])
+@pytest.mark.parametrize("slope", [-0.004, 0.004])
+def test_decode_scores_that_fall_or_rise(C, H, slope):
+    n = 8192
+    check_weights(C, values(n), torch.arange(n) * slope, H, pages=True, turn=True)
+
+
+@pytest.mark.parametrize("H", [16, 64, 7])
+@pytest.mark.parametrize("at,score", [([2], 12.0), ([2, 3, 200, 3999], 12.0), ([0], 60.0), (list(range(0, 4000, 3)), 20.0), ([3000], 90.0)])
+@pytest.mark.parametrize("pages", [False, True])
+def test_decode_heavy_keys_without_a_value(C, H, at, score, pages):
+    """Keys whose latent part is zero (stored with a scale of 1) take their share of the sum of weights and leave the others'
+    outputs as exact as without them."""
+    n = 4096
+    lat = values(n, mean=0.0, std=1.0)
+    s = torch.zeros((n,))
+    lat[at], s[at] = 0.0, score
+    check_weights(C, lat, s, H, lat_q=2.0 ** -6, pages=pages)
+
+
+@pytest.mark.parametrize("H", [16, 64])
+def test_decode_rows_of_minus_zeros(C, H):
+    """Rows without a value that hold codes of -0 (as +0) and a scale of 1."""
+    n, B = 1000, 160
+    rows = C.KvRows.empty(n, 576, 64, "cuda")
+    x = torch.randn((n, 576), generator=rng(4))
+    x[:, 512:] = 0
+    x[3::7, 512] = 12.0
+    C.csa_quantize_kv(x.cuda(), rows)
+    rows.fp8[3::7] = torch.where(torch.rand((n, 512), generator=rng(5)).cuda() < 0.5, 0x80, 0).to(torch.uint8)[3::7]
+    rows.scale[3::7] = 1.0
+    q = torch.zeros((B, 1, H, 576), dtype=BF16, device="cuda")
+    q[..., 512] = 1.0
+    q[..., :512] = torch.randn((H, 512), generator=rng(6)).cuda() * 2.0 ** -6
+    o = C.latent_attn_decode(q, rows, torch.full((B,), n - 1, dtype=I64, device="cuda"), 1.0, n, off=torch.zeros((B,), dtype=I64, device="cuda"))
+    l, r = (t.cuda() for t in L.dequant(rows.fp8, rows.rope, rows.scale))
+    qd, key = q[0, 0].to(L.F64), torch.cat([l, r], 1)
+    p = (qd @ key.T).softmax(1)
+    # as above
+    fp32 = 2 * (576 + 8) * 2.0 ** -24 * (qd.abs() @ key.abs().T).amax(1) + (n + 8) * 2.0 ** -24 + 2.0 ** -20
+    tol = 2.0 ** -8 * (p @ l).abs() + (2.0 ** -8 + fp32)[:, None] * (p @ l.abs()) + 2.0 ** -8 * (p @ l.abs().amax(1))[:, None]
+    assert ((o[:, 0].to(L.F64) - p @ l).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("H", [16, 64])
+@pytest.mark.parametrize("code", [0x7e, 0x01, 0x81])
+def test_decode_rows_of_one_code(C, H, code):
+    """A scale of 1 and one code, in any channel, the largest or the smallest there is: a row with a value.  With w = 2^x the
+    one weight, the output is (w rounded) code / w: w lies in 4 .. 8, is off by at most 2^-8 of itself and divided by
+    itself as it was, so the output by that and its own half step, 2^-8; the other channels are 0."""
+    rows = C.KvRows.empty(512, 576, 64, "cuda")
+    rows.fp8.zero_(), rows.rope.zero_(), rows.scale.fill_(1.0)
+    rows.fp8.fill_diagonal_(code)
+    q = torch.randn((512, 1, H, 576), generator=rng(1)).to(BF16).cuda()
+    o = C.latent_attn_decode(q, rows, torch.zeros((512,), dtype=I64, device="cuda"), 0.05, 1, off=torch.arange(512, device="cuda"))
+    want = torch.zeros((512, 512), dtype=torch.float64)
+    want.fill_diagonal_(float(torch.tensor([code], dtype=torch.uint8).view(torch.float8_e4m3fn).double()))
+    assert ((o[:, 0].cpu().double() - want[:, None]).abs() <= 2.02 * 2.0 ** -8 * want[:, None].abs()).all() and C.csa_device_error() == 0
+
+
+# ------------------------------------------------------------------------------------------
+# calls
+# ------------------------------------------------------------------------------------------
+
 def test_decode_contiguous_rows_and_pages_agree(C):
     """The same rows as one run and in pages of a tile: the same tiles, the same bits."""
     n = 128 * 300
