@@ -30,8 +30,11 @@ __device__ __forceinline__ void tile_step(const float *q, const float *kt, int l
     float z = 0.f;
     for (int d = 0; d < dk; ++d) z = fmaf(q[d], kt[lane * ldk + d], z);
     z = seen ? z * scale_log2 : -INFINITY;
-    const float m_new = fmaxf(m, warp_max(z));
-    if (m_new == -INFINITY) return; // nothing seen so far
+    float m_new = fmaxf(m, warp_max(z)); // (of what is a number)
+    if (m_new == -INFINITY) {
+        if (!__any_sync(0xffffffffu, z != z)) return; // nothing seen so far
+        m_new = 0.f; // a score that is none: its p, and with it the row, is NaN
+    }
     const float f = exp2f(m - m_new), p = seen ? exp2f(z - m_new) : 0.f;
     m = m_new;
     l = fmaf(l, f, warp_sum(p));

@@ -456,7 +456,8 @@ int latent_gather(const csa_kv_rows *rows, const int64_t *cu, const int64_t *sta
  *   o[b,j,h,:] = sum_s e^z lat(s) / sum_s e^z,   lse[b,j,h] = ln sum_s e^z
  * and o = 0, lse = -inf for a token that sees nothing (pos[b] + j < 0: padding).  Rows that no token of
  * the call sees are not part of the result whatever they hold; a non-finite value in a row that one
- * of a sequence's tokens sees may reach all of the sequence's tokens.
+ * of a sequence's tokens sees may reach all of the sequence's tokens.  A query with a NaN or an infinity
+ * that sees a key makes o and lse of its own row NaN.
  *   q [B, Lq, H, c] bf16;  o [B, Lq, H, R] bf16;  lse [B, Lq, H] fp32 or NULL;  pos [B] int64
  *   max_len  host-side bound of the positions (sizes the split)
  *   ws       workspace of latent_attn_decode_workspace_size(...) bytes, queried with the device
@@ -489,7 +490,8 @@ int latent_attn_decode(const void *q, const csa_kv_rows *rows, const int64_t *po
  *   CSA_BF16); lse [Tq, H] fp32 or NULL.  max_q bounds the query counts (sizes the grid; queries past
  *   it are not computed).  Rows of q outside the sequences get no output: o and lse keep what
  *   they held.  Rows of kv and k_rope outside a sequence are not part of its result whatever they
- *   hold; a non-finite value in a sequence's own rows may reach all of its outputs.
+ *   hold; a non-finite value in a sequence's own rows may reach all of its outputs, one in a query its own
+ *   row (o and lse are NaN where a score is).
  *   ws       workspace of latent_attn_prefill_workspace_size(...) bytes, queried with the device current (0
  *            where none is of use), or NULL: with it, a few queries' many keys are split over the SMs and the
  *            parts merged, without it they are not.  Calls that may overlap need one each

@@ -154,6 +154,52 @@ def test_decode_rows_of_one_code(C, H, code):
 
 
 # ------------------------------------------------------------------------------------------
+# numbers that are not finite, or beyond fp32 on the way
+# ------------------------------------------------------------------------------------------
+
+BAD = [float("nan"), float("inf"), -float("inf")]
+
+
+@pytest.mark.parametrize("R,rd,H", [(512, 64, 8), (512, 64, 40), (256, 64, 8), (96, 16, 3)])
+@pytest.mark.parametrize("bad", BAD)
+@pytest.mark.parametrize("n", [1, 40, 3000])
+def test_decode_of_a_query_that_is_not_finite(C, R, rd, H, bad, n):
+    """It makes NaN of its own row, as the formula does, and not the zeros of a row that sees nothing."""
+    rows = C.KvRows.empty(n, R + rd, rd, "cuda")
+    x = torch.randn((n, R + rd), generator=rng(1))
+    x[0, 3] = 1.0 if bad > 0 else -1.0  # (one key alone: a score of +inf, whose softmax is inf / inf)
+    C.csa_quantize_kv(x.cuda(), rows)
+    q = torch.randn((2, 1, H, R + rd), generator=rng(2)).to(BF16).cuda()
+    pos, off = ints(n - 1, n - 1), ints(0, 0)
+    lse = torch.empty((2, 1, H), device="cuda")
+    good = C.latent_attn_decode(q, rows, pos, 0.05, n, off=off)
+    q[1, 0, H // 2, 3] = bad
+    o = C.latent_attn_decode(q, rows, pos, 0.05, n, off=off, lse=lse)
+    hit = torch.zeros((2, 1, H), dtype=torch.bool, device="cuda")
+    hit[1, 0, H // 2] = True
+    assert torch.equal(o[~hit], good[~hit]) and torch.isfinite(lse[~hit]).all()
+    assert o[hit].isnan().all() and lse[hit].isnan().all()
+
+
+@pytest.mark.parametrize("dims,dtype", [((128, 64, 128), BF16), ((128, 64, 128), F32), ((64, 32, 96), BF16)])
+@pytest.mark.parametrize("bad", BAD)
+@pytest.mark.parametrize("n", [1, 40, 300])
+def test_prefill_of_a_query_that_is_not_finite(C, dims, dtype, bad, n):
+    dn, dr, dv = dims
+    q, kv, kr = (torch.randn(s, generator=rng(i)).to(dtype).cuda() for i, s in enumerate(((n, 2, dn + dr), (n, 2, dn + dv), (n, dr))))
+    kv[0, :, 3] = 1.0 if bad > 0 else -1.0
+    cu = ints(0, n)
+    lse = torch.empty((n, 2), device="cuda")
+    good = C.latent_attn_prefill(q, kv, kr, cu, cu, n, 0.1)
+    q[n // 2, 1, 3] = bad
+    o = C.latent_attn_prefill(q, kv, kr, cu, cu, n, 0.1, lse=lse)
+    hit = torch.zeros((n, 2), dtype=torch.bool, device="cuda")
+    hit[n // 2, 1] = True
+    assert torch.equal(o[~hit], good[~hit]) and torch.isfinite(lse[~hit]).all()
+    assert o[hit].isnan().all() and lse[hit].isnan().all()
+
+
+# ------------------------------------------------------------------------------------------
 # calls
 # ------------------------------------------------------------------------------------------
 
