@@ -196,18 +196,51 @@ template <typename Tin, int NV, int kBatch> __global__ void __launch_bounds__(25
         for (int r = 0; r < kBatch; ++r)
 #pragma unroll
             for (int k = 0; k < NV; ++k) raw[r][k].get(v[r][k]);
-        float s[kBatch];
-        if (a.g) {
+        auto row_amax = [&](float (&m)[kBatch]) { // this lane's share
 #pragma unroll
             for (int r = 0; r < kBatch; ++r) {
-                float2 ss = make_float2(0.f, 0.f);
+                m[r] = 0.f;
 #pragma unroll
                 for (int k = 0; k < NV; ++k)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) ss = fma2(v[r][k][e], v[r][k][e], ss);
-                s[r] = ss.x + ss.y;
+                    for (int e = 0; e < 4; ++e) m[r] = fmaxf(m[r], fmaxf(fabsf(v[r][k][e].x), fabsf(v[r][k][e].y)));
             }
-            const float f = 1.f / sqrtf(reduce(s, lane, [](float x, float y) { return x + y; }) / (float)R + a.eps);
+        };
+        float s[kBatch];
+        if (a.g) {
+            auto mean_square = [&]() { // of this lane's row
+#pragma unroll
+                for (int r = 0; r < kBatch; ++r) {
+                    float2 ss = make_float2(0.f, 0.f);
+#pragma unroll
+                    for (int k = 0; k < NV; ++k)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) ss = fma2(v[r][k][e], v[r][k][e], ss);
+                    s[r] = ss.x + ss.y;
+                }
+                return reduce(s, lane, [](float x, float y) { return x + y; }) / (float)R;
+            };
+            float ms = mean_square() + a.eps;
+            // squares that overflow, or fall among the subnormals where eps does not cover them: the row is brought near 1
+            // by a power of two first, and eps by its square, which leaves the quotient as it is
+            const bool far = !(ms < 1e38f && ms > 8.0779357e-28f); // 2^-90
+            if (__any_sync(0xffffffffu, far)) {
+                row_amax(s);
+                const float am = reduce(s, lane, [](float x, float y) { return fmaxf(x, y); });
+                const int ea = (int)(__float_as_uint(am) >> 23) - 127, ee = (int)(__float_as_uint(a.eps) >> 23) - 127;
+                const int up = far ? max(-126, min(-ea, (100 - ee) / 2)) : 0;
+                const float f = exp2i(up);
+#pragma unroll
+                for (int r = 0; r < kBatch; ++r) {
+                    const float fr = of_row<kBatch>(f, r);
+#pragma unroll
+                    for (int k = 0; k < NV; ++k)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) v[r][k][e] = mul2(v[r][k][e], make_float2(fr, fr));
+                }
+                ms = mean_square() + a.eps * f * f;
+            }
+            const float f = 1.f / sqrtf(ms);
 #pragma unroll
             for (int r = 0; r < kBatch; ++r) s[r] = of_row<kBatch>(f, r);
 #pragma unroll
@@ -222,14 +255,7 @@ template <typename Tin, int NV, int kBatch> __global__ void __launch_bounds__(25
                     for (int e = 0; e < 4; ++e) v[r][k][e] = mul2(mul2(v[r][k][e], make_float2(s[r], s[r])), g[e]);
             }
         }
-#pragma unroll
-        for (int r = 0; r < kBatch; ++r) {
-            s[r] = 0.f;
-#pragma unroll
-            for (int k = 0; k < NV; ++k)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[r] = fmaxf(s[r], fmaxf(fabsf(v[r][k][e].x), fabsf(v[r][k][e].y)));
-        }
+        row_amax(s);
         float my_sc = __fdiv_rn(reduce(s, lane, [](float x, float y) { return fmaxf(x, y); }), 448.f);
         if (!(my_sc > 0.f)) my_sc = 1.f;
         const float my_inv = 1.f / my_sc;

@@ -417,7 +417,8 @@ int csa_decode_glue(const void *o, const void *P, const void *Rm, int64_t R, int
  *
  * latent_append -- write the rows x [n, c] (in_dtype) into the cache: row i belongs to position
  * pos[i] of sequence seq[i] (seq NULL: of sequence i, n <= B).  pos[i] < 0 skips the row; seq[i]
- * outside [0, B) is refused.  Per row, in fp32:
+ * outside [0, B) is refused.  Per row, in fp32 (a finite u whose squares leave fp32's range is scaled by a
+ * power of two on the way):
  *   u = x[0:R];  u = u / sqrt(mean(u^2) + eps) * g                       when g != NULL (g [R] fp32)
  *   v = x[R:c];  the pairs (2k, 2k+1) of v rotated counter-clockwise by   when base != 0
  *       pos[i] * base^(-2k/rd)                                            (angles to 2^-25 of a turn at 2^31)

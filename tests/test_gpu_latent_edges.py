@@ -199,6 +199,29 @@ def test_prefill_of_a_query_that_is_not_finite(C, dims, dtype, bad, n):
     assert o[hit].isnan().all() and lse[hit].isnan().all()
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("R", [512, 1024, 32])
+@pytest.mark.parametrize("eps", [1e-6, 0.0, 2.0 ** -120])
+@pytest.mark.parametrize("n", [1, 2600])
+def test_append_norms_beyond_fp32(C, dtype, R, eps, n):
+    """Rows whose squares overflow fp32, or underflow where eps does not cover it, between ordinary ones: their norm is
+    that of the formula.  Off by at most 32 half steps of fp32, as any row's; a code by half a step of E4M3."""
+    sizes = torch.tensor([1.0, 1e17, 1e20, 3e37, 1e-3, 1e-20, 1e-30, 1e-36])[torch.arange(n) * 5 % 8 if n > 1 else torch.tensor([3])]
+    x = (torch.randn((n, R + 64), generator=rng(R)) * sizes[:, None]).to(dtype)
+    gain = 1 + 0.2 * torch.randn((R,), generator=rng(1))
+    out = C.KvRows.empty(n, R + 64, 64, "cuda")
+    C.latent_append(x.cuda(), torch.zeros((n,), dtype=I64, device="cuda"), out, g=gain.cuda(), eps=eps, off=torch.arange(n, device="cuda"))
+    assert C.csa_device_error() == 0
+    lat, _ = L.append_rows(x, torch.zeros((n,), dtype=I64), R, gain, float(torch.tensor(eps, dtype=F32)))
+    got, _ = L.dequant(out.fp8, out.rope, out.scale)
+    e = 32 * 2.0 ** -24
+    want = lat.abs().amax(1) / 448
+    sc = out.scale.cpu().to(L.F64)
+    assert ((sc - want).abs() <= 2 * e * want + 2.0 ** -149).all()
+    tol = lat.abs() * (2.0 ** -4 + 4 * e) + sc[:, None] * 2.0 ** -10 + 448 * 2.0 ** -149
+    assert ((got - lat).abs() <= tol).all()
+
+
 # ------------------------------------------------------------------------------------------
 # calls
 # ------------------------------------------------------------------------------------------
