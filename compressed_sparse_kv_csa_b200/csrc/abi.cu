@@ -628,6 +628,7 @@ int latent_attn_decode(const void *q, const csa_kv_rows *rows, const int64_t *po
     a.lse = lse;
     a.part = reinterpret_cast<float *>((reinterpret_cast<uintptr_t>(ws) + kAlign - 1) / kAlign * kAlign);
     a.err = dev_error_word();
+    a.wait_ns = g_wait_ns.load();
     if (latent_decode_tc_eligible(R, rd)) {
         latent_decode_tc_workspace(B, Lq, H, max_len, &a.grid, &a.par);
         note_path(CSA_PATH_LATENT_DECODE_TC);
@@ -664,13 +665,14 @@ int latent_attn_prefill(const void *q, const void *kv, const void *k_rope, const
     const LatentPrefillArgs a{q, kv, k_rope, cu_q, cu_k, B, Tq, Tk, max_q, H, dn, dr, dv, scale, causal ? 1 : 0, o, lse,
                               dev_error_word()};
     if (latent_prefill_tc_eligible(a, dtype)) {
-        LatentKeyParts parts{nullptr, 0, 1};
+        LatentKeyParts parts{nullptr, 0, 1, 0};
         if (ws) {
             const size_t need = latent_prefill_tc_workspace(a);
             if (need && ws_bytes < need + kAlign) return CSA_ERR_WORKSPACE;
             parts = latent_prefill_tc_parts(a);
             parts.part = reinterpret_cast<float *>((reinterpret_cast<uintptr_t>(ws) + kAlign - 1) / kAlign * kAlign);
         }
+        parts.wait_ns = g_wait_ns.load();
         note_path(CSA_PATH_LATENT_PREFILL_TC);
         return status_of(launch_latent_prefill_tc(a, parts, S(stream)));
     }

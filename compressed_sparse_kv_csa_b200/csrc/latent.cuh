@@ -82,6 +82,7 @@ struct LatentDecodeArgs {
     int grid;    // CTAs of the split
     int par;     // CTAs side by side on the same keys, one for each row block; 1: a CTA's runs may be of any row block
     int *err;
+    uint64_t wait_ns; // limit of the waits of the warps that copy (one in the other roles too cost up to 10%)
 };
 
 // Positions token j of a sequence sees (0 .. result - 1).
@@ -272,6 +273,7 @@ struct LatentKeyParts {
     float *part; // their partials (latent_part of 256 rows), block after block
     int whole;   // blocks of queries whose keys are not split
     int n;       // parts of each of the others; 1: there are none
+    uint64_t wait_ns; // as above (here, since two words more in the arguments above slowed the kernel by 7%)
 };
 
 // The rows of sequence b in a packed array of T rows.

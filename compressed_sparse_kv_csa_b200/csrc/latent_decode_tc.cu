@@ -264,6 +264,7 @@ using Walk = LatentWalk<Split>;
 struct Ctx {
     uint32_t base, tmem;
     __device__ __forceinline__ uint32_t bar(int b) const { return base + OFF_BAR + 8u * (uint32_t)b; }
+    __device__ __forceinline__ bool wait(int b, uint32_t parity) const { return mbar_wait(bar(b), parity); }
     __device__ __forceinline__ uint32_t stage(uint32_t n) const { return base + OFF_K + (n % kStages) * kStage; }
 };
 
@@ -377,7 +378,7 @@ static __device__ __forceinline__ bool tma_role(const LatentDecodeArgs &a, const
                 }
                 if (refused) flag_error(a.err, CSA_DEVERR_INDEX);
             }
-            if (n >= kStages && !__all_sync(0xffffffffu, mbar_wait(c.bar(B_KEMPTY + n % kStages), ((n / kStages) & 1) ^ 1))) {
+            if (n >= kStages && !__all_sync(0xffffffffu, mbar_wait(c.bar(B_KEMPTY + n % kStages), ((n / kStages) & 1) ^ 1, a.wait_ns))) {
                 ok = false;
                 break;
             }
@@ -432,7 +433,8 @@ static __device__ __forceinline__ bool tma_role(const LatentDecodeArgs &a, const
                 if (elect_one()) mbar_arrive_expect_tx(c.bar(B_TAIL), bytes);
 #pragma unroll
                 for (int k = 0; k < kKT / 32; ++k) sts1(sc + 4u * (uint32_t)(32 * k + lane), tail_scale[k]);
-                if (!__all_sync(0xffffffffu, mbar_wait(c.bar(B_TAIL), tails & 1))) {
+                if (!__all_sync(0xffffffffu, mbar_wait(c.bar(B_TAIL), tails & 1, a.wait_ns))) {
+                    mbar_wait(c.bar(B_TAIL), tails & 1);
                     ok = false;
                     break;
                 }
@@ -456,6 +458,8 @@ static __device__ __forceinline__ bool tma_role(const LatentDecodeArgs &a, const
         }
     }
     if (lane == 0) *issued = 0xffffffffu;
+    // nothing is on its way when the block ends, whatever the others waited for
+    for (uint32_t k = n - min(n, (uint32_t)kStages); k < n; ++k) ok = mbar_wait(c.bar(B_KFULL + k % kStages), (k / kStages) & 1) && ok;
     return ok;
 }
 
@@ -523,7 +527,7 @@ static __device__ __forceinline__ bool copy_role(const LatentDecodeArgs &a, cons
                 cur[h] = mine[h];
                 if (t + 1 < run.t1) mine[h] = resolve(t + 1, h);
             }
-            if (n >= kStages && !__all_sync(0xffffffffu, mbar_wait(c.bar(B_KEMPTY + n % kStages), ((n / kStages) & 1) ^ 1))) {
+            if (n >= kStages && !__all_sync(0xffffffffu, mbar_wait(c.bar(B_KEMPTY + n % kStages), ((n / kStages) & 1) ^ 1, a.wait_ns))) {
                 ok = false;
                 break;
             }
@@ -565,7 +569,7 @@ static __device__ __forceinline__ bool mma_role(const LatentDecodeArgs &a, const
     const Desc q_desc(sdesc_sw128(c.base + OFF_Q, 16, 1024)), k_desc(sdesc_sw128(c.base + OFF_K, 16, M.group)), r_desc(sdesc_sw128(c.base + OFF_K, 16, 1024));
     const Desc p_desc(sdesc_sw128(c.base + OFF_P, 16, 1024)), v_desc(sdesc_sw128(c.base + OFF_K, M.slice, M.group));
     auto output = [&](uint32_t k, bool first, int steps) { // O (+)= v code of tile k
-        if (!mbar_wait(c.bar(B_P + (k & 1)), (k >> 1) & 1)) return false;
+        if (!c.wait(B_P + (k & 1), (k >> 1) & 1)) return false;
         tc_fence_after();
         const Desc dp = p_desc.at(kPTile * (k % kPBufs)), dv = v_desc.at((k % kStages) * kStage);
 #pragma unroll
@@ -587,7 +591,7 @@ static __device__ __forceinline__ bool mma_role(const LatentDecodeArgs &a, const
             if (first) {
                 if (pending && !output(n - 1, pending_first, pending_steps)) return false;
                 pending = false;
-                if (!mbar_wait(c.bar(B_Q), runs & 1)) return false;
+                if (!c.wait(B_Q, runs & 1)) return false;
                 ++runs;
             }
             const uint32_t full = c.bar(B_KFULL + n % kStages), full_ph = (n / kStages) & 1;
@@ -753,7 +757,7 @@ static __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, c
         const int rr = run.rb * kRB + row, n_rows = a.Lq * a.H;
         const bool valid = rr < n_rows;
         // the run's last O, and the row's sum over the eight warps
-        if (!__all_sync(0xffffffffu, mbar_wait(c.bar(B_KEMPTY + n % kStages), (n / kStages) & 1))) return false;
+        if (!__all_sync(0xffffffffu, c.wait(B_KEMPTY + n % kStages, (n / kStages) & 1))) return false;
         tc_fence_after();
         if (!rows.sync() || !put(0, row_sum(l))) return false;
         get(0, other);
@@ -842,7 +846,7 @@ static __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, c
         bool begun = seen <= run.t0 * kKT;  // the row has a reference, or needs none here
         for (int64_t t = run.t0; t < run.t1; ++t, ++n) {
             const uint32_t buf = n & 1;
-            if (!__all_sync(0xffffffffu, mbar_wait(c.bar(B_KFULL + n % kStages), (n / kStages) & 1))) return false;
+            if (!__all_sync(0xffffffffu, c.wait(B_KFULL + n % kStages, (n / kStages) & 1))) return false;
             float2 z[8], s[8], v[8];
             bool odd = false; // some key may not be seen by some row
             const uint32_t sc = c.base + OFF_SC + (n % kStages) * kKT * 4 + (kStacked ? 128u : 64u) * (uint32_t)kq;
@@ -855,7 +859,7 @@ static __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, c
                     s[e] = part ? sk[8 + e] : sk[e];
                     odd |= fabsf(s[e].x) == 1.f || fabsf(s[e].y) == 1.f;
                 }
-                if (!__all_sync(0xffffffffu, mbar_wait(c.bar(B_S + buf), (n >> 1) & 1))) return false;
+                if (!__all_sync(0xffffffffu, c.wait(B_S + buf, (n >> 1) & 1))) return false;
                 tc_fence_after();
                 tmem_ld32_pairs(tw + kColSn + 64u * buf + 32u * (uint32_t)sub, sn);
                 tmem_ld32_pairs(tw + kColSr + kSrCols * buf + 32u * (uint32_t)sub, sr);
@@ -874,7 +878,7 @@ static __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, c
                 for (int e = 0; e < 4; ++e) lds4(sc + 16u * e, s[2 * e], s[2 * e + 1]);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) odd |= fabsf(s[e].x) == 1.f || fabsf(s[e].y) == 1.f;
-                if (!__all_sync(0xffffffffu, mbar_wait(c.bar(B_S + buf), (n >> 1) & 1))) return false;
+                if (!__all_sync(0xffffffffu, c.wait(B_S + buf, (n >> 1) & 1))) return false;
                 tc_fence_after();
                 // this warp has hi or lo of all 64 keys, and gives the warp with the other part what that one has to finish
                 tmem_ld16_pairs(tw + kColSn + 64u * buf + 32u * (uint32_t)(half ^ 1) + 16u * (uint32_t)sub, give);
@@ -996,7 +1000,7 @@ static __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, c
                     spent *= f;
                 }
                 if (t > run.t0 && __any_sync(0xffffffffu, f != 1.f)) { // O of the tiles before this one
-                    if (!__all_sync(0xffffffffu, mbar_wait(c.bar(B_KEMPTY + (n - 1) % kStages), ((n - 1) / kStages) & 1))) return false;
+                    if (!__all_sync(0xffffffffu, c.wait(B_KEMPTY + (n - 1) % kStages, ((n - 1) / kStages) & 1))) return false;
                     tc_fence_after();
 #pragma unroll 1
                     for (int k = 0; k < 4; ++k) {
@@ -1016,7 +1020,7 @@ static __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, c
             vs += vt;
             const uint32_t at = c.base + OFF_P + kPTile * (n % kPBufs);
             if constexpr (!kStacked) { // one buffer: O of the tile before has read it
-                if (n > 0 && !__all_sync(0xffffffffu, mbar_wait(c.bar(B_KEMPTY + (n - 1) % kStages), ((n - 1) / kStages) & 1))) return false;
+                if (n > 0 && !__all_sync(0xffffffffu, c.wait(B_KEMPTY + (n - 1) % kStages, ((n - 1) / kStages) & 1))) return false;
             }
             if constexpr (kStacked) {
                 sts4(at + sw128((uint32_t)(32 * g + r16), (uint32_t)key), hi);

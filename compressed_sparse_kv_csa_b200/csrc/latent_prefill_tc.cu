@@ -158,10 +158,17 @@ struct Ring { // slot and phase of the next 16 KB box
 };
 
 // TMA (one warp).  The ring's order is K0 V0 K1 V1 ...
-__device__ __forceinline__ bool tma_role(const Job &j, const Maps &M, uint32_t base, int lane)
+__device__ __forceinline__ bool tma_role(const Job &j, const Maps &M, uint32_t base, int lane, uint64_t wait_ns)
 {
     const uint32_t bars = base + OFF_BAR;
     auto bar = [&](int b) { return bars + 8u * (uint32_t)b; };
+    // nothing is on its way when the block ends, whatever the others waited for: Q, and the last boxes of the `boxes`
+    // that went into the ring
+    auto drain = [&](uint32_t boxes) {
+        bool ok = mbar_wait(bar(B_Q), 0);
+        for (uint32_t p = boxes - min(boxes, (uint32_t)kSlots); p < boxes; ++p) ok = mbar_wait(bar(B_FULL + p % kSlots), (p / kSlots) & 1) && ok;
+        return ok;
+    };
     if (lane == 0) {
         const int nt = j.i0 + kT < j.nq ? 2 : 1;
         mbar_arrive_expect_tx(bar(B_Q), (uint32_t)nt * 3 * kSlot);
@@ -177,7 +184,10 @@ __device__ __forceinline__ bool tma_role(const Job &j, const Maps &M, uint32_t b
         int v_slot[2];
         for (int s = 0; s < 5; ++s) {
             const int slot = r.slot;
-            if (lap && !mbar_wait(bar(B_EMPTY + slot), r.phase ^ 1)) return false;
+            if (lap && !__all_sync(0xffffffffu, mbar_wait(bar(B_EMPTY + slot), r.phase ^ 1, wait_ns))) {
+                drain(5u * (uint32_t)i + (uint32_t)min(s, 3)); // (the values' boxes go when both their slots are empty)
+                return false;
+            }
             const uint32_t dst = base + OFF_RING + (uint32_t)slot * kSlot;
             if (s < 3) {
                 if (lane == 0) {
@@ -210,7 +220,11 @@ __device__ __forceinline__ bool tma_role(const Job &j, const Maps &M, uint32_t b
                 tma_load_3d(vhi, &M.kv, kDn + 64, j.h, y, bar(B_VTAIL));
             }
             __syncwarp();
-            if (!__all_sync(0xffffffffu, mbar_wait(bar(B_VTAIL), 0))) return false;
+            if (!__all_sync(0xffffffffu, mbar_wait(bar(B_VTAIL), 0, wait_ns))) {
+                mbar_wait(bar(B_VTAIL), 0);
+                drain(5u * (uint32_t)i + 3u);
+                return false;
+            }
             for (int e = 8 * tail + lane; e < 8 * kT; e += 32)
                 for (int s = 0; s < 2; ++s)
                     asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"((s ? vhi : vlo) + 16u * (uint32_t)e), "r"(0) : "memory");
@@ -223,7 +237,7 @@ __device__ __forceinline__ bool tma_role(const Job &j, const Maps &M, uint32_t b
         }
         __syncwarp();
     }
-    return true;
+    return drain(5u * (uint32_t)j.tiles);
 }
 
 // MMA issue (one thread).
@@ -463,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_tc_kernel(LatentPr
         ok = softmax_role<KEYS>(a, parts, j, base, tmem, warp, lane);
     } else {
         regs_dec<kRegsRest>();
-        if (warp == kTmaWarp) ok = tma_role(j, maps, base, lane);
+        if (warp == kTmaWarp) ok = tma_role(j, maps, base, lane, parts.wait_ns);
         else if (warp == kMmaWarp && elect_one()) ok = mma_role(j, base, tmem);
     }
     if (!ok) flag_error(a.err, CSA_DEVERR_TIMEOUT);
@@ -561,7 +575,7 @@ LatentKeyParts latent_prefill_tc_parts(const LatentPrefillArgs &a)
 {
     constexpr double kTile = 1.9, kCta = 10, kMerge = 6, kPartial = 0.06; // us
     const int64_t blocks = query_blocks(a), sms = device_sms(), nk = a.Tk / a.B, nq = a.Tq / a.B;
-    const LatentKeyParts none{nullptr, 0, 1};
+    const LatentKeyParts none{nullptr, 0, 1, 0};
     const int64_t whole = blocks / sms * sms, rest = blocks - whole;
     if (blocks >= ((int64_t)1 << 31) || rest == 0 || (whole > 0 && 2 * nq > nk) || whole > 8 * sms) return none;
     const double tiles = (double)(nk > nq ? nk - nq / 2 : nk) / kT;

@@ -536,14 +536,15 @@ int latent_attn_prefill(const void *q, const void *kv, const void *k_rope, const
 int32_t csa_last_path(void);
 
 /*
- * csa_set_wait_limit_ns -- how long the bounded waits of hybrid_attn_decode's tensor-core kernel
- * may wait before they give up (record CSA_DEVERR_TIMEOUT and wind the CTA down), in ns, for the
- * calls launched after it (process-wide); 0 restores the default of 2 s.  Returns the previous
- * limit.  A limit of 1 ns turns every such wait into one non-blocking test that gives up unless
- * its phase has already completed.  The pages have no counterpart: this exists so that a test can
- * make the waits run out on purpose and check that the kernel winds down cleanly (it copies
- * nothing asynchronously into shared memory, and its final drain of its own MMAs always allows
- * the full 2 s) and that the next call is correct.
+ * csa_set_wait_limit_ns -- how long the bounded waits of hybrid_attn_decode's tensor-core kernel, and of the
+ * warps that copy keys in those of latent_attn_decode and latent_attn_prefill, may wait before they
+ * give up (record CSA_DEVERR_TIMEOUT and wind the CTA down), in ns, for the calls launched after it
+ * (process-wide); 0 restores the default of 2 s, which every other wait keeps.  Returns the previous
+ * limit.  A limit of 1 ns turns every such wait into one non-blocking test that gives up unless its
+ * phase has already completed.  The pages have no counterpart: this exists so that a test can make
+ * the waits run out on purpose and check that the kernels wind down cleanly (before a CTA ends, its
+ * own MMAs and its copies into shared memory are waited for, with the full 2 s) and that the next
+ * call is correct.
  */
 uint64_t csa_set_wait_limit_ns(uint64_t ns);
 

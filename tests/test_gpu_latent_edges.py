@@ -238,3 +238,44 @@ def test_decode_contiguous_rows_and_pages_agree(C):
         b = C.latent_attn_decode(q, rows, pos, 0.07, 12800, pages=torch.arange(300, dtype=I32, device="cuda").view(3, 100), page_rows=128)
         assert torch.equal(a, b)
     assert C.csa_device_error() == 0
+
+
+# ------------------------------------------------------------------------------------------
+# waits that run out
+# ------------------------------------------------------------------------------------------
+
+def runs_out(C, call, path):
+    """With a limit of 1 ns every wait that has it is one test that gives up: the kernel reports it and winds down, its own
+    copies and MMAs waited for (the warps without it take 2 s to give up).  Nothing faults or hangs, and the next calls
+    are as before."""
+    want = call()
+    assert C.csa_last_path() == path and C.csa_device_error() == 0
+    prev = C.csa_set_wait_limit_ns(1)
+    try:
+        call()
+        torch.cuda.synchronize()
+        err = C.csa_device_error()
+    finally:
+        assert C.csa_set_wait_limit_ns(prev) == 1
+    assert err & C.CSA_DEVERR_TIMEOUT
+    for _ in range(2):
+        assert torch.equal(call(), want)
+    assert C.csa_device_error() == 0
+
+
+@pytest.mark.parametrize("H,page", [(16, 128), (64, 32), (16, 1), (64, 0)])
+def test_decode_waits_run_out(C, H, page):
+    n, B = 1000, 160  # more tiles a CTA than stages, and one that is partly seen
+    rows = C.KvRows.empty(1024, 576, 64, "cuda")
+    C.csa_quantize_kv(torch.randn((1024, 576), generator=rng(1)).cuda(), rows)
+    q = torch.randn((B, 1, H, 576), generator=rng(2)).to(BF16).cuda()
+    pos = torch.full((B,), n - 1, dtype=I64, device="cuda")
+    kw = dict(pages=torch.arange(1024 // page, dtype=I32, device="cuda").repeat(B, 1), page_rows=page) if page else dict(off=torch.zeros_like(pos))
+    runs_out(C, lambda: C.latent_attn_decode(q, rows, pos, 0.05, n, **kw), C.CSA_PATH_LATENT_DECODE_TC)
+
+
+@pytest.mark.parametrize("nq,nk,H", [(700, 700, 2), (1, 5, 1), (300, 4100, 2)])
+def test_prefill_waits_run_out(C, nq, nk, H):
+    q, kv, kr = (torch.randn(s, generator=rng(i)).to(BF16).cuda() for i, s in enumerate(((nq, H, 192), (nk, H, 256), (nk, 64))))
+    cq, ck = ints(0, nq), ints(0, nk)
+    runs_out(C, lambda: C.latent_attn_prefill(q, kv, kr, cq, ck, nq, 0.1), C.CSA_PATH_LATENT_PREFILL_TC)
