@@ -1151,7 +1151,7 @@ template <int RB> static cudaError_t launch(const LatentDecodeArgs &a, cudaStrea
         if (a.map.pages) {
             maps.n_pages = (uint32_t)(n / pr);
             if (maps.box == kKT) maps.page_tiles = (uint32_t)(pr / kKT);
-            while ((1 << maps.shift) < pr) ++maps.shift;
+            else maps.shift = pr == 8 ? 3 : pr == 16 ? 4 : pr == 32 ? 5 : 6;
             maps.slice = 1024;
             maps.group = 4096;
             const cuuint64_t dims[4] = {128, 8, kR / 128, n / 8}, strides[3] = {kR, 128, 8 * kR};

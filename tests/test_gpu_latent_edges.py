@@ -279,3 +279,23 @@ def test_prefill_waits_run_out(C, nq, nk, H):
     q, kv, kr = (torch.randn(s, generator=rng(i)).to(BF16).cuda() for i, s in enumerate(((nq, H, 192), (nk, H, 256), (nk, 64))))
     cq, ck = ints(0, nq), ints(0, nk)
     runs_out(C, lambda: C.latent_attn_prefill(q, kv, kr, cq, ck, nq, 0.1), C.CSA_PATH_LATENT_PREFILL_TC)
+
+
+@pytest.mark.parametrize("page_rows", [2 ** 31 - 128, 2 ** 31 - 1, 2 ** 30 + 128])
+def test_one_page_larger_than_any_cache(C, page_rows):
+    """A page size that no cache reaches: all of a sequence's rows are in its first page."""
+    n = 1024
+    rows, flat = (C.KvRows.empty(n, 576, 64, "cuda") for _ in range(2))
+    x = torch.randn((n, 576), generator=rng(1)).cuda()
+    pos, seq = torch.arange(n, device="cuda"), torch.zeros((n,), dtype=I32, device="cuda")
+    pages = torch.zeros((1, 1), dtype=I32, device="cuda")
+    C.latent_append(x, pos, rows, seq=seq, pages=pages, page_rows=page_rows)
+    C.latent_append(x, pos, flat, seq=seq, off=ints(0))
+    assert torch.equal(rows.fp8, flat.fp8) and torch.equal(rows.scale, flat.scale)
+    for H in (16, 64):
+        q = torch.randn((1, 1, H, 576), generator=rng(2)).to(BF16).cuda()
+        a = C.latent_attn_decode(q, rows, ints(n - 1), 0.07, n, pages=pages, page_rows=page_rows)
+        assert torch.equal(a, C.latent_attn_decode(q, rows, ints(n - 1), 0.07, n, off=ints(0)))
+    a, b = C.latent_gather(rows, ints(0, n), n=n, pages=pages, page_rows=page_rows), C.latent_gather(rows, ints(0, n), n=n, off=ints(0))
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    assert C.csa_device_error() == 0
