@@ -368,10 +368,17 @@ cudaError_t launch_latent_merge_tc(const LatentDecodeArgs &a, int rows, cudaStre
     return rows == 32 ? launch_merge<TcSplit32, 32>(a, st) : launch_merge<TcSplit64, 64>(a, st);
 }
 
+// The kernels' limits of shared memory are those of the largest shapes, set once: a limit set for each call would be taken
+// from it by a call of another host thread.
+constexpr int kMaxC = 640, kMaxDk = 256, kMaxDv = 256;
+static constexpr size_t decode_smem(int c) { return (size_t)(kKT * (c + 1) + kRB * c) * sizeof(float); }
+static constexpr size_t prefill_smem(int dk, int dv) { return (size_t)(kKT * (dk + 1) + kKT * dv + kRB * dk) * sizeof(float); }
+
 cudaError_t launch_latent_decode_generic(LatentDecodeArgs a, cudaStream_t st)
 {
-    const size_t smem = (size_t)(kKT * (a.rows.c + 1) + kRB * a.rows.c) * sizeof(float);
-    cudaError_t e = cudaFuncSetAttribute(latent_decode_generic_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static std::atomic<bool> done[64];
+    const size_t smem = decode_smem(a.rows.c);
+    cudaError_t e = prepare_kernel(latent_decode_generic_kernel, decode_smem(kMaxC), 0, done);
     if (e != cudaSuccess) return e;
     latent_decode_generic_kernel<<<(unsigned)a.grid, 32 * kWarps, smem, st>>>(a);
     e = cudaGetLastError();
@@ -381,9 +388,9 @@ cudaError_t launch_latent_decode_generic(LatentDecodeArgs a, cudaStream_t st)
 
 template <typename T> static cudaError_t prefill_generic(const LatentPrefillArgs &a, cudaStream_t st)
 {
-    const int dk = a.dn + a.dr;
-    const size_t smem = (size_t)(kKT * (dk + 1) + kKT * a.dv + kRB * dk) * sizeof(float);
-    cudaError_t e = cudaFuncSetAttribute(latent_prefill_generic_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static std::atomic<bool> done[64];
+    const size_t smem = prefill_smem(a.dn + a.dr, a.dv);
+    cudaError_t e = prepare_kernel(latent_prefill_generic_kernel<T>, prefill_smem(kMaxDk, kMaxDv), 0, done);
     if (e != cudaSuccess) return e;
     const int64_t blocks = a.B * ((a.max_q + kRB - 1) / kRB);
     latent_prefill_generic_kernel<T><<<dim3((unsigned)blocks, (unsigned)a.H), 32 * kWarps, smem, st>>>(a);

@@ -1,5 +1,7 @@
 """Latent attention where its arithmetic is at its edges: keys that outweigh all others, rows without codes, queries that
 are not finite, norms beyond fp32, empty calls, calls from two threads, and waits that run out."""
+import threading
+
 import pytest
 import torch
 
@@ -299,3 +301,32 @@ def test_one_page_larger_than_any_cache(C, page_rows):
     a, b = C.latent_gather(rows, ints(0, n), n=n, pages=pages, page_rows=page_rows), C.latent_gather(rows, ints(0, n), n=n, off=ints(0))
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
     assert C.csa_device_error() == 0
+
+
+def test_two_threads_with_different_channel_counts(C):
+    """Calls of two host threads on streams of their own do not take each other's shared memory limit."""
+    cases, failed = [], []
+    for R, rd in ((512, 128), (32, 16)):
+        rows = C.KvRows.empty(64, R + rd, rd, "cuda")
+        C.csa_quantize_kv(torch.randn((64, R + rd), generator=rng(R)).cuda(), rows)
+        q = torch.randn((1, 1, 4, R + rd), generator=rng(1)).to(BF16).cuda()
+        d = 32 if R == 512 else 256
+        p = [torch.randn(s, generator=rng(i)).cuda() for i, s in enumerate(((8, 1, d), (8, 1, d - 16 + d), (8, 16)))]
+        cases.append((rows, q, ints(63), ints(0), p, ints(0, 8)))
+
+    def work(rows, q, pos, off, p, cu):
+        try:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                want = C.latent_attn_decode(q, rows, pos, 0.1, 64, off=off), C.latent_attn_prefill(*p, cu, cu, 8, 0.1)
+                for _ in range(400):
+                    got = C.latent_attn_decode(q, rows, pos, 0.1, 64, off=off), C.latent_attn_prefill(*p, cu, cu, 8, 0.1)
+                s.synchronize()
+                assert all(torch.equal(a, b) for a, b in zip(got, want))
+        except Exception as e:
+            failed.append(e)
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=c) for c in cases]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    assert not failed, failed[0]
