@@ -553,6 +553,7 @@ RowMap row_map(const int32_t *pages, int32_t max_pages, int32_t page_rows, const
 }
 
 constexpr int64_t kMaxLen = (int64_t)1 << 30;
+constexpr int64_t kMaxGather = 32 * (((int64_t)1 << 31) - 1); // 32 rows a CTA
 
 bool latent_decode_shape_ok(int64_t B, int32_t Lq, int32_t H, int32_t R, int32_t rd, int64_t max_len)
 {
@@ -573,7 +574,7 @@ int latent_append(const void *x, int32_t in_dtype, int64_t n, const float *g, fl
     if (!seq && n > B) return CSA_ERR_INVALID_ARG;
     if (g && (!aligned16(g) || !(eps >= 0.f) || !std::isfinite(eps))) return CSA_ERR_INVALID_ARG;
     if (base != 0.0 && !(base > 1.0 && std::isfinite(base))) return CSA_ERR_INVALID_ARG;
-    if (out->c - out->rope_dims > 1024 || out->rope_dims > 256) return CSA_ERR_UNSUPPORTED;
+    if (out->c - out->rope_dims > 1024 || out->rope_dims > 256 || n > ((int64_t)1 << 38)) return CSA_ERR_UNSUPPORTED;
     if (n == 0) return CSA_OK;
     const LatentAppendArgs a{x, n, B, g, eps, base, pos, seq, row_map(pages, max_pages, page_rows, off, out->n),
                              to_dev(*out), dev_error_word()};
@@ -587,7 +588,7 @@ int latent_gather(const csa_kv_rows *rows, const int64_t *cu, const int64_t *sta
     if (!cu || B < 0 || n_out < 0 || (!lat && !rope) || !dtype_ok(out_dtype)) return CSA_ERR_INVALID_ARG;
     if (!latent_rows_ok(rows) || !row_map_ok(pages, max_pages, page_rows, off)) return CSA_ERR_INVALID_ARG;
     if ((lat && !aligned16(lat)) || (rope && !aligned16(rope))) return CSA_ERR_INVALID_ARG;
-    if (rows->c - rows->rope_dims > 1024 || rows->rope_dims > 256 || n_out > ((int64_t)1 << 36)) return CSA_ERR_UNSUPPORTED;
+    if (rows->c - rows->rope_dims > 1024 || rows->rope_dims > 256 || n_out > kMaxGather) return CSA_ERR_UNSUPPORTED;
     if (n_out == 0 || B == 0) return CSA_OK;
     const LatentGatherArgs a{to_dev(*rows), cu, start, B, n_out, row_map(pages, max_pages, page_rows, off, rows->n),
                              lat, rope, dev_error_word()};

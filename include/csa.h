@@ -428,7 +428,7 @@ int csa_decode_glue(const void *o, const void *P, const void *Rm, int64_t R, int
  * Errors: CSA_ERR_INVALID_ARG for a null x, pos or out, n < 0, B < 0, a bad dtype, x or g not 16-byte
  * aligned, seq NULL with n > B, no pages and no off, pages with max_pages or page_rows < 1, a g with
  * a negative or non-finite eps, a base that is neither 0 nor a finite number > 1, or rows that are
- * not as above; CSA_ERR_UNSUPPORTED for R > 1024 or rd > 256.
+ * not as above; CSA_ERR_UNSUPPORTED for R > 1024, rd > 256 or n > 2^38.
  */
 int latent_append(const void *x, int32_t in_dtype, int64_t n, const float *g, float eps, double base, const int64_t *pos,
                   const int32_t *seq, int64_t B, const int32_t *pages, int32_t max_pages, int32_t page_rows,
@@ -443,7 +443,7 @@ int latent_append(const void *x, int32_t in_dtype, int64_t n, const float *g, fl
  * up-projection is the kv of latent_attn_prefill, rope its k_rope.
  * Errors: CSA_ERR_INVALID_ARG for null or misaligned (16 bytes) arrays, no output, B or n_out < 0, a
  * bad dtype, a bad page table as above, or rows that are not as above; CSA_ERR_UNSUPPORTED for
- * R > 1024, rd > 256 or n_out > 2^36.
+ * R > 1024, rd > 256 or n_out > 32 (2^31 - 1).
  */
 int latent_gather(const csa_kv_rows *rows, const int64_t *cu, const int64_t *start, int64_t B, const int32_t *pages,
                   int32_t max_pages, int32_t page_rows, const int64_t *off, int64_t n_out, void *lat, void *rope,
