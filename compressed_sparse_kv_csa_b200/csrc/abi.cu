@@ -542,9 +542,10 @@ bool latent_rows_ok(const csa_kv_rows *rows)
     return rows && rows->n >= 0 && rows->rope_dims > 0 && rows->rope_dims < rows->c && kv_rows_ok(rows, 0, rows->c);
 }
 
-bool row_map_ok(const int32_t *pages, int32_t max_pages, int32_t page_rows, const int64_t *off)
+// Of calls with nothing to do (none) the arrays may be empty, and have no address.
+bool row_map_ok(const int32_t *pages, int32_t max_pages, int32_t page_rows, const int64_t *off, bool none)
 {
-    return pages ? max_pages >= 1 && page_rows >= 1 : off != nullptr;
+    return pages ? max_pages >= 1 && page_rows >= 1 : none || off != nullptr;
 }
 
 RowMap row_map(const int32_t *pages, int32_t max_pages, int32_t page_rows, const int64_t *off, int64_t n)
@@ -569,8 +570,8 @@ int latent_append(const void *x, int32_t in_dtype, int64_t n, const float *g, fl
                   const int32_t *seq, int64_t B, const int32_t *pages, int32_t max_pages, int32_t page_rows,
                   const int64_t *off, const csa_kv_rows *out, void *stream)
 {
-    if (!x || !pos || n < 0 || B < 0 || !dtype_ok(in_dtype) || !aligned16(x)) return CSA_ERR_INVALID_ARG;
-    if (!latent_rows_ok(out) || !row_map_ok(pages, max_pages, page_rows, off)) return CSA_ERR_INVALID_ARG;
+    if (n < 0 || B < 0 || (n > 0 && (!x || !pos)) || !dtype_ok(in_dtype) || !aligned16(x)) return CSA_ERR_INVALID_ARG;
+    if (!latent_rows_ok(out) || !row_map_ok(pages, max_pages, page_rows, off, n == 0)) return CSA_ERR_INVALID_ARG;
     if (!seq && n > B) return CSA_ERR_INVALID_ARG;
     if (g && (!aligned16(g) || !(eps >= 0.f) || !std::isfinite(eps))) return CSA_ERR_INVALID_ARG;
     if (base != 0.0 && !(base > 1.0 && std::isfinite(base))) return CSA_ERR_INVALID_ARG;
@@ -585,8 +586,8 @@ int latent_gather(const csa_kv_rows *rows, const int64_t *cu, const int64_t *sta
                   int32_t max_pages, int32_t page_rows, const int64_t *off, int64_t n_out, void *lat, void *rope,
                   int32_t out_dtype, void *stream)
 {
-    if (!cu || B < 0 || n_out < 0 || (!lat && !rope) || !dtype_ok(out_dtype)) return CSA_ERR_INVALID_ARG;
-    if (!latent_rows_ok(rows) || !row_map_ok(pages, max_pages, page_rows, off)) return CSA_ERR_INVALID_ARG;
+    if (!cu || B < 0 || n_out < 0 || (n_out > 0 && !lat && !rope) || !dtype_ok(out_dtype)) return CSA_ERR_INVALID_ARG;
+    if (!latent_rows_ok(rows) || !row_map_ok(pages, max_pages, page_rows, off, B == 0 || n_out == 0)) return CSA_ERR_INVALID_ARG;
     if ((lat && !aligned16(lat)) || (rope && !aligned16(rope))) return CSA_ERR_INVALID_ARG;
     if (rows->c - rows->rope_dims > 1024 || rows->rope_dims > 256 || n_out > kMaxGather) return CSA_ERR_UNSUPPORTED;
     if (n_out == 0 || B == 0) return CSA_OK;
@@ -608,8 +609,8 @@ int latent_attn_decode(const void *q, const csa_kv_rows *rows, const int64_t *po
                        int32_t page_rows, const int64_t *off, float scale, int64_t B, int32_t Lq, int32_t H,
                        int64_t max_len, void *o, float *lse, void *ws, size_t ws_bytes, void *stream)
 {
-    if (!q || !pos || !o || B < 0 || Lq < 1 || H < 1 || max_len < 0 || !std::isfinite(scale)) return CSA_ERR_INVALID_ARG;
-    if (!latent_rows_ok(rows) || !row_map_ok(pages, max_pages, page_rows, off)) return CSA_ERR_INVALID_ARG;
+    if ((B > 0 && (!q || !pos || !o)) || B < 0 || Lq < 1 || H < 1 || max_len < 0 || !std::isfinite(scale)) return CSA_ERR_INVALID_ARG;
+    if (!latent_rows_ok(rows) || !row_map_ok(pages, max_pages, page_rows, off, B == 0)) return CSA_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(o)) return CSA_ERR_INVALID_ARG;
     const int32_t rd = rows->rope_dims, R = rows->c - rd;
     if (!latent_decode_shape_ok(B, Lq, H, R, rd, max_len)) return CSA_ERR_UNSUPPORTED;
@@ -655,7 +656,7 @@ int latent_attn_prefill(const void *q, const void *kv, const void *k_rope, const
                         int64_t Tq, int64_t Tk, int32_t H, int32_t dn, int32_t dr, int32_t dv, int64_t max_q, float scale,
                         int32_t causal, int32_t dtype, void *o, float *lse, void *ws, size_t ws_bytes, void *stream)
 {
-    if (!q || !cu_q || !cu_k || !o || B < 0 || Tq < 0 || Tk < 0 || max_q < 0 || !dtype_ok(dtype)) return CSA_ERR_INVALID_ARG;
+    if ((Tq > 0 && (!q || !o)) || !cu_q || !cu_k || B < 0 || Tq < 0 || Tk < 0 || max_q < 0 || !dtype_ok(dtype)) return CSA_ERR_INVALID_ARG;
     if (Tk > 0 && (!kv || !k_rope)) return CSA_ERR_INVALID_ARG;
     if (H < 1 || dn < 1 || dr < 1 || dv < 1 || !std::isfinite(scale)) return CSA_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(kv) || !aligned16(k_rope) || !aligned16(o)) return CSA_ERR_INVALID_ARG;

@@ -425,6 +425,7 @@ int csa_decode_glue(const void *o, const void *P, const void *Rm, int64_t R, int
  *   s = amax(|u|) / 448 (1 when that is not positive), fp8 = e4m3(u / s), rope = bf16(v)
  * as csa_quantize_kv quantises.  The (sequence, position) pairs of one call have to be distinct: of
  * rows written to the same place at once, an unspecified mixture remains.
+ * n = 0 is no error, and needs neither x, pos, seq, pages nor off.
  * Errors: CSA_ERR_INVALID_ARG for a null x, pos or out, n < 0, B < 0, a bad dtype, x or g not 16-byte
  * aligned, seq NULL with n > B, no pages and no off, pages with max_pages or page_rows < 1, a g with
  * a negative or non-finite eps, a base that is neither 0 nor a finite number > 1, or rows that are
@@ -441,6 +442,7 @@ int latent_append(const void *x, int32_t in_dtype, int64_t n, const float *g, fl
  * part, in out_dtype; either may be NULL.  Output rows below cu[0], from cu[B] on, or past n_out are
  * left as they were; a refused row comes out as zeros.  For the expanded form: lat times the
  * up-projection is the kv of latent_attn_prefill, rope its k_rope.
+ * n_out = 0 or B = 0 is no error; no outputs, pages or off are needed then.
  * Errors: CSA_ERR_INVALID_ARG for null or misaligned (16 bytes) arrays, no output, B or n_out < 0, a
  * bad dtype, a bad page table as above, or rows that are not as above; CSA_ERR_UNSUPPORTED for
  * R > 1024, rd > 256 or n_out > 32 (2^31 - 1).
@@ -470,6 +472,7 @@ int latent_gather(const csa_kv_rows *rows, const int64_t *cu, const int64_t *sta
  * A sequence's tokens are summed in an order that depends on the batch's lengths, max_len and the
  * device's SM count, not on timing: the same call gives the same bits.
  * Limits: R a multiple of 32 and <= 512, rd <= 128, H <= 128, Lq <= 64, max_len <= 2^30, B <= 2^18.
+ * B = 0 is no error, and needs none of the arrays but rows.
  * Errors: CSA_ERR_INVALID_ARG for a null q, rows, pos or o, B < 0, Lq or H < 1, max_len < 0, a
  * non-finite scale, q or o not 16-byte aligned, a bad page table or rows as above;
  * CSA_ERR_UNSUPPORTED outside the limits; CSA_ERR_WORKSPACE when ws is NULL or too small.
@@ -499,8 +502,8 @@ int latent_attn_decode(const void *q, const csa_kv_rows *rows, const int64_t *po
  * The order of a row's sums depends on the sizes and the device's SM count, not on timing.
  * Limits: dn, dr, dv multiples of 16, dn + dr <= 256, dv <= 256, H <= 128, Tq and Tk < 2^31,
  * B * H * ceil(max_q / 32) < 2^31.
- * Errors: CSA_ERR_WORKSPACE for a ws that is too small; CSA_ERR_INVALID_ARG for a null q, cu_q, cu_k or o, a null kv or k_rope with Tk > 0, negative
- * sizes, H, dn, dr or dv < 1, a bad dtype, a non-finite scale, or q, kv, k_rope or o not 16-byte aligned;
+ * Errors: CSA_ERR_WORKSPACE for a ws that is too small; CSA_ERR_INVALID_ARG for a null cu_q or cu_k, a null q or o with Tq > 0, a
+ * null kv or k_rope with Tk > 0, negative sizes, H, dn, dr or dv < 1, a bad dtype, a non-finite scale, or q, kv, k_rope or o not 16-byte aligned;
  * CSA_ERR_UNSUPPORTED outside the limits.
  */
 size_t latent_attn_prefill_workspace_size(int64_t B, int64_t Tq, int64_t Tk, int32_t H, int32_t dn, int32_t dr, int32_t dv,

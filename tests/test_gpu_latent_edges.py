@@ -330,3 +330,35 @@ def test_two_threads_with_different_channel_counts(C):
     [t.start() for t in threads]
     [t.join() for t in threads]
     assert not failed, failed[0]
+
+
+# ------------------------------------------------------------------------------------------
+# calls
+# ------------------------------------------------------------------------------------------
+
+def test_empty_calls(C):
+    """No rows, no sequences, no queries: nothing to do, and nothing wrong."""
+    rows = C.KvRows.empty(32, 576, 64, "cuda")
+    pages, none = torch.zeros((0, 2), dtype=I32, device="cuda"), torch.zeros((0,), dtype=I64, device="cuda")
+    one = torch.zeros((1, 2), dtype=I32, device="cuda")
+    x = torch.zeros((0, 576), device="cuda")
+    C.latent_append(x, none, rows, g=torch.ones((512,), device="cuda"), base=10000.0, pages=one, page_rows=16)
+    C.latent_append(x, none, rows, seq=torch.zeros((0,), dtype=I32, device="cuda"), off=none)
+    C.latent_append(x, none, rows, pages=pages, page_rows=16)
+    lat, rope = C.latent_gather(rows, ints(0), n=0, pages=pages, page_rows=16)
+    assert lat.shape == (0, 512) and rope.shape == (0, 64)
+    lat, _ = C.latent_gather(rows, ints(0, 0), n=0, off=ints(0))
+    assert lat.shape == (0, 512)
+    lat = torch.full((3, 512), 7.0, device="cuda")
+    C.latent_gather(rows, ints(0), off=none, lat=lat)
+    assert (lat == 7).all()
+    o = C.latent_attn_decode(torch.zeros((0, 1, 16, 576), dtype=BF16, device="cuda"), rows, none, 1.0, 64, pages=pages, page_rows=16)
+    assert o.shape == (0, 1, 16, 512)
+    for dt in (BF16, F32):
+        e = lambda *s: torch.zeros(s, dtype=dt, device="cuda")
+        assert C.latent_attn_prefill(e(0, 4, 192), e(0, 4, 256), e(0, 64), ints(0), ints(0), 0, 1.0).shape == (0, 4, 128)
+        assert C.latent_attn_prefill(e(0, 4, 192), e(9, 4, 256), e(9, 64), ints(0, 0), ints(0, 9), 0, 1.0).shape == (0, 4, 128)
+        o, lse = torch.full((3, 4, 128), 7.0, dtype=dt, device="cuda"), torch.full((3, 4), 7.0, device="cuda")
+        C.latent_attn_prefill(e(3, 4, 192), e(0, 4, 256), e(0, 64), ints(0, 3), ints(0, 0), 3, 1.0, o=o, lse=lse)
+        assert (o == 0).all() and (lse == -torch.inf).all()  # queries without keys
+    assert C.csa_device_error() == 0
