@@ -41,7 +41,7 @@ constexpr int kRegs = 168, kRegsSoft = 208, kRegsRest = 88;
 static_assert(256 * kRegsSoft + 128 * kRegsRest <= kThreads * kRegs, "register split");
 constexpr uint32_t kSlot = 16384;
 constexpr int kSlots = 8;
-constexpr int kParts = 2; // P is handed over in parts, so that P V begins while the rest is computed
+constexpr int kParts = 2; // P is handed over in halves, so that P V begins while the rest is computed
 constexpr uint32_t OFF_Q = 0, OFF_RING = 2 * 3 * kSlot, OFF_BAR = OFF_RING + kSlots * kSlot, OFF_TMEM = OFF_BAR + 256;
 constexpr uint32_t SMEM_ALLOC = OFF_TMEM + 64 + 1024; // slack to align the base to 1024 bytes
 static_assert(SMEM_ALLOC <= 232448, "shared memory per block");
@@ -97,13 +97,6 @@ __device__ __forceinline__ bool find_job(const LatentPrefillArgs &a, int64_t id,
     return j.i0 < j.nq;
 }
 
-__device__ __forceinline__ float ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 __device__ __forceinline__ uint32_t pk_bf16(float lo, float hi)
 {
     __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
@@ -115,37 +108,6 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     float y;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
     return y;
-}
-
-__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[32]) { tmem_st32(taddr, r); }
-__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[16])
-{
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr), "r"(r[0]),
-                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
-                 "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-                 : "memory");
-}
-
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
-{
-    float2 d;
-    asm("{\n\t.reg .b64 x, y, z;\n\t"
-        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
-        "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return d;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b)
-{
-    float2 d;
-    asm("{\n\t.reg .b64 x, y;\n\t"
-        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
-        "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return d;
 }
 
 struct Ring { // slot and phase of the next 16 KB box
@@ -387,7 +349,7 @@ template <Keys KEYS> __device__ __forceinline__ bool softmax_role(const LatentPr
                 sum[e & 1] = add2(sum[e & 1], z);
                 p[e] = pk_bf16(z.x, z.y);
             }
-            tmem_st(tS + (uint32_t)(64 / kParts) * g, p);
+            tmem_st32(tS + (uint32_t)(64 / kParts) * g, p);
             tmem_st_wait();
             tc_fence_before();
             mbar_arrive(bar(B_P + kParts * t + g));

@@ -7,31 +7,15 @@
 // lane beside its neighbour's.  Measured, 512 + 64 channels in pages of 128: append of 65,536 bf16 rows 34 us
 // (3.5 TB/s; the arithmetic of a row bounds it), gather of 190,000 rows 60 us (5.7 TB/s).
 #include "latent.cuh"
+#include "tc_common.cuh"
 
 namespace csa {
 
 namespace {
 
-constexpr double kTwoPi = 6.283185307179586476925287;
+using namespace tc;
 
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
-{
-    float2 d;
-    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
-        "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return d;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) // (the products are not fused into what follows)
-{
-    float2 d;
-    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
-        "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return d;
-}
+constexpr double kTwoPi = 6.283185307179586476925287;
 
 // 8 channels as they are stored.
 template <typename T> struct Raw8;

@@ -362,3 +362,30 @@ def test_empty_calls(C):
         C.latent_attn_prefill(e(3, 4, 192), e(0, 4, 256), e(0, 64), ints(0, 3), ints(0, 0), 3, 1.0, o=o, lse=lse)
         assert (o == 0).all() and (lse == -torch.inf).all()  # queries without keys
     assert C.csa_device_error() == 0
+
+
+def test_decode_of_many_sequences(C):
+    """More sequences than SMs and warps, of 0 to 300 keys: each as by itself."""
+    B, H = 2000, 16
+    rows = C.KvRows.empty(4096, 576, 64, "cuda")
+    C.csa_quantize_kv(torch.randn((4096, 576), generator=rng(1)).cuda(), rows)
+    q = torch.randn((B, 1, H, 576), generator=rng(2)).to(BF16).cuda()
+    lens = torch.randint(0, 301, (B,), generator=rng(3)).cuda()
+    off = torch.randint(0, 3700, (B,), generator=rng(4)).cuda()
+    lse = torch.empty((B, 1, H), device="cuda")
+    o = C.latent_attn_decode(q, rows, lens - 1, 0.07, 300, off=off, lse=lse)
+    assert C.csa_device_error() == 0
+    l, r = (t.cuda() for t in L.dequant(rows.fp8, rows.rope, rows.scale))
+    at = off[:, None] + torch.arange(300, device="cuda")
+    key, v = torch.cat([l, r], 1)[at], l[at]
+    z = torch.einsum("bhc,bsc->bhs", q[:, 0].to(L.F64), key) * 0.07
+    z = z.masked_fill((torch.arange(300, device="cuda") >= lens[:, None])[:, None], -torch.inf)
+    some = lens > 0
+    p = z[some].softmax(2)
+    ref, size = p @ v[some], p @ v[some].abs()
+    dz = (576 + 8) * 2.0 ** -24 * 0.07 * torch.einsum("bhc,bsc->bhs", q[:, 0].to(L.F64).abs(), key.abs()).amax(2)[some]
+    tol = 2.0 ** -8 * ref.abs() + (2.0 ** -8 + 2 * dz + 308 * 2.0 ** -24 + 2.0 ** -20)[..., None] * size + 2.0 ** -8 * (p @ v[some].abs().amax(2, keepdim=True))
+    assert ((o[some, 0].to(L.F64) - ref).abs() <= tol).all()
+    assert (o[~some] == 0).all() and (lse[~some] == -torch.inf).all()
+    ref = z[some].logsumexp(2)
+    assert ((lse[some, 0].to(L.F64) - ref).abs() <= dz + 308 * 2.0 ** -24 + 2.0 ** -19 + 2.0 ** -22 * ref.abs()).all()
