@@ -697,20 +697,27 @@ static __device__ __forceinline__ bool softmax_role(const LatentDecodeArgs &a, c
         if constexpr (kStacked) v += other_part(v);
         return v;
     };
-    // Bit e: key e of this thread's has no value -- a scale of 1 and no code but +0 and -0.  The warp looks at the quarter's
-    // scales, a lane each, and together at the codes of the rows that may be such.
+    // Bit e: key e of this thread's has no value -- a scale of 1 and no code but +0 and -0.  Of the quarter's keys a lane looks
+    // at one's scale and 16 of its codes, and the warp at all codes of those that may be such.
     auto no_value = [&](uint32_t st, uint32_t sc) {
         constexpr uint32_t kKeys = kKT / 4;
+        auto row = [&](uint32_t i) {
+            const uint32_t j = kKeys * (uint32_t)kq + i;
+            return st + (j >> 3) * M.group + (j & 7u) * 128u;
+        };
+        auto any_code = [](uint32_t at) {
+            uint32_t c[4];
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3]) : "r"(at) : "memory");
+            return ((c[0] | c[1] | c[2] | c[3]) & 0x7f7f7f7fu) != 0;
+        };
+        const uint32_t mine = (uint32_t)lane % kKeys;
         float x;
-        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(sc + 4u * ((uint32_t)lane % kKeys)) : "memory");
-        uint32_t none = __ballot_sync(0xffffffffu, x == 1.f);
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(sc + 4u * mine) : "memory");
+        uint32_t none = __ballot_sync(0xffffffffu, x == 1.f && (uint32_t)lane < kKeys && !any_code(row(mine) + 16u * (mine & 7u)));
 #pragma unroll 1
         for (uint32_t left = none; left; left &= left - 1) {
-            const uint32_t i = (uint32_t)__ffs(left) - 1, j = kKeys * (uint32_t)kq + i % kKeys, e = (uint32_t)lane;
-            uint32_t c[4];
-            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3])
-                         : "r"(st + (e >> 3) * M.slice + (j >> 3) * M.group + (j & 7u) * 128u + 16u * (e & 7u)) : "memory");
-            if (__any_sync(0xffffffffu, ((c[0] | c[1] | c[2] | c[3]) & 0x7f7f7f7fu) != 0)) none &= ~(left & (0u - left));
+            const uint32_t i = (uint32_t)__ffs(left) - 1, e = (uint32_t)lane;
+            if (__any_sync(0xffffffffu, any_code(row(i) + (e >> 3) * M.slice + 16u * (e & 7u)))) none &= ~(1u << i);
         }
         return none >> (16 * part);
     };
