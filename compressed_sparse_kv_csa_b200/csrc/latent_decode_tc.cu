@@ -39,8 +39,8 @@
 // Roles: warps 0-7 softmax and output; warp 8 copies the keys by TMA, in boxes of a page or of a tile, and warp 9
 // brings the tiles after into L2 (with pages that no box fits, both copy by cp.async); warp 10 MMA.  Rows that are
 // not to be seen are zeros in shared memory, or not read: the probability 0 times whatever they held would not be 0.
-// Measured: 64 sequences of 1k to 16k keys x 16 heads 63 us (3.7 TB/s), 32 of them x 128 heads x 2 tokens 175 us,
-// 4 x 1M keys x 64 heads 0.65 ms (4.1 TB/s).
+// Measured: 64 sequences of 1k to 16k keys x 16 heads 66 us (3.6 TB/s), 32 of 3k to 12k x 128 heads x 2 tokens 178 us (of
+// contiguous rows 158), 4 x 1M keys x 64 heads 0.65 to 0.68 ms in a short run (4 TB/s), 0.78 in a loop of seconds.
 #include "latent.cuh"
 #include "tc_common.cuh"
 #include "tma_host.cuh"

@@ -22,7 +22,8 @@
 // Roles: warps 0-3 and 4-7 softmax, rescale and output of the two query tiles (one row a thread), warp 8
 // TMA, warp 9 MMA.  Per pair of query tiles and tile of keys the tensor cores need 2,560 cycles and the chain S - softmax - P V
 // of each, beside the other's MMAs, 3,800; in long calls the chip's power limits what is left (990 W, 1.5 GHz): 16k
-// x 16 heads causal 1.03 ms in a short run (1.33 PFLOP/s), 1.12 ms in a loop of seconds; 4k 70 us.
+// x 16 heads causal 0.99 to 1.05 ms in a short run (1.3 PFLOP/s), 1.13 to 1.16 ms in a loop of seconds; 4k 72 us.
+// The threads that issue copies and MMAs index a tile's slot numbers at run time, which lie in a stack of 64 to 72 bytes.
 #include "latent.cuh"
 #include "tc_common.cuh"
 #include "tma_host.cuh"
@@ -531,8 +532,8 @@ static int64_t query_blocks(const LatentPrefillArgs &a) { return a.B * a.H * ((a
 // round by themselves: full rounds are then followed by none that is split.
 //   256 queries of 16 heads (16 blocks) after 64k keys: 150 us in 9 parts, 914 whole; after 2k: 20 in 4, 36 whole;
 //   80 blocks after 8k: 116 in 3, 126 whole; 100 blocks: 129 whole, 141 in 4;
-//   2,560 queries of 16 heads after 8k (148 blocks whole, 12 in 12): 147 us, 191 whole;
-//   3 x 1,024 after 4k (148 whole, 44 in 3): 105, 118 whole; 2 x 2,048 after 14k: 487 whole, 505 with 108 blocks in 4.
+//   2,560 queries of 16 heads, the last of 8k keys (148 blocks whole, 12 in 12): 147 us, 191 whole;
+//   3 x 1,024, the last of 4k (148 whole, 44 in 3): 105, 118 whole; 2 x 2,048 after 14k: 487 whole, 505 with 108 blocks in 4.
 LatentKeyParts latent_prefill_tc_parts(const LatentPrefillArgs &a)
 {
     constexpr double kTile = 1.9, kCta = 10, kMerge = 6, kPartial = 0.06; // us

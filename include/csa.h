@@ -465,10 +465,12 @@ int latent_gather(const csa_kv_rows *rows, const int64_t *cu, const int64_t *sta
  *   max_len  host-side bound of the positions (sizes the split)
  *   ws       workspace of latent_attn_decode_workspace_size(...) bytes, queried with the device
  *            current; calls that may overlap (two streams, two captured graphs) need one each
- * Statistics and sums are fp32.  With 512 + 64 channels the products p * scale that meet the FP8 codes are
- * held in two 8-bit terms: an output is off by at most 2^-8 of the weighted mean of |lat| and 2^-8 of
- * the weighted mean of 448 * scale over the rows that have a code other than zero (for rows as
- * latent_append writes them, of their largest |lat|), beside its own rounding.
+ * Statistics and sums are fp32.  With 512 + 64 channels what meets the FP8 codes is held in two 8-bit
+ * terms.  A row's latent queries are exact down to 2^-10 of the largest of them, and off by at most
+ * 2^-18 of it below.  The products p * scale are rounded such that an output is off by at most 2^-8 of
+ * the weighted mean of |lat| and 2^-8 of the weighted mean of 448 * scale, beside its own rounding.
+ * For rows as latent_append writes them 448 * scale is their largest |lat|; a row of zero codes
+ * with a scale of 1 counts as 0.  Scales are positive.
  * A sequence's tokens are summed in an order that depends on the batch's lengths, max_len and the
  * device's SM count, not on timing: the same call gives the same bits.
  * Limits: R a multiple of 32 and <= 512, rd <= 128, H <= 128, Lq <= 64, max_len <= 2^30, B <= 2^18.
