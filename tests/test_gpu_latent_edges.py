@@ -155,6 +155,31 @@ def test_decode_rows_of_one_code(C, H, code):
     assert ((o[:, 0].cpu().double() - want[:, None]).abs() <= 2.02 * 2.0 ** -8 * want[:, None].abs()).all() and C.csa_device_error() == 0
 
 
+@pytest.mark.parametrize("H", [16, 64])
+@pytest.mark.parametrize("size", [2.0 ** 4, 2.0 ** 8, 2.0 ** 12])
+def test_decode_queries_with_an_outlier(C, H, size):
+    """One channel of the queries far above the others, where the keys have nothing: the others count to 2^-18 of it
+    (include/csa.h), which a score's error adds up over a key's channels."""
+    n = 3000
+    x = torch.randn((n, 576), generator=rng(1))
+    x[:, 5] = 0
+    rows = C.KvRows.empty(n, 576, 64, "cuda")
+    C.csa_quantize_kv(x.cuda(), rows)
+    q = torch.randn((1, 1, H, 576), generator=rng(2))
+    q[..., 5] = size
+    q = q.to(BF16).cuda()
+    lse = torch.empty((1, 1, H), device="cuda")
+    o = C.latent_attn_decode(q, rows, ints(n - 1), 0.05, n, off=ints(0), lse=lse)
+    l, r = (t.cuda() for t in L.dequant(rows.fp8, rows.rope, rows.scale))
+    key, qd = torch.cat([l, r], 1), q[0, 0].to(L.F64)
+    z = qd @ key.T * 0.05
+    p = z.softmax(1)
+    dz = 0.05 * ((576 + 8) * 2.0 ** -24 * (qd.abs() @ key.abs().T).amax(1) + 2.0 ** -18 * size * l.abs().sum(1).max())
+    tol = 2.0 ** -8 * (p @ l).abs() + (2 * dz + 2.0 ** -8 + (n + 8) * 2.0 ** -24 + 2.0 ** -20)[:, None] * (p @ l.abs()) + 2.0 ** -8 * (p @ l.abs().amax(1))[:, None]
+    assert ((o[0, 0].to(L.F64) - p @ l).abs() <= tol).all() and C.csa_device_error() == 0
+    assert ((lse[0, 0].to(L.F64) - z.logsumexp(1)).abs() <= dz + (n + 8) * 2.0 ** -24 + 2.0 ** -19).all()
+
+
 # ------------------------------------------------------------------------------------------
 # numbers that are not finite, or beyond fp32 on the way
 # ------------------------------------------------------------------------------------------
